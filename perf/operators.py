@@ -298,7 +298,7 @@ def _plain_scan(s, train):
     y = st.to(t["x"].dtype)
     if not train:
         return {"y": y, "ht": ht}
-    dy = s["dy"].float()
+    dy = s["dy"].to(torch.float32, copy=True)
     dy[last] += s["dht"][full]
     nxt = torch.zeros_like(a)
     nxt[:-1] = a[1:]
