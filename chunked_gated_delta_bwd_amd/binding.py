@@ -28,7 +28,9 @@ STAGE_NAMES = {GDR_STAGE_PREP: "prep", GDR_STAGE_CHAIN_FWD: "chain_fwd", GDR_STA
                GDR_STAGE_CHAIN_BOTH: "chain_both", GDR_STAGE_GRADS: "grads", GDR_STAGE_FINISH: "finish"}
 
 SYMBOLS = ("gdr_workspace_bytes", "gdr_fwd_recompute", "gdr_fwd", "gdr_bwd", "gdr_fwd_bwd",
-           "gdr_workspace_region", "gdr_run_stage", "gdr_fwd_bwd_noalloc", "gdr_last_error")
+           "gdr_workspace_region", "gdr_run_stage", "gdr_fwd_bwd_noalloc", "gdr_step",
+           "gdr_scan_workspace_bytes", "gdr_scan_fwd", "gdr_scan_bwd", "gdr_scan_step",
+           "gdr_norm_fwd", "gdr_norm_quant", "gdr_norm_workspace_bytes", "gdr_norm_bwd", "gdr_last_error")
 # the device array gdr_fwd_bwd_noalloc uses as its workspace (128 MiB per GPU)
 NOALLOC_WORKSPACE_BYTES = 128 << 20
 
@@ -59,6 +61,28 @@ class Grads(ctypes.Structure):
                 ("dA_log", ctypes.c_void_p), ("ddt_bias", ctypes.c_void_p)]
 
 
+class ScanShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("H", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("N", ctypes.c_int32), ("cu_seqlens_host", ctypes.POINTER(ctypes.c_int64)),
+                ("gate", ctypes.c_int32), ("dtype", ctypes.c_int32), ("gate_scale", ctypes.c_float),
+                ("convex", ctypes.c_int32)]
+
+
+class ScanInputs(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("g", ctypes.c_void_p), ("A_log", ctypes.c_void_p),
+                ("dt_bias", ctypes.c_void_p), ("h0", ctypes.c_void_p)]
+
+
+class ScanGrads(ctypes.Structure):
+    _fields_ = [("dx", ctypes.c_void_p), ("dg", ctypes.c_void_p), ("dh0", ctypes.c_void_p),
+                ("dA_log", ctypes.c_void_p), ("ddt_bias", ctypes.c_void_p)]
+
+
+class NormShape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("width", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("group", ctypes.c_int32)]
+
+
 def library_path() -> str:
     return _LIB_PATH
 
@@ -86,6 +110,16 @@ def load_library():
                                   ctypes.c_size_t, P(Grads), ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p]
     lib.gdr_fwd_bwd_noalloc.argtypes = [P(Shape), P(Inputs), ctypes.c_void_p, ctypes.c_void_p, P(Grads),
                                         ctypes.c_void_p, ctypes.c_void_p]
+    ptr, size = ctypes.c_void_p, ctypes.c_size_t
+    lib.gdr_step.argtypes = [P(Shape), P(Inputs), ptr, ctypes.c_int32, ptr, ptr, ptr]
+    lib.gdr_scan_workspace_bytes.argtypes = [P(ScanShape), P(size)]
+    lib.gdr_scan_fwd.argtypes = [P(ScanShape), P(ScanInputs), ptr, size, ptr, ptr, ptr]
+    lib.gdr_scan_bwd.argtypes = [P(ScanShape), P(ScanInputs), ptr, ptr, ptr, size, P(ScanGrads), ptr]
+    lib.gdr_scan_step.argtypes = [P(ScanShape), P(ScanInputs), ptr, ctypes.c_int32, ptr, ptr, ptr]
+    lib.gdr_norm_fwd.argtypes = [P(NormShape), ptr, ptr, ptr, ptr, ptr, ptr]
+    lib.gdr_norm_quant.argtypes = [P(NormShape), ptr, ptr, ptr, ptr, ptr, ptr, ptr]
+    lib.gdr_norm_workspace_bytes.argtypes = [P(NormShape), P(size)]
+    lib.gdr_norm_bwd.argtypes = [P(NormShape), ptr, ptr, ptr, ptr, ptr, size, ptr, ptr, ptr]
     lib.gdr_last_error.argtypes = []
     lib.gdr_last_error.restype = ctypes.c_char_p
     for name in SYMBOLS[:-1]:
@@ -206,6 +240,202 @@ def gdr_run_stage(prob: Problem, t: Dict, dO: torch.Tensor, dht: Optional[torch.
     _check(load_library().gdr_run_stage(ctypes.byref(prob.shape), ctypes.byref(inp), _ptr(dO), _ptr(dht),
                                         _ptr(ws), ws.numel() * ws.element_size(), ctypes.byref(gr), _ptr(ht),
                                         stage, _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# the operators around the delta rule: the single-token steps, the gated linear
+# recurrence and the row norm.  These entry points check their tensors (type,
+# size, layout, device) before the library is called; its own checks follow.
+# ---------------------------------------------------------------------------
+
+_DTYPE = {GDR_BF16: torch.bfloat16, GDR_F32: torch.float32}
+
+
+def _bad(message: str) -> None:
+    raise GdrError(GDR_EINVAL, message)
+
+
+def _check_tensors(specs) -> None:
+    """specs: (name, tensor or None, numel, dtype).  Every tensor given has that type
+    and size, is contiguous, and lies on the current GPU, where the call is enqueued."""
+    devices = set()
+    for name, t, numel, dtype in specs:
+        if t is None:
+            continue
+        if t.dtype != dtype:
+            _bad(f"{name} is {t.dtype}, expected {dtype}")
+        if t.numel() != numel:
+            _bad(f"{name} has {t.numel()} elements, expected {numel}")
+        if not t.is_contiguous():
+            _bad(f"{name} is not contiguous")
+        devices.add(t.device)
+    for d in devices:
+        if d.type != "cuda":
+            _bad(f"tensors are on {d}, expected a GPU")
+    if len(devices) > 1:
+        _bad(f"tensors are on several devices: {sorted(map(str, devices))}")
+    for d in devices:
+        if d.index != torch.cuda.current_device():
+            _bad(f"tensors are on {d}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _check_workspace(ws: Optional[torch.Tensor], like: Optional[torch.Tensor]) -> int:
+    if ws is None:
+        return 0
+    if not ws.is_contiguous():
+        _bad("the workspace is not contiguous")
+    if like is not None and ws.device != like.device:
+        _bad(f"the workspace is on {ws.device}, the tensors are on {like.device}")
+    return ws.numel() * ws.element_size()
+
+
+def _pool_size(state: torch.Tensor, per_state: int) -> int:
+    """Number of states in a pool [P, ...] of per_state elements each."""
+    if state.dim() < 1 or state.numel() != state.shape[0] * per_state:
+        _bad(f"state has shape {tuple(state.shape)}, expected [P, ...] with {per_state} elements a state")
+    return state.shape[0]
+
+
+class ScanProblem:
+    """Host-side description of one gated linear recurrence (gdr_scan_shape)."""
+
+    def __init__(self, B: int, T: int, H: int, D: int, N: int, gate: int, dtype: int, cu_seqlens=None,
+                 gate_scale: float = 0.0, convex: bool = False):
+        self.cu = None
+        if cu_seqlens is not None:
+            self.cu = torch.as_tensor(cu_seqlens, dtype=torch.int64).contiguous().cpu()
+            if self.cu.numel() != N + 1:
+                _bad(f"cu_seqlens has {self.cu.numel()} entries, expected {N + 1}")
+        self.shape = ScanShape(B, T, H, D, N,
+                               None if self.cu is None else ctypes.cast(self.cu.data_ptr(),
+                                                                        ctypes.POINTER(ctypes.c_int64)),
+                               gate, dtype, gate_scale if gate == GDR_GATE_CHANNEL_SIGMOID else 0.0, int(convex))
+        self.ref = ctypes.byref(self.shape)
+        tokens = B * T
+        self.x_numel = tokens * H * D
+        self.g_numel = tokens * H if gate == GDR_GATE_SCALAR else self.x_numel
+        self.state_numel, self.per_state, self.D, self.H = N * H * D, H * D, D, H
+        self.rows, self.io = N, _DTYPE.get(dtype)
+
+    def input_specs(self, t: Dict):
+        return (("x", t["x"], self.x_numel, self.io), ("g", t["g"], self.g_numel, self.io),
+                ("A_log", t.get("A_log"), self.H, torch.float32),
+                ("dt_bias", t.get("dt_bias"), self.per_state, torch.float32),
+                ("h0", t.get("h0"), self.state_numel, torch.float32))
+
+
+def _scan_inputs(t: Dict) -> ScanInputs:
+    return ScanInputs(_ptr(t["x"]), _ptr(t["g"]), _ptr(t.get("A_log")), _ptr(t.get("dt_bias")), _ptr(t.get("h0")))
+
+
+def gdr_scan_workspace_bytes(prob: ScanProblem) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load_library().gdr_scan_workspace_bytes(prob.ref, ctypes.byref(out)))
+    return out.value
+
+
+def alloc_scan_workspace(prob: ScanProblem, device="cuda") -> torch.Tensor:
+    return torch.empty(max(gdr_scan_workspace_bytes(prob), 256), dtype=torch.uint8, device=device)
+
+
+def gdr_scan_fwd(prob: ScanProblem, t: Dict, ws: torch.Tensor, y: torch.Tensor, ht: Optional[torch.Tensor] = None,
+                 stream=None) -> None:
+    _check_tensors(prob.input_specs(t) + (("y", y, prob.x_numel, prob.io), ("ht", ht, prob.state_numel, torch.float32)))
+    n = _check_workspace(ws, y)
+    inp = _scan_inputs(t)
+    _check(load_library().gdr_scan_fwd(prob.ref, ctypes.byref(inp), _ptr(ws), n, _ptr(y), _ptr(ht), _stream(stream)))
+
+
+def gdr_scan_bwd(prob: ScanProblem, t: Dict, dy: torch.Tensor, dht: Optional[torch.Tensor], ws: torch.Tensor,
+                 out: Dict, stream=None) -> None:
+    """out: dx, dg, and optionally dh0; for the per-channel gates dA_log and ddt_bias."""
+    f32 = torch.float32
+    _check_tensors(prob.input_specs(t) + (
+        ("dy", dy, prob.x_numel, prob.io), ("dht", dht, prob.state_numel, f32), ("dx", out["dx"], prob.x_numel, prob.io),
+        ("dg", out["dg"], prob.g_numel, prob.io), ("dh0", out.get("dh0"), prob.state_numel, f32),
+        ("dA_log", out.get("dA_log"), prob.H, f32), ("ddt_bias", out.get("ddt_bias"), prob.per_state, f32)))
+    n = _check_workspace(ws, dy)
+    inp = _scan_inputs(t)
+    gr = ScanGrads(_ptr(out["dx"]), _ptr(out["dg"]), _ptr(out.get("dh0")), _ptr(out.get("dA_log")),
+                   _ptr(out.get("ddt_bias")))
+    _check(load_library().gdr_scan_bwd(prob.ref, ctypes.byref(inp), _ptr(dy), _ptr(dht), _ptr(ws), n, ctypes.byref(gr),
+                                       _stream(stream)))
+
+
+def gdr_scan_step(prob: ScanProblem, t: Dict, state: torch.Tensor, y: torch.Tensor,
+                  slots: Optional[torch.Tensor] = None, stream=None) -> None:
+    P = _pool_size(state, prob.per_state)
+    _check_tensors(prob.input_specs(t) + (("y", y, prob.x_numel, prob.io), ("state", state, state.numel(), torch.float32),
+                                          ("slots", slots, prob.rows, torch.int32)))
+    inp = _scan_inputs(t)
+    _check(load_library().gdr_scan_step(prob.ref, ctypes.byref(inp), _ptr(state), P, _ptr(slots), _ptr(y),
+                                        _stream(stream)))
+
+
+def gdr_step(prob: Problem, t: Dict, state: torch.Tensor, o: torch.Tensor, slots: Optional[torch.Tensor] = None,
+             stream=None) -> None:
+    """prob: Problem(N, 1, H, D, N, ...); t: q k v g b (and A_log, dt_bias)."""
+    s = prob.shape
+    N, H, D, io = s.B * s.T, s.H, s.Dk, _DTYPE.get(s.dtype)
+    qk = N * (s.Hk or H) * D
+    gn = N * H if s.gate == GDR_GATE_SCALAR else N * H * D
+    P = _pool_size(state, H * D * D)
+    _check_tensors((("q", t["q"], qk, io), ("k", t["k"], qk, io), ("v", t["v"], N * H * D, io), ("g", t["g"], gn, io),
+                    ("b", t["b"], N * H, io), ("A_log", t.get("A_log"), H, torch.float32),
+                    ("dt_bias", t.get("dt_bias"), H * D, torch.float32), ("o", o, N * H * D, io),
+                    ("state", state, state.numel(), torch.float32), ("slots", slots, N, torch.int32)))
+    inp = _inputs(t)
+    _check(load_library().gdr_step(ctypes.byref(s), ctypes.byref(inp), _ptr(state), P, _ptr(slots), _ptr(o),
+                                   _stream(stream)))
+
+
+class NormProblem:
+    """Host-side description of one row norm (gdr_norm_shape)."""
+
+    def __init__(self, rows: int, width: int, dtype: int, eps: float = 1e-6, group: int = 0):
+        self.shape = NormShape(rows, width, dtype, eps, group)
+        self.ref = ctypes.byref(self.shape)
+        self.numel, self.width, self.io = rows * width, width, _DTYPE.get(dtype)
+        self.scales_numel = rows * (-(-width // group) if group > 0 else 1)
+
+
+def gdr_norm_workspace_bytes(prob: NormProblem) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load_library().gdr_norm_workspace_bytes(prob.ref, ctypes.byref(out)))
+    return out.value
+
+
+def alloc_norm_workspace(prob: NormProblem, device="cuda") -> torch.Tensor:
+    return torch.empty(max(gdr_norm_workspace_bytes(prob), 256), dtype=torch.uint8, device=device)
+
+
+def gdr_norm_fwd(prob: NormProblem, x: torch.Tensor, w: Optional[torch.Tensor], y: torch.Tensor,
+                 res: Optional[torch.Tensor] = None, res_out: Optional[torch.Tensor] = None, stream=None) -> None:
+    n, io = prob.numel, prob.io
+    _check_tensors((("x", x, n, io), ("w", w, prob.width, torch.float32), ("y", y, n, io), ("res", res, n, io),
+                    ("res_out", res_out, n, io)))
+    _check(load_library().gdr_norm_fwd(prob.ref, _ptr(x), _ptr(res), _ptr(w), _ptr(y), _ptr(res_out), _stream(stream)))
+
+
+def gdr_norm_quant(prob: NormProblem, x: torch.Tensor, w: Optional[torch.Tensor], q: torch.Tensor,
+                   scales: torch.Tensor, res: Optional[torch.Tensor] = None, res_out: Optional[torch.Tensor] = None,
+                   stream=None) -> None:
+    n, io = prob.numel, prob.io
+    _check_tensors((("x", x, n, io), ("w", w, prob.width, torch.float32), ("q", q, n, torch.float8_e4m3fn),
+                    ("scales", scales, prob.scales_numel, torch.float32), ("res", res, n, io),
+                    ("res_out", res_out, n, io)))
+    _check(load_library().gdr_norm_quant(prob.ref, _ptr(x), _ptr(res), _ptr(w), _ptr(q), _ptr(scales), _ptr(res_out),
+                                         _stream(stream)))
+
+
+def gdr_norm_bwd(prob: NormProblem, r: torch.Tensor, w: Optional[torch.Tensor], dy: torch.Tensor, dx: torch.Tensor,
+                 dw: Optional[torch.Tensor], ws: Optional[torch.Tensor], dres: Optional[torch.Tensor] = None,
+                 stream=None) -> None:
+    n, io = prob.numel, prob.io
+    _check_tensors((("r", r, n, io), ("w", w, prob.width, torch.float32), ("dy", dy, n, io), ("dx", dx, n, io),
+                    ("dw", dw, prob.width, torch.float32), ("dres", dres, n, io)))
+    _check(load_library().gdr_norm_bwd(prob.ref, _ptr(r), _ptr(w), _ptr(dy), _ptr(dres), _ptr(ws),
+                                       _check_workspace(ws, dy), _ptr(dx), _ptr(dw), _stream(stream)))
 
 
 # ---------------------------------------------------------------------------

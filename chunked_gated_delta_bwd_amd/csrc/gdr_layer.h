@@ -1,0 +1,98 @@
+// Internal declarations of the operators around the delta rule: the gated linear
+// recurrence (gdr_scan.hip), the row norm (gdr_norm.hip) and the delta rule's
+// single-token step (gdr_step.hip).  Their argument checks are in gdr_layer.cpp.
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "../../include/gdr.h"
+
+namespace gdr {
+
+// How the recurrence's kernels read the gate.
+enum ScanGate {
+  kScanLog = 0,       // one log decay per channel (scalar gate, D = 1)
+  kScanHeadLog = 1,   // one log decay per head (scalar gate, D > 1)
+  kScanSoftplus = 2,
+  kScanSigmoid = 3,
+};
+
+constexpr int kScanTile = 128;   // tokens per tile of the recurrence
+
+// One row per tile: at most kScanTile tokens of one sequence.  A sequence without
+// tokens has one empty tile, so that its states are passed through.
+struct ScanTile {
+  int32_t t_start, len, seq, idx;   // idx: the tile's place in its sequence
+};
+
+// Sequences handed to the table kernel by value, kScanBatch per launch.
+constexpr int kScanBatch = 120;
+struct ScanBatch {
+  int32_t n, seq0, pad[2];
+  int32_t t_start[kScanBatch], len[kScanBatch], tile0[kScanBatch];
+};
+static_assert(sizeof(ScanBatch) <= 2048, "kernel argument size");
+
+struct ScanParams {
+  int32_t H, D, C, N;          // C = H D channels
+  int32_t gate, dtype, convex;
+  int32_t NT;                  // tiles over all sequences
+  int32_t dense_T;             // dense: tokens per sequence; -1: the tiles are in `tab`
+  float gate_scale;
+  const void *x, *g, *dy;
+  const float *A_log, *dt_bias, *h0, *dht;
+  void *y, *dx, *dg;
+  float *ht, *dh0, *dA_log, *ddt_bias;
+  ScanTile* tab;
+  float* carry;                // [NT][C] state at the start of each tile
+  float* part;                 // [NT][2][C] partial sums of ddt_bias and dA_log
+};
+
+int launch_scan_tables(const ScanParams& p, const ScanBatch& b, void* stream);
+int launch_scan(const ScanParams& p, bool backward, void* stream);
+int launch_scan_params(const ScanParams& p, void* stream);
+
+struct ScanStepParams {
+  int32_t H, D, C, N, P;
+  int32_t gate, dtype, convex;
+  float gate_scale;
+  const void *x, *g;
+  const float *A_log, *dt_bias;
+  const int32_t* slots;
+  float* state;
+  void* y;
+};
+int launch_scan_step(const ScanStepParams& p, void* stream);
+
+constexpr int kNormMaxWidth = 32768;
+constexpr int kNormPartials = 512;   // workgroups of the backward, each with a row of partial sums of dw
+
+struct NormParams {
+  int64_t rows;
+  int32_t width, dtype, group;
+  float eps;
+  const void *x, *res, *dy, *dres;
+  const float* w;
+  void *y, *res_out, *q, *dx;
+  float *scales, *dw, *part;
+};
+int launch_norm(const NormParams& p, void* stream);        // y, or q and scales
+int launch_norm_bwd(const NormParams& p, void* stream);
+int norm_bwd_partials(int64_t rows, int32_t width, int32_t dtype);
+
+struct StepParams {
+  int32_t N, H, Hk, G, D, P;
+  int32_t gate, gate_fn, dtype;   // gate: 0 per head, 1 per channel; gate_fn as in Params
+  float scale, gate_scale;
+  const void *q, *k, *v, *g, *b;
+  const float *A_log, *dt_bias;
+  const int32_t* slots;
+  float* state;
+  void* o;
+};
+int launch_step(const StepParams& p, void* stream);
+// gdr_step's pool, slots and output (gdr_layer.cpp).
+gdr_status check_step_pool(int32_t N, const float* state, int32_t P, const int32_t* slots, const void* o);
+
+}  // namespace gdr

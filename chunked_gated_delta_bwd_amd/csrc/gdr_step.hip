@@ -1,0 +1,142 @@
+// The gated delta rule's single-token step on a pool of states (gdr_step).
+//
+//   S' = S Diag(e^lambda),  d = beta (v - S' kn),  S = S' + d kn^T,
+//   o = scale S qn = scale (S' qn + d (kn . qn))
+// Every row of S (one value channel) is independent given q, k and the gate, so
+// eight lanes hold a row in registers, both products with the row reduce over
+// those lanes alone, and the state is read and written once.  Each group of eight
+// lanes forms the norms of q and k itself from its share of the channels: no LDS
+// and no barrier.  The state's bytes bound the step.
+#include <hip/hip_runtime.h>
+
+#include "gdr_device.h"
+#include "gdr_gate.h"
+#include "gdr_layer.h"
+
+namespace gdr {
+namespace {
+
+// Lane j of a row's eight holds channels 32 m + 4 j .. + 3, m < D / 32: the eight
+// lanes read 128 contiguous bytes of the row at a time.
+template <typename TIO, int D>
+__device__ __forceinline__ void load_row(const void* base, int64_t off, int j, float (&x)[D / 8]) {
+#pragma unroll
+  for (int m = 0; m < D / 32; ++m) {
+    float y[4];
+    IO<TIO>::load4(base, off + 32 * m + 4 * j, y);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[4 * m + e] = y[e];
+  }
+}
+
+// R: rows of the state per workgroup (32 per pass)
+template <typename TIO, int D, int GM, int R>
+__global__ __launch_bounds__(256) void k_step(const StepParams p) {
+  constexpr int E = D / 8, NP = R / 32, SPLIT = D / R;
+  const int64_t id = blockIdx.x;
+  const int part = int(id % SPLIT);
+  const int h = int(id / SPLIT % p.H);
+  int n = int(id / SPLIT / p.H);
+  const int slot = p.slots ? p.slots[n] : n;
+  if (slot < 0 || slot >= p.P) return;
+  bool later = false;
+  if (p.slots) {
+    bool earlier = false;
+    for (int m = threadIdx.x; m < p.N; m += 256)
+      if (p.slots[m] == slot) {
+        earlier |= m < n;
+        later |= m > n;
+      }
+    if (__syncthreads_or(earlier)) return;
+    later = __syncthreads_or(later);
+  }
+  const int j = threadIdx.x & 7, row0 = part * R + (threadIdx.x >> 3);
+  float* st = p.state + (int64_t(slot) * p.H + h) * (D * D);
+  float S[NP][E];
+#pragma unroll
+  for (int i = 0; i < NP; ++i) load_row<float, D>(st, int64_t(row0 + 32 * i) * D, j, S[i]);
+  float bias[E], eA = 0.f;
+  if constexpr (GM != 0) {
+    eA = expf(p.A_log[h]);
+    load_row<float, D>(p.dt_bias, int64_t(h) * D, j, bias);
+  }
+  for (;;) {
+    const int64_t hk = int64_t(n) * p.Hk + h / p.G, hv = int64_t(n) * p.H + h;
+    float q[E], k[E], a[E], qq = 0.f, kk = 0.f, kq = 0.f;
+    load_row<TIO, D>(p.q, hk * D, j, q);
+    load_row<TIO, D>(p.k, hk * D, j, k);
+    if constexpr (GM == 0) {
+      a[0] = exp_io<TIO>(IO<TIO>::load1(p.g, hv));
+#pragma unroll
+      for (int e = 1; e < E; ++e) a[e] = a[0];
+    } else {
+      load_row<TIO, D>(p.g, hv * D, j, a);
+#pragma unroll
+      for (int e = 0; e < E; ++e) a[e] = exp_io<TIO>(gate_log<TIO, GM - 1>(a[e] + bias[e], eA, p.gate_scale));
+    }
+    const float beta = 1.f / (1.f + exp_io<TIO>(-IO<TIO>::load1(p.b, hv)));
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      qq += q[e] * q[e];
+      kk += k[e] * k[e];
+    }
+    const float rq = rsqrtf(group_sum_dpp<8>(qq) + 1e-6f), rk = rsqrtf(group_sum_dpp<8>(kk) + 1e-6f);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      q[e] *= rq;
+      k[e] *= rk;
+      kq += k[e] * q[e];
+    }
+    kq = group_sum_dpp<8>(kq);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int row = row0 + 32 * i;
+      float r = 0.f, o = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        S[i][e] *= a[e];
+        r += S[i][e] * k[e];
+        o += S[i][e] * q[e];
+      }
+      r = group_sum_dpp<8>(r);
+      o = group_sum_dpp<8>(o);
+      const float d = beta * (IO<TIO>::load1(p.v, hv * D + row) - r);
+#pragma unroll
+      for (int e = 0; e < E; ++e) S[i][e] += d * k[e];
+      if (j == 0) IO<TIO>::store1(p.o, hv * D + row, p.scale * (o + d * kq));
+    }
+    if (!later) break;
+    do ++n; while (n < p.N && p.slots[n] != slot);
+    if (n >= p.N) break;
+  }
+#pragma unroll
+  for (int i = 0; i < NP; ++i)
+#pragma unroll
+    for (int m = 0; m < D / 32; ++m)
+      IO<float>::store4(st, int64_t(row0 + 32 * i) * D + 32 * m + 4 * j, S[i][4 * m], S[i][4 * m + 1], S[i][4 * m + 2],
+                        S[i][4 * m + 3]);
+}
+
+template <typename TIO, int D, int GM>
+int launch_gate(const StepParams& p, hipStream_t s) {
+  k_step<TIO, D, GM, 32><<<dim3(unsigned(int64_t(p.N) * p.H * (D / 32))), 256, 0, s>>>(p);
+  return static_cast<int>(hipGetLastError());
+}
+
+template <typename TIO, int D>
+int launch_dim(const StepParams& p, hipStream_t s) {
+  if (p.gate == 0) return launch_gate<TIO, D, 0>(p, s);
+  return p.gate_fn == 0 ? launch_gate<TIO, D, 1>(p, s) : launch_gate<TIO, D, 2>(p, s);
+}
+
+}  // namespace
+
+int launch_step(const StepParams& p, void* stream) {
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  (void)hipGetLastError();
+  if (p.N == 0) return 0;
+  if (p.dtype == GDR_BF16) return p.D == 128 ? launch_dim<bf16, 128>(p, s) : launch_dim<bf16, 64>(p, s);
+  return p.D == 128 ? launch_dim<float, 128>(p, s) : launch_dim<float, 64>(p, s);
+}
+
+}  // namespace gdr

@@ -222,6 +222,125 @@ gdr_status gdr_run_stage(const gdr_shape* shape, const gdr_inputs* in, const voi
 gdr_status gdr_fwd_bwd_noalloc(const gdr_shape* shape, const gdr_inputs* in, const void* dO, const float* dht,
                                gdr_grads* grads, float* ht, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Single-token step of the gated delta rule (serving).
+ *
+ * One token for each of N rows: shape is a dense gdr_shape with T == 1 and
+ * B == N rows (seq_split is ignored), `in` as above with h0 NULL.  `state` holds
+ * P states [P,H,Dv,Dk] fp32, as gdr_fwd's ht leaves them, updated in place; row
+ * n works on state slots[n] (slots: device int32 [N]; NULL: slot n, which needs
+ * P >= N).  Row n's token:
+ *   S <- S Diag(exp(lambda)) (I - beta kn kn^T) + beta v kn^T,  o = scale S qn.
+ * A row whose slot is outside [0, P) is padding: no state is touched and its row
+ * of o is left as it was.  Rows with the same slot are successive tokens of one
+ * sequence, taken in the order of n.  o: [N,1,H,Dv] dtype.  No workspace.
+ * No output may overlap an input.  Errors as gdr_fwd_recompute, and GDR_EINVAL
+ * for T != 1, a varlen shape, an h0, a NULL state, P < 0 or P < N without slots. */
+gdr_status gdr_step(const gdr_shape* shape, const gdr_inputs* in, float* state, int32_t P, const int32_t* slots,
+                    void* o, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Gated linear recurrence: the channel-wise member of the same family, for
+ * layers whose state is one number per channel.  Per sequence, head and channel:
+ *   a_t = exp(lambda_t), lambda_t by the gate as in the delta rule above,
+ *   s_t = a_t s_{t-1} + m_t x_t,   m_t = 1, or 1 - a_t with `convex`,
+ *   y_t = s_t,  s_0 = h0 (or 0).
+ * GDR_GATE_SCALAR takes one log decay per token and head, shared by the head's D
+ * channels (D == 1: one per channel); the per-channel gates take g, A_log and
+ * dt_bias as the delta rule does.  The log decay is meant to be <= 0; -inf is a
+ * reset (a = 0).  A positive one is taken as it stands as long as the product of
+ * exp(lambda) over any run of tokens stays in the fp32 range.
+ * The backward returns the gradients of L = sum_t <dy_t, y_t> + <dht, s_T>.
+ * x, y: [B,T,H,D] (or packed [1,T,H,D]), 1 <= D <= 256 with D == 1 or a multiple
+ * of 8; B, T, N, cu_seqlens_host, dtype and alignment as in gdr_shape.  States,
+ * products and sums are fp32; y, dx and dg are rounded once to dtype. */
+typedef struct {
+  int32_t B, T, H, D;               /* dense: [B,T,H,D]; varlen: B == 1, T == total tokens */
+  int32_t N;                        /* sequences, as in gdr_shape */
+  const int64_t* cu_seqlens_host;   /* as in gdr_shape (read during the call only) */
+  int32_t gate;                     /* gdr_gate */
+  int32_t dtype;                    /* gdr_dtype of x, g, y, dy, dx, dg */
+  float gate_scale;                 /* GDR_GATE_CHANNEL_SIGMOID only, as in gdr_shape */
+  int32_t convex;                   /* 0: s = a s + x; 1: s = a s + (1 - a) x */
+} gdr_scan_shape;
+
+typedef struct {                    /* device pointers; x and g may be NULL when B * T == 0 */
+  const void* x;                    /* [B,T,H,D] dtype */
+  const void* g;                    /* SCALAR: [B,T,H] log decay; CHANNEL: [B,T,H,D] raw gate; dtype */
+  const float *A_log, *dt_bias;     /* CHANNEL: [H], [H,D]; SCALAR: must be NULL */
+  const float* h0;                  /* [N,H,D] or NULL (zero initial state) */
+} gdr_scan_inputs;
+
+typedef struct {                    /* device pointers, all overwritten; dx and dg may be NULL when B * T == 0 */
+  void *dx, *dg;                    /* as x and g */
+  float* dh0;                       /* [N,H,D] or NULL (not returned) */
+  float *dA_log, *ddt_bias;         /* CHANNEL: [H], [H,D] required; SCALAR: must be NULL */
+} gdr_scan_grads;
+
+gdr_status gdr_scan_workspace_bytes(const gdr_scan_shape* shape, size_t* bytes);
+
+/* Forward: y (required unless there are no tokens) and optionally the final
+ * states ht [N,H,D] fp32 (a sequence without tokens returns its h0).  `ws` needs
+ * gdr_scan_workspace_bytes(), 256-byte aligned, with any content; afterwards it
+ * holds the states that gdr_scan_bwd on the same shape and inputs starts from.
+ * Calls that overlap in time need a workspace each.  Outputs must not overlap
+ * inputs.  Errors as gdr_fwd_recompute. */
+gdr_status gdr_scan_fwd(const gdr_scan_shape* shape, const gdr_scan_inputs* in, void* ws, size_t ws_bytes, void* y,
+                        float* ht, void* stream);
+
+/* Backward, after gdr_scan_fwd on the same shape, inputs and workspace (which it
+ * leaves fit for another gdr_scan_bwd).  dy as y, required unless there are no
+ * tokens; dht [N,H,D] fp32 or NULL (zero). */
+gdr_status gdr_scan_bwd(const gdr_scan_shape* shape, const gdr_scan_inputs* in, const void* dy, const float* dht,
+                        void* ws, size_t ws_bytes, const gdr_scan_grads* grads, void* stream);
+
+/* One token for each of N rows on a pool of states [P,H,D] fp32, updated in
+ * place: shape dense with T == 1, in->h0 NULL; state, P, slots, padding rows and
+ * rows that share a slot as in gdr_step.  y: [N,1,H,D] dtype. */
+gdr_status gdr_scan_step(const gdr_scan_shape* shape, const gdr_scan_inputs* in, float* state, int32_t P,
+                         const int32_t* slots, void* y, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Root-mean-square norm of rows with the residual's addition: what stands
+ * between the recurrences and the projections (over one head's channels of an
+ * output o, or over the whole model width).
+ *   r = x + res (res NULL: r = x),  n = r / sqrt(mean(r^2) + eps),  y = n * w.
+ * x, res, y, res_out: [rows,width] dtype; w: [width] fp32 or NULL (ones).  r is
+ * kept in fp32 for y; res_out (required with res, NULL without) is r rounded to
+ * dtype and may be res or x itself; y may be x or res itself unless that is
+ * res_out.  1 <= width <= 32768. */
+typedef struct {
+  int64_t rows;
+  int32_t width;
+  int32_t dtype;                    /* gdr_dtype of x, res, res_out, y, r, dy, dres, dx */
+  float eps;                        /* finite, >= 0 */
+  int32_t group;                    /* gdr_norm_quant: channels per scale, 0 (the whole row) or 128; else ignored */
+} gdr_norm_shape;
+
+gdr_status gdr_norm_fwd(const gdr_norm_shape* shape, const void* x, const void* res, const float* w, void* y,
+                        void* res_out, void* stream);
+
+/* The same with an 8-bit output: per row and group of channels
+ *   scale = max(max|y| / 448, 2^-126),  q = e4m3(y / scale)
+ * (OCP e4m3, round to nearest even), so that q * scale stands for y.  q:
+ * [rows,width] bytes; scales: [rows,ceil(width / group)] fp32 (group 0: [rows,1];
+ * the last group of a width that is no multiple of it is shorter).  A group that
+ * holds a NaN gets a NaN scale and NaN bytes. */
+gdr_status gdr_norm_quant(const gdr_norm_shape* shape, const void* x, const void* res, const float* w, void* q,
+                          float* scales, void* res_out, void* stream);
+
+/* Backward from r (res_out of the forward, or x without a residual; the row's
+ * statistics are taken again from it):
+ *   dr = (w dy - n mean(n w dy)) / sqrt(mean(r^2) + eps) + dres,  dw = sum_rows dy n
+ * dr is the gradient of x and of res alike.  dres: the gradient that reaches
+ * res_out from elsewhere, or NULL.  dx: [rows,width], may be dy or dres itself;
+ * dw: [width] fp32 or NULL (not returned; then ws may be NULL).  ws:
+ * gdr_norm_workspace_bytes(), 256-byte aligned, any content; calls that overlap
+ * in time need one each.  Sums run in a fixed order. */
+gdr_status gdr_norm_workspace_bytes(const gdr_norm_shape* shape, size_t* bytes);
+gdr_status gdr_norm_bwd(const gdr_norm_shape* shape, const void* r, const float* w, const void* dy, const void* dres,
+                        void* ws, size_t ws_bytes, void* dx, float* dw, void* stream);
+
 /* Thread-local text for the last non-OK status returned to this thread. */
 const char* gdr_last_error(void);
 
