@@ -6,55 +6,51 @@
 
 namespace gdr {
 
-// exp for the storage type: the hardware exponential of x log2(e) (rounding the
-// product costs |x| 2^-24 relative, nothing beside a bf16 result) or expf
-template <typename TIO> __device__ __forceinline__ float exp_io(float x);
-template <> __device__ __forceinline__ float exp_io<bf16>(float x) { return __expf(x); }
-template <> __device__ __forceinline__ float exp_io<float>(float x) { return expf(x); }
-
-// log(1 + e) for e in [0, 1]: the hardware log of a rounded 1 + e loses the
-// relative accuracy of a small e, so there the series (next term e^6 / 6 < 2e-8 e)
-__device__ __forceinline__ float log1p01(float e) {
-  const float series = e * (1.f + e * (-0.5f + e * (1.f / 3.f + e * (-0.25f + e * 0.2f))));
-  return e < 0.04f ? series : __logf(1.f + e);
+// log2(1 + e) for e in [0, 1].  u = 1 + e is rounded; c = e - (u - 1) is what the
+// rounding lost, exactly, and log2(u + c) = log2(u) + c log2(e) / u with u near 1
+// wherever c matters: without it a small e would keep no relative accuracy.
+__device__ __forceinline__ float log2_1p(float e) {
+  const float u = 1.f + e;
+  return fmaf(e - (u - 1.f), kLog2e, __builtin_amdgcn_logf(u));
 }
 
-// 1 - exp(l) given a = exp(l): near l = 0 by the series (next term l^7 / 5040)
-__device__ __forceinline__ float one_minus_exp(float l, float a) {
-  const float series = -l * (1.f + l * (0.5f + l * (1.f / 6.f + l * (1.f / 24.f + l * (1.f / 120.f + l * (1.f / 720.f))))));
-  return fabsf(l) < 0.25f ? series : 1.f - a;
+// 1 - 2^l given a = 2^l: near l = 0 by the series of 1 - e^x, x = l ln 2 (next term
+// x^7 / 5040)
+__device__ __forceinline__ float one_minus_exp2(float l, float a) {
+  const float x = l * 0.6931471805599453f;
+  const float series = -x * (1.f + x * (0.5f + x * (1.f / 6.f + x * (1.f / 24.f + x * (1.f / 120.f + x * (1.f / 720.f))))));
+  return fabsf(l) < 0.36f ? series : 1.f - a;
 }
 
-// Log decay of the per-channel gates from the raw gate plus bias z.
+// Base-2 log decay of the per-channel gates (lambda log2(e), so that the decay is
+// one bare exponential) from z2 = (raw gate + bias) log2(e).
 //   FN 0: -eA softplus(z);  FN 1: gs sigmoid(eA z)
-template <typename TIO, int FN>
-__device__ __forceinline__ float gate_log(float z, float eA, float gs) {
-  if constexpr (FN == 0) {
-    return -eA * (fmaxf(z, 0.f) + log1p01(exp_io<TIO>(-fabsf(z))));
-  } else {
-    return gs / (1.f + exp_io<TIO>(-eA * z));
-  }
+template <int FN>
+__device__ __forceinline__ float gate_log2(float z2, float eA, float gs) {
+  if constexpr (FN == 0) return -eA * (fmaxf(z2, 0.f) + log2_1p(fast_exp2(-fabsf(z2))));
+  else return gs * kLog2e * __builtin_amdgcn_rcpf(1.f + fast_exp2(-eA * z2));
 }
 
-// The same with d lambda / d z and d lambda / d A_log.  Where the sigmoid or the
-// decay saturates (z infinite) the slopes are finite, so a gate that is shut or
-// open for good gives zero gradients and no NaN.
-template <typename TIO, int FN>
-__device__ __forceinline__ void gate_log_grad(float z, float eA, float gs, float& lam, float& dz, float& dA) {
+// The same with d lambda / d z and d lambda / d A_log.  Where the gate saturates
+// (z or lambda infinite) the slopes are finite, so a gate that is shut or open for
+// good gives zero gradients and no NaN.
+template <int FN>
+__device__ __forceinline__ void gate_log2_grad(float z2, float eA, float gs, float& l2, float& dz, float& dA) {
+  constexpr float kLn2 = 0.6931471805599453f;
   if constexpr (FN == 0) {
-    const float e = exp_io<TIO>(-fabsf(z));
-    const float r = 1.f / (1.f + e);
-    lam = -eA * (fmaxf(z, 0.f) + log1p01(e));
-    dz = -eA * (z >= 0.f ? r : e * r);
-    dA = fmaxf(lam, -3.0e38f);
+    const float e = fast_exp2(-fabsf(z2));
+    const float r = __builtin_amdgcn_rcpf(1.f + e);
+    l2 = -eA * (fmaxf(z2, 0.f) + log2_1p(e));
+    dz = -eA * (z2 >= 0.f ? r : e * r);
+    dA = fmaxf(l2, -3.0e38f) * kLn2;
   } else {
-    const float w = eA * z;
-    const float e = exp_io<TIO>(-fabsf(w));
-    const float r = 1.f / (1.f + e);
+    const float w2 = eA * z2;
+    const float e = fast_exp2(-fabsf(w2));
+    const float r = __builtin_amdgcn_rcpf(1.f + e);
     const float slope = gs * e * r * r;
-    lam = gs * (w >= 0.f ? r : e * r);
+    l2 = gs * kLog2e * (w2 >= 0.f ? r : e * r);
     dz = slope * eA;
-    dA = slope * fminf(fmaxf(w, -200.f), 200.f);
+    dA = slope * fminf(fmaxf(w2, -256.f), 256.f) * kLn2;
   }
 }
 

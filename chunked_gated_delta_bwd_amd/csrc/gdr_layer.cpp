@@ -49,6 +49,7 @@ gdr_status check_ws(size_t need, const void* ws, size_t ws_bytes) {
 
 int64_t tiles_of(int64_t len) { return std::max<int64_t>(1, (len + gdr::kScanTile - 1) / gdr::kScanTile); }
 
+// NT_out: tiles over all sequences.
 gdr_status check_scan_shape(const gdr_scan_shape* s, int64_t* NT_out) {
   if (!s) return set_error(GDR_EINVAL, "shape is NULL");
   if (s->gate != GDR_GATE_SCALAR && s->gate != GDR_GATE_CHANNEL && s->gate != GDR_GATE_CHANNEL_SIGMOID)
@@ -85,7 +86,7 @@ gdr_status check_scan_shape(const gdr_scan_shape* s, int64_t* NT_out) {
 }
 
 struct ScanLayout {
-  size_t tab = 0, carry = 0, part = 0, total = 0;
+  size_t tab = 0, counter = 0, words = 0, carry = 0, part = 0, total = 0;
 };
 
 ScanLayout scan_layout(const gdr_scan_shape* s, int64_t NT) {
@@ -94,6 +95,8 @@ ScanLayout scan_layout(const gdr_scan_shape* s, int64_t NT) {
   auto take = [&](size_t bytes) { size_t o = off; off = align256(off + bytes); return o; };
   const size_t C = size_t(s->H) * s->D;
   L.tab = take(s->cu_seqlens_host ? NT * sizeof(gdr::ScanTile) : 0);
+  L.counter = take(4);
+  L.words = take(NT * C * 16);
   L.carry = take(NT * C * 4);
   L.part = take(s->gate != GDR_GATE_SCALAR ? NT * 2 * C * 4 : 0);
   L.total = off;
@@ -127,13 +130,21 @@ gdr::ScanParams scan_params(const gdr_scan_shape* s, const gdr_scan_inputs* in, 
   p.x = in->x; p.g = in->g; p.A_log = in->A_log; p.dt_bias = in->dt_bias; p.h0 = in->h0;
   char* w = static_cast<char*>(ws);
   p.tab = reinterpret_cast<gdr::ScanTile*>(w + L.tab);
+  // as many tiles as sequences: none waits for another
+  p.words = NT > s->N ? reinterpret_cast<uint64_t*>(w + L.words) : nullptr;
+  p.counter = reinterpret_cast<uint32_t*>(w + L.counter);
   p.carry = reinterpret_cast<float*>(w + L.carry);
   p.part = reinterpret_cast<float*>(w + L.part);
   return p;
 }
 
-// The tile table of a packed problem: sequences by value, kScanBatch a launch.
-gdr_status scan_tables(const gdr_scan_shape* s, const gdr::ScanParams& p, void* stream) {
+// What a call's main kernel finds: the words cleared, and the tile table of a
+// packed problem (sequences by value, kScanBatch a launch).
+gdr_status scan_prologue(const gdr_scan_shape* s, const gdr::ScanParams& p, void* stream) {
+  if (p.words) {
+    const gdr_status st = hip_status(gdr::launch_scan_clear(p, stream), "scan clear kernel");
+    if (st != GDR_OK) return st;
+  }
   if (!s->cu_seqlens_host) return GDR_OK;
   gdr::ScanBatch b;
   std::memset(&b, 0, sizeof(b));
@@ -240,7 +251,7 @@ gdr_status gdr_scan_fwd(const gdr_scan_shape* shape, const gdr_scan_inputs* in, 
   gdr::ScanParams p = scan_params(shape, in, NT, L, ws);
   p.y = y;
   p.ht = ht;
-  if ((st = scan_tables(shape, p, stream)) != GDR_OK) return st;
+  if ((st = scan_prologue(shape, p, stream)) != GDR_OK) return st;
   return hip_status(gdr::launch_scan(p, false, stream), "scan kernel");
 }
 
@@ -264,7 +275,7 @@ gdr_status gdr_scan_bwd(const gdr_scan_shape* shape, const gdr_scan_inputs* in, 
   gdr::ScanParams p = scan_params(shape, in, NT, L, ws);
   p.dy = dy; p.dht = dht;
   p.dx = grads->dx; p.dg = grads->dg; p.dh0 = grads->dh0; p.dA_log = grads->dA_log; p.ddt_bias = grads->ddt_bias;
-  if ((st = scan_tables(shape, p, stream)) != GDR_OK) return st;
+  if ((st = scan_prologue(shape, p, stream)) != GDR_OK) return st;
   if ((st = hip_status(gdr::launch_scan(p, true, stream), "scan gradient kernel")) != GDR_OK) return st;
   return par ? hip_status(gdr::launch_scan_params(p, stream), "parameter reduction kernel") : GDR_OK;
 }

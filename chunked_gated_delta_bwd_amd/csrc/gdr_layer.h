@@ -18,12 +18,13 @@ enum ScanGate {
   kScanSigmoid = 3,
 };
 
-constexpr int kScanTile = 128;   // tokens per tile of the recurrence
+constexpr int kScanTile = 64;   // tokens per tile of the recurrence
 
 // One row per tile: at most kScanTile tokens of one sequence.  A sequence without
 // tokens has one empty tile, so that its states are passed through.
 struct ScanTile {
-  int32_t t_start, len, seq, idx;   // idx: the tile's place in its sequence
+  int32_t t_start, len, seq;
+  int32_t idx, after;   // tiles of the sequence before and after it
 };
 
 // Sequences handed to the table kernel by value, kScanBatch per launch.
@@ -46,11 +47,14 @@ struct ScanParams {
   float *ht, *dh0, *dA_log, *ddt_bias;
   ScanTile* tab;
   float* carry;                // [NT][C] state at the start of each tile
+  uint64_t* words;             // [NT][2][C] published folds and states; NULL: every sequence is one tile
+  uint32_t* counter;           // tiles taken
   float* part;                 // [NT][2][C] partial sums of ddt_bias and dA_log
 };
 
 int launch_scan_tables(const ScanParams& p, const ScanBatch& b, void* stream);
 int launch_scan(const ScanParams& p, bool backward, void* stream);
+int launch_scan_clear(const ScanParams& p, void* stream);
 int launch_scan_params(const ScanParams& p, void* stream);
 
 struct ScanStepParams {

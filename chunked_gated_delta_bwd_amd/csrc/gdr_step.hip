@@ -59,6 +59,8 @@ __global__ __launch_bounds__(256) void k_step(const StepParams p) {
   if constexpr (GM != 0) {
     eA = expf(p.A_log[h]);
     load_row<float, D>(p.dt_bias, int64_t(h) * D, j, bias);
+#pragma unroll
+    for (int e = 0; e < E; ++e) bias[e] *= kLog2e;
   }
   for (;;) {
     const int64_t hk = int64_t(n) * p.Hk + h / p.G, hv = int64_t(n) * p.H + h;
@@ -66,15 +68,15 @@ __global__ __launch_bounds__(256) void k_step(const StepParams p) {
     load_row<TIO, D>(p.q, hk * D, j, q);
     load_row<TIO, D>(p.k, hk * D, j, k);
     if constexpr (GM == 0) {
-      a[0] = exp_io<TIO>(IO<TIO>::load1(p.g, hv));
+      a[0] = fast_exp2(IO<TIO>::load1(p.g, hv) * kLog2e);
 #pragma unroll
       for (int e = 1; e < E; ++e) a[e] = a[0];
     } else {
       load_row<TIO, D>(p.g, hv * D, j, a);
 #pragma unroll
-      for (int e = 0; e < E; ++e) a[e] = exp_io<TIO>(gate_log<TIO, GM - 1>(a[e] + bias[e], eA, p.gate_scale));
+      for (int e = 0; e < E; ++e) a[e] = fast_exp2(gate_log2<GM - 1>(fmaf(a[e], kLog2e, bias[e]), eA, p.gate_scale));
     }
-    const float beta = 1.f / (1.f + exp_io<TIO>(-IO<TIO>::load1(p.b, hv)));
+    const float beta = 1.f / (1.f + fast_exp2(-kLog2e * IO<TIO>::load1(p.b, hv)));
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       qq += q[e] * q[e];
