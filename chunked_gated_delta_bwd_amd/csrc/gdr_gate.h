@@ -31,26 +31,22 @@ __device__ __forceinline__ float gate_log2(float z2, float eA, float gs) {
   else return gs * kLog2e * __builtin_amdgcn_rcpf(1.f + fast_exp2(-eA * z2));
 }
 
-// The same with d lambda / d z and d lambda / d A_log.  Where the gate saturates
-// (z or lambda infinite) the slopes are finite, so a gate that is shut or open for
-// good gives zero gradients and no NaN.
+// The same with the slope d lambda / d z.  Where the gate saturates (z infinite) the
+// slope is finite, so a gate that is shut or open for good gives zero gradients and
+// no NaN.
 template <int FN>
-__device__ __forceinline__ void gate_log2_grad(float z2, float eA, float gs, float& l2, float& dz, float& dA) {
-  constexpr float kLn2 = 0.6931471805599453f;
+__device__ __forceinline__ void gate_log2_grad(float z2, float eA, float gs, float& l2, float& dz) {
   if constexpr (FN == 0) {
     const float e = fast_exp2(-fabsf(z2));
     const float r = __builtin_amdgcn_rcpf(1.f + e);
     l2 = -eA * (fmaxf(z2, 0.f) + log2_1p(e));
     dz = -eA * (z2 >= 0.f ? r : e * r);
-    dA = fmaxf(l2, -3.0e38f) * kLn2;
   } else {
     const float w2 = eA * z2;
     const float e = fast_exp2(-fabsf(w2));
     const float r = __builtin_amdgcn_rcpf(1.f + e);
-    const float slope = gs * e * r * r;
     l2 = gs * kLog2e * (w2 >= 0.f ? r : e * r);
-    dz = slope * eA;
-    dA = slope * fminf(fmaxf(w2, -256.f), 256.f) * kLn2;
+    dz = gs * eA * (e * r * r);
   }
 }
 

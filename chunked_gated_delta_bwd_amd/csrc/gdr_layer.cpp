@@ -47,9 +47,16 @@ gdr_status check_ws(size_t need, const void* ws, size_t ws_bytes) {
 // gated linear recurrence
 // ---------------------------------------------------------------------------
 
-int64_t tiles_of(int64_t len) { return std::max<int64_t>(1, (len + gdr::kScanTile - 1) / gdr::kScanTile); }
+int64_t tiles_of(int64_t len, int64_t tile) { return std::max<int64_t>(1, (len + tile - 1) / tile); }
 
-// NT_out: tiles over all sequences.
+int scan_gate(const gdr_scan_shape* s) {
+  if (s->gate == GDR_GATE_CHANNEL) return gdr::kScanSoftplus;
+  if (s->gate == GDR_GATE_CHANNEL_SIGMOID) return gdr::kScanSigmoid;
+  return s->D == 1 ? gdr::kScanLog : gdr::kScanHeadLog;
+}
+
+
+// NT_out: backward tiles over all sequences (there are no more forward tiles).
 gdr_status check_scan_shape(const gdr_scan_shape* s, int64_t* NT_out) {
   if (!s) return set_error(GDR_EINVAL, "shape is NULL");
   if (s->gate != GDR_GATE_SCALAR && s->gate != GDR_GATE_CHANNEL && s->gate != GDR_GATE_CHANNEL_SIGMOID)
@@ -62,9 +69,10 @@ gdr_status check_scan_shape(const gdr_scan_shape* s, int64_t* NT_out) {
   if (s->D > 256 || (s->D != 1 && s->D % 8 != 0))
     return set_error(GDR_EUNSUPPORTED, "head dim %d must be 1 or a multiple of 8 up to 256", s->D);
   int64_t NT = 0;
+  const int tile = gdr::bwd_tile(scan_gate(s));
   if (s->cu_seqlens_host == nullptr) {
     if (s->N != s->B) return set_error(GDR_EINVAL, "dense shape needs N == B (N=%d, B=%d)", s->N, s->B);
-    NT = int64_t(s->B) * tiles_of(s->T);
+    NT = int64_t(s->B) * tiles_of(s->T, tile);
   } else {
     if (s->B != 1) return set_error(GDR_EINVAL, "varlen shape needs B == 1");
     if (s->N < 1) return set_error(GDR_EINVAL, "varlen shape needs N >= 1");
@@ -73,7 +81,7 @@ gdr_status check_scan_shape(const gdr_scan_shape* s, int64_t* NT_out) {
     for (int n = 0; n < s->N; ++n) {
       if (cu[n + 1] < cu[n]) return set_error(GDR_EINVAL, "cu_seqlens decreases at %d", n);
       if (cu[n + 1] > s->T) return set_error(GDR_EINVAL, "cu_seqlens[%d] = %lld > T = %d", n + 1, (long long)cu[n + 1], s->T);
-      NT += tiles_of(cu[n + 1] - cu[n]);
+      NT += tiles_of(cu[n + 1] - cu[n], tile);
     }
     if (cu[s->N] != s->T) return set_error(GDR_EINVAL, "cu_seqlens[N] = %lld != T = %d", (long long)cu[s->N], s->T);
   }
@@ -86,7 +94,7 @@ gdr_status check_scan_shape(const gdr_scan_shape* s, int64_t* NT_out) {
 }
 
 struct ScanLayout {
-  size_t tab = 0, counter = 0, words = 0, carry = 0, part = 0, total = 0;
+  size_t tab = 0, counters = 0, words = 0, carry = 0, part = 0, runs = 0, total = 0;
 };
 
 ScanLayout scan_layout(const gdr_scan_shape* s, int64_t NT) {
@@ -95,18 +103,13 @@ ScanLayout scan_layout(const gdr_scan_shape* s, int64_t NT) {
   auto take = [&](size_t bytes) { size_t o = off; off = align256(off + bytes); return o; };
   const size_t C = size_t(s->H) * s->D;
   L.tab = take(s->cu_seqlens_host ? NT * sizeof(gdr::ScanTile) : 0);
-  L.counter = take(4);
-  L.words = take(NT * C * 16);
+  L.counters = take(size_t(gdr::scan_counters(int(C))) * gdr::kScanCounterStep * 4);
+  L.words = take((NT * C + 1) * 8);
   L.carry = take(NT * C * 4);
   L.part = take(s->gate != GDR_GATE_SCALAR ? NT * 2 * C * 4 : 0);
+  L.runs = take(s->gate != GDR_GATE_SCALAR && NT >= gdr::kParamSplitTiles ? gdr::kParamSplit * 2 * C * 8 : 0);
   L.total = off;
   return L;
-}
-
-int scan_gate(const gdr_scan_shape* s) {
-  if (s->gate == GDR_GATE_CHANNEL) return gdr::kScanSoftplus;
-  if (s->gate == GDR_GATE_CHANNEL_SIGMOID) return gdr::kScanSigmoid;
-  return s->D == 1 ? gdr::kScanLog : gdr::kScanHeadLog;
 }
 
 gdr_status check_scan_inputs(const gdr_scan_shape* s, const gdr_scan_inputs* in, bool tokens) {
@@ -119,6 +122,14 @@ gdr_status check_scan_inputs(const gdr_scan_shape* s, const gdr_scan_inputs* in,
   return check_ptrs(a, 5);
 }
 
+int64_t fwd_tiles(const gdr_scan_shape* s) {
+  if (!s->cu_seqlens_host) return int64_t(s->B) * tiles_of(s->T, gdr::fwd_tile(scan_gate(s)));
+  int64_t n = 0;
+  for (int i = 0; i < s->N; ++i) n += tiles_of(s->cu_seqlens_host[i + 1] - s->cu_seqlens_host[i], gdr::fwd_tile(scan_gate(s)));
+  return n;
+}
+
+// NT: the direction's tiles.
 gdr::ScanParams scan_params(const gdr_scan_shape* s, const gdr_scan_inputs* in, int64_t NT, const ScanLayout& L,
                             void* ws) {
   gdr::ScanParams p;
@@ -132,15 +143,16 @@ gdr::ScanParams scan_params(const gdr_scan_shape* s, const gdr_scan_inputs* in, 
   p.tab = reinterpret_cast<gdr::ScanTile*>(w + L.tab);
   // as many tiles as sequences: none waits for another
   p.words = NT > s->N ? reinterpret_cast<uint64_t*>(w + L.words) : nullptr;
-  p.counter = reinterpret_cast<uint32_t*>(w + L.counter);
+  p.counters = reinterpret_cast<uint32_t*>(w + L.counters);
   p.carry = reinterpret_cast<float*>(w + L.carry);
   p.part = reinterpret_cast<float*>(w + L.part);
+  p.runs = NT >= gdr::kParamSplitTiles ? reinterpret_cast<double*>(w + L.runs) : nullptr;
   return p;
 }
 
 // What a call's main kernel finds: the words cleared, and the tile table of a
 // packed problem (sequences by value, kScanBatch a launch).
-gdr_status scan_prologue(const gdr_scan_shape* s, const gdr::ScanParams& p, void* stream) {
+gdr_status scan_prologue(const gdr_scan_shape* s, const gdr::ScanParams& p, int tile, void* stream) {
   if (p.words) {
     const gdr_status st = hip_status(gdr::launch_scan_clear(p, stream), "scan clear kernel");
     if (st != GDR_OK) return st;
@@ -148,7 +160,7 @@ gdr_status scan_prologue(const gdr_scan_shape* s, const gdr::ScanParams& p, void
   if (!s->cu_seqlens_host) return GDR_OK;
   gdr::ScanBatch b;
   std::memset(&b, 0, sizeof(b));
-  int64_t tile = 0;
+  int64_t row = 0, saved = 0;
   for (int n0 = 0; n0 < s->N; n0 += gdr::kScanBatch) {
     b.n = std::min(gdr::kScanBatch, s->N - n0);
     b.seq0 = n0;
@@ -156,10 +168,12 @@ gdr_status scan_prologue(const gdr_scan_shape* s, const gdr::ScanParams& p, void
       const int64_t start = s->cu_seqlens_host[n0 + i], len = s->cu_seqlens_host[n0 + i + 1] - start;
       b.t_start[i] = int32_t(start);
       b.len[i] = int32_t(len);
-      b.tile0[i] = int32_t(tile);
-      tile += tiles_of(len);
+      b.tile0[i] = int32_t(row);
+      b.saved0[i] = int32_t(saved);
+      row += tiles_of(len, tile);
+      saved += tiles_of(len, gdr::bwd_tile(p.gate));
     }
-    const gdr_status st = hip_status(gdr::launch_scan_tables(p, b, stream), "tile table kernel");
+    const gdr_status st = hip_status(gdr::launch_scan_tables(p, tile, b, stream), "tile table kernel");
     if (st != GDR_OK) return st;
   }
   return GDR_OK;
@@ -248,10 +262,10 @@ gdr_status gdr_scan_fwd(const gdr_scan_shape* shape, const gdr_scan_inputs* in, 
   if ((st = check_ptrs(a, 2)) != GDR_OK) return st;
   const ScanLayout L = scan_layout(shape, NT);
   if ((st = check_ws(L.total, ws, ws_bytes)) != GDR_OK) return st;
-  gdr::ScanParams p = scan_params(shape, in, NT, L, ws);
+  gdr::ScanParams p = scan_params(shape, in, fwd_tiles(shape), L, ws);
   p.y = y;
   p.ht = ht;
-  if ((st = scan_prologue(shape, p, stream)) != GDR_OK) return st;
+  if ((st = scan_prologue(shape, p, gdr::fwd_tile(p.gate), stream)) != GDR_OK) return st;
   return hip_status(gdr::launch_scan(p, false, stream), "scan kernel");
 }
 
@@ -275,7 +289,7 @@ gdr_status gdr_scan_bwd(const gdr_scan_shape* shape, const gdr_scan_inputs* in, 
   gdr::ScanParams p = scan_params(shape, in, NT, L, ws);
   p.dy = dy; p.dht = dht;
   p.dx = grads->dx; p.dg = grads->dg; p.dh0 = grads->dh0; p.dA_log = grads->dA_log; p.ddt_bias = grads->ddt_bias;
-  if ((st = scan_prologue(shape, p, stream)) != GDR_OK) return st;
+  if ((st = scan_prologue(shape, p, gdr::bwd_tile(p.gate), stream)) != GDR_OK) return st;
   if ((st = hip_status(gdr::launch_scan(p, true, stream), "scan gradient kernel")) != GDR_OK) return st;
   return par ? hip_status(gdr::launch_scan_params(p, stream), "parameter reduction kernel") : GDR_OK;
 }

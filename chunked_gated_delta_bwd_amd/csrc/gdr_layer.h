@@ -18,27 +18,40 @@ enum ScanGate {
   kScanSigmoid = 3,
 };
 
-constexpr int kScanTile = 64;   // tokens per tile of the recurrence
+// Tokens per tile of the recurrence, backward and forward.
+constexpr int bwd_tile(int gate) { return gate == kScanHeadLog ? 128 : 64; }
+constexpr int fwd_tile(int gate) { return gate == kScanHeadLog ? 256 : 128; }
 
-// One row per tile: at most kScanTile tokens of one sequence.  A sequence without
+// One row per tile: at most a tile's tokens of one sequence.  A sequence without
 // tokens has one empty tile, so that its states are passed through.
 struct ScanTile {
   int32_t t_start, len, seq;
   int32_t idx, after;   // tiles of the sequence before and after it
+  int32_t saved;        // its (first) backward tile: the row of the saved states
 };
 
 // Sequences handed to the table kernel by value, kScanBatch per launch.
 constexpr int kScanBatch = 120;
 struct ScanBatch {
   int32_t n, seq0, pad[2];
-  int32_t t_start[kScanBatch], len[kScanBatch], tile0[kScanBatch];
+  int32_t t_start[kScanBatch], len[kScanBatch], tile0[kScanBatch], saved0[kScanBatch];
 };
 static_assert(sizeof(ScanBatch) <= 2048, "kernel argument size");
+
+// Counters of the tiles taken, one per channel tile and each in a cache line of its
+// own: one counter for all of them bounds a launch (13 ns a workgroup, 210 us for the
+// 16384 tiles of T = 32768 and 4096 channels).
+constexpr int kScanCounterStep = 32;
+inline int scan_counters(int C) { return C / 64 + 1; }   // channel tiles: 64 channels or more each
+
+// Runs in which the backward's per-tile parameter sums are added up, from this many
+// tiles on.
+constexpr int kParamSplit = 16, kParamSplitTiles = 128;
 
 struct ScanParams {
   int32_t H, D, C, N;          // C = H D channels
   int32_t gate, dtype, convex;
-  int32_t NT;                  // tiles over all sequences
+  int32_t NT;                  // this direction's tiles over all sequences
   int32_t dense_T;             // dense: tokens per sequence; -1: the tiles are in `tab`
   float gate_scale;
   const void *x, *g, *dy;
@@ -46,13 +59,14 @@ struct ScanParams {
   void *y, *dx, *dg;
   float *ht, *dh0, *dA_log, *ddt_bias;
   ScanTile* tab;
-  float* carry;                // [NT][C] state at the start of each tile
-  uint64_t* words;             // [NT][2][C] published folds and states; NULL: every sequence is one tile
-  uint32_t* counter;           // tiles taken
+  float* carry;                // [backward tiles][C] state at the start of each
+  uint64_t* words;             // [NT][C] published folds and states; NULL: every sequence is one tile
+  uint32_t* counters;          // tiles taken, per channel tile (kScanCounterStep apart)
   float* part;                 // [NT][2][C] partial sums of ddt_bias and dA_log
+  double* runs;                // [kParamSplit][2][C] sums of runs of tiles; NULL: few tiles
 };
 
-int launch_scan_tables(const ScanParams& p, const ScanBatch& b, void* stream);
+int launch_scan_tables(const ScanParams& p, int TT, const ScanBatch& b, void* stream);
 int launch_scan(const ScanParams& p, bool backward, void* stream);
 int launch_scan_clear(const ScanParams& p, void* stream);
 int launch_scan_params(const ScanParams& p, void* stream);

@@ -1,7 +1,7 @@
 // Gated linear recurrence s_t = a_t s_{t-1} + m_t x_t, forward and backward, and
 // its single-token step.
 //
-// A tile is kScanTile tokens of one sequence by CT channels, a workgroup's work.
+// A tile is fwd_tile or bwd_tile tokens of one sequence by CT channels, a workgroup's work.
 // Its threads are LX lanes across the channels (VEC each, one 16-byte load a
 // token) by LY groups along the tokens; a group's L tokens stay in registers.  The
 // recurrence is affine in the state, so a group folds its tokens into
@@ -16,11 +16,12 @@
 // Between tiles: every tile publishes its fold (A, S) and, once it knows the state
 // it starts from, the state it ends with.  A tile looks back over its predecessors,
 // composing folds, until it meets a published end state; so the inputs cross HBM
-// once and no tile waits for a chain of others to finish.  A value and its tag are
-// one 64-bit word, stored and loaded as one atomic access at device scope, so no
-// fence is needed.  Workgroups take tiles in an order (by a counter) in which a
-// tile's predecessors were taken before it: they are running or done, and publish
-// their folds without waiting for anybody, so every wait ends.  (Waits are
+// once and no tile waits for a chain of others to finish.  What a tile publishes of
+// a channel is one 64-bit word, stored and loaded as one atomic access at device
+// scope, so no fence is needed.  The workgroups of a channel tile take their tiles
+// in an order (by a counter of that channel tile) in which a tile's predecessors
+// were taken before it: they are running or done, and publish their folds without
+// waiting for anybody, so every wait ends.  (Waits are
 // bounded all the same: should the workspace be overwritten by someone else during
 // the call, the states become NaN and the kernel ends.)
 #include <hip/hip_runtime.h>
@@ -34,48 +35,103 @@
 namespace gdr {
 namespace {
 
-constexpr int kTT = kScanTile;
+// Threads of a forward workgroup and of a backward one.
+constexpr int kFwdThreads = 256, kBwdThreads = 256;
 
 // ---- published words ----
-enum : uint32_t { kTagNone = 0, kTagFold = 1, kTagState = 2 };
+// One 64-bit word per tile and channel: the high half is the fold's A, or one of
+// two bit patterns (NaNs that put_fold never writes) that say that nothing is
+// there yet or that the low half is the end state instead of the fold's S.
+constexpr uint32_t kNothing = 0x7fffffffu, kState = 0x7ffffffeu;
 constexpr int kMaxPolls = 1 << 20;
 
-__device__ __forceinline__ void put(uint64_t* w, float v, uint32_t tag) {
-  __hip_atomic_store(w, (uint64_t(tag) << 32) | __float_as_uint(v), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+__device__ __forceinline__ void put(uint64_t* w, uint32_t hi, float lo) {
+  __hip_atomic_store(w, (uint64_t(hi) << 32) | __float_as_uint(lo), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 __device__ __forceinline__ uint64_t get(const uint64_t* w) {
   return __hip_atomic_load(w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-__device__ __forceinline__ uint32_t tag_of(uint64_t w) { return uint32_t(w >> 32); }
-__device__ __forceinline__ float val_of(uint64_t w) { return __uint_as_float(uint32_t(w)); }
+__device__ __forceinline__ void put_fold(uint64_t* w, float A, float S) {
+  put(w, A != A ? 0x7fc00000u : __float_as_uint(A), S);
+}
+__device__ __forceinline__ void put_state(uint64_t* w, float s) { put(w, kState, s); }
+__device__ __forceinline__ uint32_t hi_of(uint64_t w) { return uint32_t(w >> 32); }
+__device__ __forceinline__ float lo_of(uint64_t w) { return __uint_as_float(uint32_t(w)); }
 
-// The state that reaches a tile of one channel from the tiles `step` rows apart
-// before it (`w` addresses the nearest one's words: A at w, S at w + C), `count` of
-// them up to the sequence's first, which always publishes a state.
-__device__ __forceinline__ float look_back(const uint64_t* w, int64_t step, int C, int count) {
-  constexpr int kAhead = 4;   // predecessors whose words are loaded at a time
+// Folds W words of the `count` (at least one) before a tile (after it, in the
+// backward): from the k0-th nearest on.  w (the same for the whole workgroup) is the
+// nearest tile's row, each next row is `step` words on.  The farthest of the `count`
+// always publishes a state, and words past it stand for it.  With a state among the W
+// words S is the state that reaches the k0-th tile's far end and true is returned;
+// else (A, S) is their fold.  All words are loaded at once and again until all are
+// there (the nearest is the last to come): the states' front advances by up to W
+// tiles, over all threads of a channel, per trip to memory.
+template <int W>
+__device__ __forceinline__ bool fold_words(const uint64_t* w, int64_t step, int count, int k0, int c, float& A, float& S) {
+  uint64_t x[W];
+  for (int polls = 0;; ++polls) {
+    // one word a poll: polling all W of them slows the stores that are waited for
+    if (hi_of(get(w + step * k0 + c)) != kNothing) {
+      bool ready = true;
+#pragma unroll
+      for (int i = 0; i < W; ++i) x[i] = get(w + step * min(k0 + i, count - 1) + c);
+#pragma unroll
+      for (int i = 0; i < W; ++i) ready &= hi_of(x[i]) != kNothing;
+      if (ready) break;
+    }
+    if (polls > kMaxPolls) {
+      S = __builtin_nanf("");
+      return true;
+    }
+    __builtin_amdgcn_s_sleep(4);
+  }
+  A = 1.f;
+  S = 0.f;
+  bool done = false;
+#pragma unroll
+  for (int i = W - 1; i >= 0; --i) {
+    const bool state = hi_of(x[i]) == kState;
+    const float a = __uint_as_float(hi_of(x[i]));
+    S = state ? lo_of(x[i]) : fmaf(a, S, lo_of(x[i]));
+    A *= a;
+    done |= state;
+  }
+  return done;
+}
+
+constexpr int kWindow = 4;   // words a thread loads at a time
+
+// The state that reaches a tile's channel c, known to its thread of part 0.  The
+// PARTS threads of the channel fold a window of words each, the nearest part 0's;
+// beyond their windows part 0 goes on alone.  Every thread of the workgroup calls
+// this; `on`: the channel exists; pA, pS hold a float per thread.
+template <int CT, int PARTS>
+__device__ __forceinline__ float look_back(const uint64_t* w, int64_t step, int count, int c, bool on, int part,
+                                           float* pA, float* pS) {
   float A = 1.f, S = 0.f;
-  int polls = 0;
-  for (int k = 0; k < count; k += kAhead) {
-    uint64_t wa[kAhead], ws[kAhead];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int64_t o = -step * min(k + i, count - 1);
-      ws[i] = get(w + o + C);
-      wa[i] = get(w + o);
+  bool done = false;
+  if (on && part * kWindow < count) done = fold_words<kWindow>(w, step, count, part * kWindow, c, A, S);
+  if constexpr (PARTS > 1) {
+    if (part > 0) {
+      pA[part * CT + c] = done ? __uint_as_float(kState) : A;
+      pS[part * CT + c] = S;
     }
+    __syncthreads();
+  }
+  if (part > 0 || !on) return 0.f;
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int64_t o = -step * min(k + i, count - 1);
-      while (tag_of(ws[i]) == kTagNone || (tag_of(ws[i]) == kTagFold && tag_of(wa[i]) == kTagNone)) {
-        if (++polls > kMaxPolls) return __builtin_nanf("");
-        ws[i] = get(w + o + C);
-        wa[i] = get(w + o);
-      }
-      S += A * val_of(ws[i]);
-      if (tag_of(ws[i]) == kTagState) return S;
-      A *= val_of(wa[i]);
-    }
+  for (int i = 1; i < PARTS; ++i) {
+    if (done) break;
+    S = fmaf(A, pS[i * CT + c], S);
+    const float Ai = pA[i * CT + c];
+    done = __float_as_uint(Ai) == kState;
+    A *= Ai;
+  }
+  for (int k = PARTS * kWindow; !done && k < count; k += kWindow) {
+    float Ak, Sk;
+    done = fold_words<kWindow>(w, step, count, k, c, Ak, Sk);
+    S = fmaf(A, Sk, S);
+    A *= Ak;
   }
   return S;
 }
@@ -106,11 +162,13 @@ struct Vec<TIO, 1> {
 };
 
 // Geometry of a variant.
-template <int VEC, int LX>
+template <int VEC, int LX, int TH, int TT>
 struct Geo {
-  static constexpr int LY = 256 / LX;
-  static constexpr int L = kTT / LY;      // tokens per thread
+  static constexpr int LY = TH / LX;
+  static constexpr int L = TT / LY;       // tokens per thread
   static constexpr int CT = LX * VEC;     // channels per tile
+  static constexpr int PARTS = TH / CT;   // threads per channel
+  static_assert(PARTS >= 1 && L >= 1, "tile geometry");
 };
 
 // Channels a tile advances by: CT, or with one gate per head the whole heads that
@@ -120,25 +178,28 @@ __host__ __device__ __forceinline__ int tile_channels(int CT, int D) {
   return GM == kScanHeadLog ? CT / D * D : CT;
 }
 
-// The place of a tile (its row of the published words and of the saved states) in
-// the order in which the workgroups take them, and the tile.
+// The place of a tile (its row of the published words) in the order in which the
+// workgroups take them, and the tile.  SAVED: tokens of a backward tile.
+template <int TT, int SAVED>
 __device__ __forceinline__ ScanTile tile_at(const ScanParams& p, int order, bool backward, int& row) {
   if (p.dense_T < 0) {
     row = backward ? p.NT - 1 - order : order;
     return p.tab[row];
   }
   // all sequences' first tiles, then all second ones, ...
-  const int per = max(1, (p.dense_T + kTT - 1) / kTT);
+  const int per = max(1, (p.dense_T + TT - 1) / TT);
   const int level = order / p.N, seq = order - level * p.N, idx = backward ? per - 1 - level : level;
   row = seq * per + idx;
-  return ScanTile{seq * p.dense_T + idx * kTT, min(kTT, p.dense_T - idx * kTT), seq, idx, per - 1 - idx};
+  const int saved = max(1, (p.dense_T + SAVED - 1) / SAVED);
+  return ScanTile{seq * p.dense_T + idx * TT, min(TT, p.dense_T - idx * TT), seq, idx, per - 1 - idx,
+                  seq * saved + idx * (TT / SAVED)};
 }
 
-// The workgroup's place in the order: its number where no tile waits for another,
-// else the next of the counter.
-__device__ __forceinline__ int take_order(const ScanParams& p, int* slot) {
-  if (!p.words) return blockIdx.x;
-  if (threadIdx.x == 0) *slot = int(atomicAdd(p.counter, 1u));
+// The workgroup's place in the order of its channels' tiles: its number where no
+// tile waits for another, else the next of the channel tile's counter.
+__device__ __forceinline__ int take_order(const ScanParams& p, int ct, int nct, int* slot) {
+  if (!p.words) return blockIdx.x / nct;
+  if (threadIdx.x == 0) *slot = int(atomicAdd(p.counters + int64_t(ct) * kScanCounterStep, 1u));
   __syncthreads();
   return *slot;
 }
@@ -184,28 +245,37 @@ struct GateRaw<TIO, VEC, kScanHeadLog> {
   }
 };
 
-// Tokens and channels of a thread, with the loads kept in bounds: rows past the
-// tile's end and lanes past its channels load a valid neighbour's values, which
-// are then left out (a = 1, no input).
-template <typename TIO, int VEC, int LX, int GM>
-__global__ __launch_bounds__(256) void k_scan_fwd(const ScanParams p) {
-  typedef Geo<VEC, LX> G;
+// Both kernels keep their loads in bounds without branches: rows past the tile's
+// end and lanes past its channels load a valid neighbour's values, and the rows past
+// the end are then made neutral (a = 1, no input), in a loop of its own that full
+// tiles skip.
+template <typename TIO, int VEC, int LX, int GM, bool CONVEX>
+__global__ __launch_bounds__(kFwdThreads) void k_scan_fwd(const ScanParams p) {
+  constexpr int TT = fwd_tile(GM);
+  typedef Geo<VEC, LX, kFwdThreads, TT> G;
   typedef Vec<TIO, VEC> V;
   typedef GateRaw<TIO, VEC, GM> GR;
   constexpr int L = G::L, LY = G::LY, CT = G::CT;
-  __shared__ float sA[LY][CT], sS[LY][CT];
+  __shared__ float sA[LY][CT], sS[LY][CT], pA[kFwdThreads], pS[kFwdThreads];
   __shared__ int slot;
-  const int order = take_order(p, &slot);
   const int tid = threadIdx.x, lx = tid % LX, ly = tid / LX;
   const int cstep = tile_channels<GM>(CT, p.D);
-  const int nct = (p.C + cstep - 1) / cstep;
-  const int cbase = order % nct * cstep, nc = min(p.C - cbase, cstep);
+  const int nct = (p.C + cstep - 1) / cstep, ct = blockIdx.x % nct;
+  const int cbase = ct * cstep, nc = min(p.C - cbase, cstep);
   int row;
-  const ScanTile tile = tile_at(p, order / nct, false, row);
+  const ScanTile tile = tile_at<TT, bwd_tile(GM)>(p, take_order(p, ct, nct, &slot), false, row);
+  const int c = tid % CT, part = tid / CT;   // the channel this thread composes, and its share
+  const bool lead = part == 0 && c < nc;
+  const int64_t sc = int64_t(tile.seq) * p.C + cbase + c;
+  if (tile.len == 0) {
+    // a sequence without tokens: its state passes through
+    if (lead && p.ht) p.ht[sc] = p.h0 ? p.h0[sc] : 0.f;
+    return;
+  }
   const bool on = lx * VEC < nc;
   const int c0 = cbase + (on ? lx * VEC : 0);
   float a[L][VEC], u[L][VEC];
-  if (tile.len > 0) {
+  {
     typename GR::Raw rg[L];
     typename V::Raw rx[L];
 #pragma unroll
@@ -218,149 +288,28 @@ __global__ __launch_bounds__(256) void k_scan_fwd(const ScanParams p) {
     gate.init(p, c0);
 #pragma unroll
     for (int i = 0; i < L; ++i) {
-      float g[VEC], x[VEC];
+      float g[VEC];
       GR::unpack(rg[i], g);
-      V::unpack(rx[i], x);
-      const bool live = ly * L + i < tile.len;
+      V::unpack(rx[i], u[i]);
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
         const float l = gate.log2_decay(g[v], v, p.gate_scale);
-        const float d = fast_exp2(l);
-        const float w = p.convex ? one_minus_exp2(l, d) * x[v] : x[v];
-        a[i][v] = live ? d : 1.f;
-        u[i][v] = live ? w : 0.f;
+        a[i][v] = fast_exp2(l);
+        if constexpr (CONVEX) u[i][v] *= one_minus_exp2(l, a[i][v]);
       }
     }
-  } else {
+  }
+  if (tile.len < TT) {
 #pragma unroll
     for (int i = 0; i < L; ++i)
+      if (ly * L + i >= tile.len)
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) { a[i][v] = 1.f; u[i][v] = 0.f; }
-  }
-  float A[VEC], S[VEC];
-#pragma unroll
-  for (int v = 0; v < VEC; ++v) { A[v] = a[0][v]; S[v] = u[0][v]; }
-#pragma unroll
-  for (int i = 1; i < L; ++i)
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-      S[v] = fmaf(a[i][v], S[v], u[i][v]);
-      A[v] *= a[i][v];
-    }
-#pragma unroll
-  for (int v = 0; v < VEC; ++v) { sA[ly][lx * VEC + v] = A[v]; sS[ly][lx * VEC + v] = S[v]; }
-  __syncthreads();
-  for (int c = tid; c < nc; c += 256) {
-    uint64_t* w = p.words + int64_t(row) * 2 * p.C + cbase + c;
-    float s;
-    if (tile.idx == 0) {
-      s = p.h0 ? p.h0[int64_t(tile.seq) * p.C + cbase + c] : 0.f;
-    } else {
-      float At = 1.f, St = 0.f;
-#pragma unroll
-      for (int y = 0; y < LY; ++y) {
-        St = fmaf(sA[y][c], St, sS[y][c]);
-        At *= sA[y][c];
-      }
-      if (tile.after > 0) {
-        put(w, At, kTagFold);
-        put(w + p.C, St, kTagFold);
-      }
-      s = look_back(w - 2 * int64_t(p.C), 2 * int64_t(p.C), p.C, tile.idx);
-    }
-    p.carry[int64_t(row) * p.C + cbase + c] = s;
-#pragma unroll
-    for (int y = 0; y < LY; ++y) {
-      const float Sy = sS[y][c];
-      sS[y][c] = s;
-      s = fmaf(sA[y][c], s, Sy);
-    }
-    if (tile.after > 0) put(w + p.C, s, kTagState);
-    else if (p.ht) p.ht[int64_t(tile.seq) * p.C + cbase + c] = s;
-  }
-  __syncthreads();
-  float s[VEC];
-#pragma unroll
-  for (int v = 0; v < VEC; ++v) s[v] = sS[ly][lx * VEC + v];
-#pragma unroll
-  for (int i = 0; i < L; ++i) {
-    const int r = ly * L + i;
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) s[v] = fmaf(a[i][v], s[v], u[i][v]);
-    if (on && r < tile.len) V::store(p.y, (int64_t(tile.t_start) + r) * p.C + c0, s);
-  }
-}
-
-template <typename TIO, int VEC, int LX, int GM>
-__global__ __launch_bounds__(256) void k_scan_bwd(const ScanParams p) {
-  typedef Geo<VEC, LX> G;
-  typedef Vec<TIO, VEC> V;
-  typedef GateRaw<TIO, VEC, GM> GR;
-  constexpr int L = G::L, LY = G::LY, CT = G::CT;
-  constexpr bool kPar = GM == kScanSoftplus || GM == kScanSigmoid;
-  __shared__ float sA[LY][CT], sS[LY][CT], sE[LY][CT];
-  __shared__ float sG[GM == kScanHeadLog ? kTT : 1][LX + 1];
-  __shared__ int slot;
-  const int order = take_order(p, &slot);
-  const int tid = threadIdx.x, lx = tid % LX, ly = tid / LX;
-  const int cstep = tile_channels<GM>(CT, p.D);
-  const int nct = (p.C + cstep - 1) / cstep;
-  const int cbase = order % nct * cstep, nc = min(p.C - cbase, cstep);
-  int row;
-  const ScanTile tile = tile_at(p, order / nct, true, row);
-  const bool on = lx * VEC < nc;
-  const int c0 = cbase + (on ? lx * VEC : 0);
-  // per token: the decay, its base-2 logarithm, the gate's slopes (per-channel
-  // gates), the input; `u` becomes the state before the token
-  float a[L][VEC], l[L][VEC], dz[kPar ? L : 1][VEC], dA[kPar ? L : 1][VEC], u[L][VEC];
-  typename V::Raw rx[L], rdy[L];
-  if (tile.len > 0) {
-    typename GR::Raw rg[L];
-#pragma unroll
-    for (int i = 0; i < L; ++i) {
-      const int64_t t = int64_t(tile.t_start) + min(ly * L + i, tile.len - 1);
-      rg[i] = GR::load(p, t, c0);
-      rx[i] = V::load(p.x, t * p.C + c0);
-      rdy[i] = V::load(p.dy, t * p.C + c0);
-    }
-    Gate<VEC, GM> gate;
-    gate.init(p, c0);
-#pragma unroll
-    for (int i = 0; i < L; ++i) {
-      float g[VEC], x[VEC];
-      GR::unpack(rg[i], g);
-      V::unpack(rx[i], x);
-      const bool live = ly * L + i < tile.len;
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        float l2;
-        if constexpr (kPar) {
-          gate_log2_grad<GM == kScanSoftplus ? 0 : 1>(fmaf(g[v], kLog2e, gate.bias[v]), gate.eA[v], p.gate_scale, l2,
-                                                       dz[i][v], dA[i][v]);
-        } else {
-          l2 = g[v] * kLog2e;
-        }
-        const float d = fast_exp2(l2);
-        const float w = p.convex ? one_minus_exp2(l2, d) * x[v] : x[v];
-        l[i][v] = l2;
-        a[i][v] = live ? d : 1.f;
-        u[i][v] = live ? w : 0.f;
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < L; ++i)
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        a[i][v] = 1.f;
-        u[i][v] = l[i][v] = 0.f;
-        if constexpr (kPar) dz[i][v] = dA[i][v] = 0.f;
-      }
+        for (int v = 0; v < VEC; ++v) { a[i][v] = 1.f; u[i][v] = 0.f; }
   }
   {
-    float A[VEC], S[VEC], E[VEC];
+    float A[VEC], S[VEC];
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) { A[v] = a[0][v]; S[v] = u[0][v]; E[v] = 0.f; }
+    for (int v = 0; v < VEC; ++v) { A[v] = a[0][v]; S[v] = u[0][v]; }
 #pragma unroll
     for (int i = 1; i < L; ++i)
 #pragma unroll
@@ -368,15 +317,145 @@ __global__ __launch_bounds__(256) void k_scan_bwd(const ScanParams p) {
         S[v] = fmaf(a[i][v], S[v], u[i][v]);
         A[v] *= a[i][v];
       }
-    if (tile.len > 0) {
 #pragma unroll
-      for (int i = L - 1; i >= 0; --i) {
-        float dy[VEC];
-        V::unpack(rdy[i], dy);
-        const bool live = ly * L + i < tile.len;
+    for (int v = 0; v < VEC; ++v) { sA[ly][lx * VEC + v] = A[v]; sS[ly][lx * VEC + v] = S[v]; }
+  }
+  __syncthreads();
+  // one thread per channel composes the groups; the other threads of the channel
+  // (PARTS in all) share the look back
+  uint64_t* w = p.words + int64_t(row) * p.C + cbase;
+  if (lead && tile.idx > 0 && tile.after > 0) {
+    float At = 1.f, St = 0.f;
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) E[v] = a[i][v] * ((live ? dy[v] : 0.f) + E[v]);
+    for (int y = 0; y < LY; ++y) {
+      St = fmaf(sA[y][c], St, sS[y][c]);
+      At *= sA[y][c];
+    }
+    put_fold(w + c, At, St);
+  }
+  float s = 0.f;
+  if (tile.idx == 0) {
+    if (p.h0 && lead) s = p.h0[sc];
+  } else {
+    s = look_back<CT, G::PARTS>(w - p.C, -int64_t(p.C), tile.idx, c, c < nc, part, pA, pS);
+  }
+  if (lead) {
+    float* saved = p.carry + int64_t(tile.saved) * p.C + cbase + c;
+#pragma unroll
+    for (int y = 0; y < LY; ++y) {
+      constexpr int kPer = bwd_tile(GM) / L;   // groups per backward tile
+      static_assert(kPer * L == bwd_tile(GM) && TT % bwd_tile(GM) == 0, "saved states at group borders");
+      if (y % kPer == 0 && y * L < tile.len) saved[int64_t(y / kPer) * p.C] = s;
+      const float Sy = sS[y][c];
+      sS[y][c] = s;
+      s = fmaf(sA[y][c], s, Sy);
+    }
+    if (tile.after > 0) put_state(w + c, s);
+    else if (p.ht) p.ht[sc] = s;
+  }
+  __syncthreads();
+  float y[VEC];
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) y[v] = sS[ly][lx * VEC + v];
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    const int r = ly * L + i;
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) y[v] = fmaf(a[i][v], y[v], u[i][v]);
+    if (on && r < tile.len) V::store(p.y, (int64_t(tile.t_start) + r) * p.C + c0, y);
+  }
+}
+
+template <typename TIO, int VEC, int LX, int GM, bool CONVEX>
+__global__ __launch_bounds__(kBwdThreads, 2) void k_scan_bwd(const ScanParams p) {
+  constexpr int TT = bwd_tile(GM);
+  typedef Geo<VEC, LX, kBwdThreads, TT> G;
+  typedef Vec<TIO, VEC> V;
+  typedef GateRaw<TIO, VEC, GM> GR;
+  constexpr int L = G::L, LY = G::LY, CT = G::CT;
+  constexpr bool kPar = GM == kScanSoftplus || GM == kScanSigmoid;
+  constexpr bool kLog = GM == kScanSoftplus || CONVEX;   // the logarithm is needed again
+  __shared__ float sA[LY][CT], sS[LY][CT], sE[LY][CT], pA[kBwdThreads], pS[kBwdThreads];
+  __shared__ float sG[GM == kScanHeadLog ? TT : 1][LX + 1];
+  __shared__ int slot;
+  const int tid = threadIdx.x, lx = tid % LX, ly = tid / LX;
+  const int cstep = tile_channels<GM>(CT, p.D);
+  const int nct = (p.C + cstep - 1) / cstep, ct = blockIdx.x % nct;
+  const int cbase = ct * cstep, nc = min(p.C - cbase, cstep);
+  int row;
+  const ScanTile tile = tile_at<TT, TT>(p, take_order(p, ct, nct, &slot), true, row);
+  const int c = tid % CT, part = tid / CT;
+  const bool lead = part == 0 && c < nc;
+  const int64_t sc = int64_t(tile.seq) * p.C + cbase + c;
+  float* partial = p.part + int64_t(row) * 2 * p.C + cbase + c;
+  if (tile.len == 0) {
+    if (lead && p.dh0) p.dh0[sc] = p.dht ? p.dht[sc] : 0.f;
+    if (kPar && lead) partial[0] = partial[p.C] = 0.f;
+    return;
+  }
+  const bool on = lx * VEC < nc;
+  const int c0 = cbase + (on ? lx * VEC : 0);
+  // per token: the decay, its base-2 logarithm, the gate's slope, the input; `u`
+  // becomes the state before the token
+  float a[L][VEC], l[kLog ? L : 1][VEC], dz[kPar ? L : 1][VEC], u[L][VEC];
+  typename GR::Raw rg[L];
+  typename V::Raw rx[L], rdy[L];
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    const int64_t t = int64_t(tile.t_start) + min(ly * L + i, tile.len - 1);
+    rg[i] = GR::load(p, t, c0);
+    rx[i] = V::load(p.x, t * p.C + c0);
+    rdy[i] = V::load(p.dy, t * p.C + c0);
+  }
+  Gate<VEC, GM> gate;
+  gate.init(p, c0);
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    float g[VEC];
+    GR::unpack(rg[i], g);
+    V::unpack(rx[i], u[i]);
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+      float l2;
+      if constexpr (kPar)
+        gate_log2_grad<GM == kScanSoftplus ? 0 : 1>(fmaf(g[v], kLog2e, gate.bias[v]), gate.eA[v], p.gate_scale, l2,
+                                                     dz[i][v]);
+      else l2 = g[v] * kLog2e;
+      a[i][v] = fast_exp2(l2);
+      if constexpr (kLog) l[i][v] = l2;
+      if constexpr (CONVEX) u[i][v] *= one_minus_exp2(l2, a[i][v]);
+    }
+  }
+  if (tile.len < TT) {
+#pragma unroll
+    for (int i = 0; i < L; ++i)
+      if (ly * L + i >= tile.len) {
+        rdy[i] = {};
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+          a[i][v] = 1.f;
+          u[i][v] = 0.f;
+          if constexpr (kPar) dz[i][v] = 0.f;
+        }
       }
+  }
+  {
+    float A[VEC], S[VEC], E[VEC], dy[VEC];
+    V::unpack(rdy[L - 1], dy);
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) { A[v] = a[0][v]; S[v] = u[0][v]; E[v] = a[L - 1][v] * dy[v]; }
+#pragma unroll
+    for (int i = 1; i < L; ++i)
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        S[v] = fmaf(a[i][v], S[v], u[i][v]);
+        A[v] *= a[i][v];
+      }
+#pragma unroll
+    for (int i = L - 2; i >= 0; --i) {
+      V::unpack(rdy[i], dy);
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) E[v] = a[i][v] * (dy[v] + E[v]);
     }
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
@@ -386,37 +465,39 @@ __global__ __launch_bounds__(256) void k_scan_bwd(const ScanParams p) {
     }
   }
   __syncthreads();
-  for (int c = tid; c < nc; c += 256) {
-    uint64_t* w = p.words + int64_t(row) * 2 * p.C + cbase + c;
-    float s = p.carry[int64_t(row) * p.C + cbase + c], e;
-    if (tile.after == 0) {
-      e = p.dht ? p.dht[int64_t(tile.seq) * p.C + cbase + c] : 0.f;
-    } else {
+  uint64_t* w = p.words + int64_t(row) * p.C + cbase;
+  float s0 = 0.f, e0 = 0.f;
+  if (lead) {
+    s0 = p.carry[int64_t(tile.saved) * p.C + cbase + c];
+    if (tile.idx > 0 && tile.after > 0) {
       float At = 1.f, Et = 0.f;
 #pragma unroll
       for (int y = LY - 1; y >= 0; --y) {
         Et = fmaf(sA[y][c], Et, sE[y][c]);
         At *= sA[y][c];
       }
-      if (tile.idx > 0) {
-        put(w, At, kTagFold);
-        put(w + p.C, Et, kTagFold);
-      }
-      e = look_back(w + 2 * int64_t(p.C), -2 * int64_t(p.C), p.C, tile.after);
+      put_fold(w + c, At, Et);
     }
+  }
+  if (tile.after == 0) {
+    if (p.dht && lead) e0 = p.dht[sc];
+  } else {
+    e0 = look_back<CT, G::PARTS>(w + p.C, p.C, tile.after, c, c < nc, part, pA, pS);
+  }
+  if (lead) {
 #pragma unroll
     for (int y = LY - 1; y >= 0; --y) {
       const float Ey = sE[y][c];
-      sE[y][c] = e;
-      e = fmaf(sA[y][c], e, Ey);
+      sE[y][c] = e0;
+      e0 = fmaf(sA[y][c], e0, Ey);
     }
-    if (tile.idx > 0) put(w + p.C, e, kTagState);
-    else if (p.dh0) p.dh0[int64_t(tile.seq) * p.C + cbase + c] = e;
+    if (tile.idx > 0) put_state(w + c, e0);
+    else if (p.dh0) p.dh0[sc] = e0;
 #pragma unroll
     for (int y = 0; y < LY; ++y) {
       const float Sy = sS[y][c];
-      sS[y][c] = s;
-      s = fmaf(sA[y][c], s, Sy);
+      sS[y][c] = s0;
+      s0 = fmaf(sA[y][c], s0, Sy);
     }
   }
   __syncthreads();
@@ -438,42 +519,53 @@ __global__ __launch_bounds__(256) void k_scan_bwd(const ScanParams p) {
         s[v] = n;
       }
   }
-  if (tile.len > 0) {
 #pragma unroll
-    for (int i = L - 1; i >= 0; --i) {
-      const int r = ly * L + i;
-      const bool live = r < tile.len;
-      float dx[VEC], dg[VEC], x[VEC], dy[VEC];
-      V::unpack(rx[i], x);
-      V::unpack(rdy[i], dy);
-      float dsum = 0.f;
+  for (int i = L - 1; i >= 0; --i) {
+    const int r = ly * L + i;
+    float dx[VEC], dg[VEC], x[VEC], dy[VEC], g[VEC];
+    V::unpack(rdy[i], dy);
+    if constexpr (CONVEX) V::unpack(rx[i], x);
+    if constexpr (GM == kScanSigmoid) GR::unpack(rg[i], g);
+    float dsum = 0.f;
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        const float ds = (live ? dy[v] : 0.f) + e[v];
-        e[v] = a[i][v] * ds;
-        const float dl = live ? e[v] * (p.convex ? u[i][v] - x[v] : u[i][v]) : 0.f;
-        dx[v] = p.convex ? one_minus_exp2(l[i][v], a[i][v]) * ds : ds;
-        if constexpr (kPar) {
-          dg[v] = dl * dz[i][v];
-          sumz[v] += dg[v];
-          sumA[v] = fmaf(dl, dA[i][v], sumA[v]);
+    for (int v = 0; v < VEC; ++v) {
+      const float ds = dy[v] + e[v];
+      e[v] = a[i][v] * ds;
+      float dl;
+      if constexpr (CONVEX) {
+        dl = e[v] * (u[i][v] - x[v]);
+        dx[v] = one_minus_exp2(l[i][v], a[i][v]) * ds;
+      } else {
+        dl = e[v] * u[i][v];
+        dx[v] = ds;
+      }
+      if constexpr (kPar) {
+        dg[v] = dl * dz[i][v];
+        // d lambda / d A_log: lambda, or the slope by z times z; rows past the end
+        // have a slope of zero, and a lambda to be left out
+        if constexpr (GM == kScanSoftplus) {
+          const float lam = fmaxf(l[i][v], -3.0e38f);
+          sumA[v] = fmaf(r < tile.len ? dl : 0.f, lam, sumA[v]);
         } else {
-          dg[v] = dl;
-          dsum += dl;
+          sumA[v] = fmaf(dg[v], fminf(fmaxf(fmaf(g[v], kLog2e, gate.bias[v]), -3.0e38f), 3.0e38f), sumA[v]);
         }
+        sumz[v] += dg[v];
+      } else {
+        dg[v] = dl;
+        dsum += dl;
       }
-      if (on && live) {
-        const int64_t t = int64_t(tile.t_start) + r;
-        V::store(p.dx, t * p.C + c0, dx);
-        if constexpr (GM != kScanHeadLog) V::store(p.dg, t * p.C + c0, dg);
-      }
-      if constexpr (GM == kScanHeadLog) sG[r][lx] = dsum;
     }
+    if (on && r < tile.len) {
+      const int64_t t = int64_t(tile.t_start) + r;
+      V::store(p.dx, t * p.C + c0, dx);
+      if constexpr (GM != kScanHeadLog) V::store(p.dg, t * p.C + c0, dg);
+    }
+    if constexpr (GM == kScanHeadLog) sG[r][lx] = dsum;
   }
   if constexpr (GM == kScanHeadLog) {
     __syncthreads();
     const int heads = nc / p.D, lanes = p.D / VEC, h0 = cbase / p.D;
-    for (int i = tid; i < tile.len * heads; i += 256) {
+    for (int i = tid; i < tile.len * heads; i += kBwdThreads) {
       const int r = i / heads, h = i - r * heads;
       float d = 0.f;
       for (int m = 0; m < lanes; ++m) d += sG[r][h * lanes + m];
@@ -485,33 +577,59 @@ __global__ __launch_bounds__(256) void k_scan_bwd(const ScanParams p) {
 #pragma unroll
     for (int v = 0; v < VEC; ++v) { sS[ly][lx * VEC + v] = sumz[v]; sE[ly][lx * VEC + v] = sumA[v]; }
     __syncthreads();
-    for (int c = tid; c < nc; c += 256) {
+    if (lead) {
       float z = 0.f, zA = 0.f;
 #pragma unroll
       for (int y = 0; y < LY; ++y) { z += sS[y][c]; zA += sE[y][c]; }
-      float* q = p.part + int64_t(row) * 2 * p.C + cbase + c;
-      q[0] = z;
-      q[p.C] = zA;
+      partial[0] = z;
+      partial[p.C] = zA * 0.6931471805599453f;   // lambda and z are in base-2 units
     }
   }
 }
 
-// ddt_bias and dA_log from the tiles' partial sums: a workgroup per head (several
-// narrow ones), its threads a row group each of the tiles; 64-bit sums in a fixed
-// order.
+// ddt_bias and dA_log from the tiles' partial sums, in 64 bits and a fixed order.
+// Many tiles are first summed in kParamSplit runs (64 channels a workgroup), so
+// that the whole chip reads them: 8 us for 512 tiles of 2048 channels, 14 us with a
+// workgroup per head alone.
+__global__ __launch_bounds__(256) void k_scan_param_runs(const ScanParams p) {
+  __shared__ double sz[256], sa[256];
+  const int tid = threadIdx.x, c = blockIdx.x * 64 + (tid & 63), g = tid >> 6;
+  const int r0 = int(int64_t(p.NT) * blockIdx.y / kParamSplit), r1 = int(int64_t(p.NT) * (blockIdx.y + 1) / kParamSplit);
+  double z = 0.0, zA = 0.0;
+  if (c < p.C) {
+#pragma unroll 8
+    for (int i = r0 + g; i < r1; i += 4) {
+      const float* q = p.part + int64_t(i) * 2 * p.C + c;
+      z += q[0];
+      zA += q[p.C];
+    }
+  }
+  sz[tid] = z;
+  sa[tid] = zA;
+  __syncthreads();
+  if (g == 0 && c < p.C) {
+    double* q = p.runs + int64_t(blockIdx.y) * 2 * p.C + c;
+    q[0] = sz[tid] + sz[tid + 64] + sz[tid + 128] + sz[tid + 192];
+    q[p.C] = sa[tid] + sa[tid + 64] + sa[tid + 128] + sa[tid + 192];
+  }
+}
+
+// A workgroup per head (several narrow ones), its threads a row group each of the
+// tiles or of their runs.
 constexpr int kParamThreads = 1024;
 __host__ __device__ __forceinline__ int param_heads(int D) { return D >= 64 ? 1 : 64 / D; }
 
-__global__ __launch_bounds__(kParamThreads) void k_scan_params(const ScanParams p) {
+template <typename T>
+__global__ __launch_bounds__(kParamThreads) void k_scan_params(const ScanParams p, const T* rows, int n) {
   __shared__ double sz[kParamThreads], sa[kParamThreads];
   const int h0 = blockIdx.x * param_heads(p.D), heads = min(param_heads(p.D), p.H - h0);
   const int cw = heads * p.D, groups = kParamThreads / cw;
   const int tid = threadIdx.x, c = tid % cw, g = tid / cw;
   double z = 0.0, zA = 0.0;
   if (g < groups) {
-    const float* q = p.part + int64_t(h0) * p.D + c;
+    const T* q = rows + int64_t(h0) * p.D + c;
 #pragma unroll 8
-    for (int i = g; i < p.NT; i += groups) {
+    for (int i = g; i < n; i += groups) {
       z += q[int64_t(i) * 2 * p.C];
       zA += q[int64_t(i) * 2 * p.C + p.C];
     }
@@ -532,19 +650,22 @@ __global__ __launch_bounds__(kParamThreads) void k_scan_params(const ScanParams 
   }
 }
 
-// The tile rows of up to kScanBatch sequences.
-__global__ __launch_bounds__(64) void k_scan_tables(ScanTile* tab, const ScanBatch b) {
+// The tile rows of up to kScanBatch sequences, TT tokens a tile.
+__global__ __launch_bounds__(64) void k_scan_tables(ScanTile* tab, int TT, int saved, const ScanBatch b) {
   const int i = blockIdx.x;
-  const int len = b.len[i], tiles = max(1, (len + kTT - 1) / kTT);
+  const int len = b.len[i], tiles = max(1, (len + TT - 1) / TT);
   for (int j = threadIdx.x; j < tiles; j += 64)
-    tab[b.tile0[i] + j] = ScanTile{b.t_start[i] + j * kTT, min(kTT, len - j * kTT), b.seq0 + i, j, tiles - 1 - j};
+    tab[b.tile0[i] + j] = ScanTile{b.t_start[i] + j * TT, min(TT, len - j * TT), b.seq0 + i, j, tiles - 1 - j,
+                                   b.saved0[i] + j * (TT / saved)};
 }
 
-// Clears the counter and the published words' tags.
-__global__ __launch_bounds__(256) void k_scan_clear(uint32_t* counter, uint4* words, int64_t n) {
-  if (blockIdx.x == 0 && threadIdx.x == 0) *counter = 0;
-  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256)
-    words[i] = make_uint4(0, 0, 0, 0);
+// Clears the counters and marks the words as not published.
+__global__ __launch_bounds__(256) void k_scan_clear(uint32_t* counters, int nc, uint64_t* words, int64_t n) {
+  const int64_t t = int64_t(blockIdx.x) * 256 + threadIdx.x, all = int64_t(gridDim.x) * 256;
+  for (int64_t i = t; i < nc; i += all) counters[i * kScanCounterStep] = 0;
+  ulonglong2* w = reinterpret_cast<ulonglong2*>(words);
+  constexpr uint64_t kNo = uint64_t(kNothing) << 32;
+  for (int64_t i = t; 2 * i < n; i += all) w[i] = ulonglong2{kNo, kNo};
 }
 
 // One token a row: a workgroup takes 256 VEC channels of one row, and where later
@@ -597,13 +718,19 @@ __global__ __launch_bounds__(256) void k_scan_step(const ScanStepParams p) {
   else IO<float>::store8(st, 0, s);
 }
 
-template <typename TIO, int VEC, int LX, int GM>
-int launch_variant(const ScanParams& p, bool backward, hipStream_t s) {
+template <typename TIO, int VEC, int LX, int GM, bool CONVEX>
+int launch_convex(const ScanParams& p, bool backward, hipStream_t s) {
   const int cstep = tile_channels<GM>(LX * VEC, p.D);
   const int64_t blocks = int64_t(p.NT) * ((p.C + cstep - 1) / cstep);
-  if (backward) k_scan_bwd<TIO, VEC, LX, GM><<<dim3(unsigned(blocks)), 256, 0, s>>>(p);
-  else k_scan_fwd<TIO, VEC, LX, GM><<<dim3(unsigned(blocks)), 256, 0, s>>>(p);
+  if (backward) k_scan_bwd<TIO, VEC, LX, GM, CONVEX><<<dim3(unsigned(blocks)), kBwdThreads, 0, s>>>(p);
+  else k_scan_fwd<TIO, VEC, LX, GM, CONVEX><<<dim3(unsigned(blocks)), kFwdThreads, 0, s>>>(p);
   return static_cast<int>(hipGetLastError());
+}
+
+template <typename TIO, int VEC, int LX, int GM>
+int launch_variant(const ScanParams& p, bool backward, hipStream_t s) {
+  return p.convex ? launch_convex<TIO, VEC, LX, GM, true>(p, backward, s)
+                  : launch_convex<TIO, VEC, LX, GM, false>(p, backward, s);
 }
 
 // Vectors of 16 bytes where every row starts on one; one channel a lane otherwise
@@ -667,24 +794,30 @@ int launch_scan_params(const ScanParams& p, void* stream) {
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   (void)hipGetLastError();
   const int hb = param_heads(p.D);
-  k_scan_params<<<dim3((p.H + hb - 1) / hb), kParamThreads, 0, s>>>(p);
+  const dim3 heads((p.H + hb - 1) / hb);
+  if (p.runs) {
+    k_scan_param_runs<<<dim3((p.C + 63) / 64, kParamSplit), 256, 0, s>>>(p);
+    k_scan_params<double><<<heads, kParamThreads, 0, s>>>(p, p.runs, kParamSplit);
+  } else {
+    k_scan_params<float><<<heads, kParamThreads, 0, s>>>(p, p.part, p.NT);
+  }
   return static_cast<int>(hipGetLastError());
 }
 
 int launch_scan_clear(const ScanParams& p, void* stream) {
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   (void)hipGetLastError();
-  const int64_t n = int64_t(p.NT) * p.C;   // 16 bytes of words per tile and channel
-  k_scan_clear<<<dim3(unsigned(std::min<int64_t>((n + 255) / 256, 2048))), 256, 0, s>>>(
-      p.counter, reinterpret_cast<uint4*>(p.words), n);
+  const int64_t n = int64_t(p.NT) * p.C;
+  k_scan_clear<<<dim3(unsigned(std::min<int64_t>((n + 511) / 512, 2048))), 256, 0, s>>>(
+      p.counters, scan_counters(p.C), p.words, n);
   return static_cast<int>(hipGetLastError());
 }
 
-int launch_scan_tables(const ScanParams& p, const ScanBatch& b, void* stream) {
+int launch_scan_tables(const ScanParams& p, int TT, const ScanBatch& b, void* stream) {
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   (void)hipGetLastError();
   if (b.n <= 0) return 0;
-  k_scan_tables<<<dim3(b.n), 64, 0, s>>>(p.tab, b);
+  k_scan_tables<<<dim3(b.n), 64, 0, s>>>(p.tab, TT, bwd_tile(p.gate), b);
   return static_cast<int>(hipGetLastError());
 }
 
