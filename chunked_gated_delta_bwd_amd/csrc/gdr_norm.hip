@@ -3,8 +3,11 @@
 //
 // TPR threads hold a row in registers (NV vectors of VEC elements each), so every
 // input is read once and every output written once whatever the row needs in
-// between: the sum of squares, and for e4m3 the largest magnitude per group.
-// Sums are fp32.  Streaming work, bound by HBM.
+// between: the sum of squares, and for e4m3 the largest magnitude per group.  Narrow
+// rows share a wave, and a thread takes UNR rows at a time, so that each has four or
+// so 16-byte loads per tensor in flight.  Sums are fp32.  Streaming work, bound by
+// HBM.  Rows need not start on 16 bytes (the device takes vector accesses at the
+// elements' own alignment); only a last partial vector goes element by element.
 #include <hip/hip_runtime.h>
 
 #include "gdr_device.h"
@@ -16,32 +19,64 @@ namespace {
 constexpr float kE4m3Max = 448.f;
 constexpr float kMinScale = 1.17549435e-38f;   // 2^-126: 1 / scale stays finite
 
-template <typename TIO, int VEC>
-__device__ __forceinline__ void load_v(const void* b, int64_t o, float (&x)[VEC]) {
-  if constexpr (VEC == 8) IO<TIO>::load8(b, o, x);
-  else if constexpr (VEC == 4) IO<TIO>::load4(b, o, x);
-  else x[0] = IO<TIO>::load1(b, o);
-}
-template <typename TIO, int VEC>
-__device__ __forceinline__ void store_v(void* b, int64_t o, const float (&x)[VEC]) {
-  if constexpr (VEC == 8) IO<TIO>::store8(b, o, x);
-  else if constexpr (VEC == 4) IO<TIO>::store4(b, o, x[0], x[1], x[2], x[3]);
-  else IO<TIO>::store1(b, o, x[0]);
-}
+// 16 bytes at the alignment of the elements
+template <typename TIO> struct Wide;
+template <> struct Wide<bf16> { typedef u32x4 __attribute__((aligned(2))) T; };
+template <> struct Wide<float> { typedef u32x4 __attribute__((aligned(4))) T; };
 
-// Sum over the TPR threads of a row, on each of them.  `red`: one float per wave
-// and call slot.
-template <int TPR>
-__device__ __forceinline__ float row_sum(float x, float* red) {
-  x = group_sum<(TPR < 64 ? TPR : 64)>(x);
-  if constexpr (TPR > 64) {
-    if (lane_id() == 0) red[wave_id()] = x;
-    __syncthreads();
-    x = 0.f;
+template <typename TIO> constexpr int kVec = 16 / int(sizeof(TIO));
+
+// n of the VEC elements from o on (all of them but at a row's end); the rest is zero
+template <typename TIO, int VEC>
+__device__ __forceinline__ u32x4 load_raw(const void* b, int64_t o, int n) {
+  const TIO* p = static_cast<const TIO*>(b) + o;
+  if (n >= VEC) return *reinterpret_cast<const typename Wide<TIO>::T*>(p);
+  TIO t[VEC];
 #pragma unroll
-    for (int i = 0; i < TPR / 64; ++i) x += red[i];
+  for (int v = 0; v < VEC; ++v) t[v] = v < n ? p[v] : TIO(0.f);
+  return __builtin_bit_cast(u32x4, t);
+}
+template <typename TIO, int VEC>
+__device__ __forceinline__ void unpack(const u32x4& u, float (&x)[VEC]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (VEC == 8) {
+      x[2 * i] = __uint_as_float(u[i] << 16);
+      x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    } else {
+      x[i] = __uint_as_float(u[i]);
+    }
   }
-  return x;
+}
+template <typename TIO, int VEC>
+__device__ __forceinline__ void store_n(void* b, int64_t o, int n, const float (&x)[VEC]) {
+  TIO* p = static_cast<TIO*>(b) + o;
+  if (n >= VEC) {
+    u32x4 u;
+    if constexpr (VEC == 8) {
+      const uint2 lo = pack4_bf16(x[0], x[1], x[2], x[3]), hi = pack4_bf16(x[4], x[5], x[6], x[7]);
+      u = u32x4{lo.x, lo.y, hi.x, hi.y};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i] = __float_as_uint(x[i]);
+    }
+    *reinterpret_cast<typename Wide<TIO>::T*>(p) = u;
+  } else {
+#pragma unroll
+    for (int v = 0; v < VEC; ++v)
+      if (v < n) p[v] = TIO(x[v]);
+  }
+}
+// the weight: fp32, and every vector starts on 16 bytes of it
+template <int VEC>
+__device__ __forceinline__ void load_w(const float* w, int c, int n, float (&x)[VEC]) {
+  if (n >= VEC) {
+    if constexpr (VEC == 8) IO<float>::load8(w, c, x);
+    else IO<float>::load4(w, c, x);
+  } else {
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) x[v] = v < n ? w[c + v] : 0.f;
+  }
 }
 
 // Largest magnitude as the bits of |x|: integer order is the order of the
@@ -54,8 +89,7 @@ __device__ __forceinline__ uint32_t group_max(uint32_t x) {
 }
 
 __device__ __forceinline__ float scale_of(uint32_t bits) {
-  const float m = __uint_as_float(bits);
-  const float s = m / kE4m3Max;
+  const float s = __uint_as_float(bits) / kE4m3Max;
   return s < kMinScale ? kMinScale : s;   // a NaN passes through
 }
 
@@ -66,130 +100,145 @@ __device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d
   return uint32_t(r);
 }
 
-template <typename TIO, int VEC, int TPR, int NV, bool QUANT>
+template <typename TIO, int TPR, int NV, int UNR, bool QUANT>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm(const NormParams p) {
-  constexpr int BS = TPR > 256 ? TPR : 256, RPW = BS / TPR;
+  constexpr int VEC = kVec<TIO>, BS = TPR > 256 ? TPR : 256, RPW = BS / TPR;
+  constexpr int LANES = TPR < 64 ? TPR : 64;   // of the row's threads in a wave
+  static_assert(UNR == 1 || TPR <= 64, "several rows a thread only within a wave");
   __shared__ float red[BS / 64];
   __shared__ uint32_t redm[QUANT ? BS / 64 : 1];
-  __shared__ uint32_t gmax[QUANT && VEC == 1 ? RPW : 1][QUANT && VEC == 1 ? (TPR * NV + 127) / 128 : 1];
   const int lane = threadIdx.x % TPR, rw = threadIdx.x / TPR;
-  const int64_t row = int64_t(blockIdx.x) * RPW + rw;
-  const bool on = row < p.rows;
-  const int64_t base = row * p.width;
-  float r[NV][VEC], ss = 0.f;
+  const int64_t row0 = int64_t(blockIdx.x) * RPW * UNR + rw;   // then every RPW rows
+  u32x4 rx[UNR][NV], rr[UNR][NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * TPR + lane) * VEC;
-    if (on && c < p.width) {
-      load_v<TIO, VEC>(p.x, base + c, r[i]);
-      if (p.res) {
-        float y[VEC];
-        load_v<TIO, VEC>(p.res, base + c, y);
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) r[i][v] += y[v];
-      }
-    } else {
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) r[i][v] = 0.f;
-    }
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) ss += r[i][v] * r[i][v];
-  }
-  ss = row_sum<TPR>(ss, red);
-  const float rstd = rsqrtf(ss / float(p.width) + p.eps);
-  uint32_t amax = 0, gm[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * TPR + lane) * VEC;
-    const bool in = on && c < p.width;
-    float w[VEC];
-    if (in) {
-      if (p.res_out) store_v<TIO, VEC>(p.res_out, base + c, r[i]);
-      if (p.w) load_v<float, VEC>(p.w, c, w);
-      else
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) w[v] = 1.f;
-    } else {
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) w[v] = 0.f;
-    }
-    gm[i] = 0;
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-      r[i][v] = in ? r[i][v] * rstd * w[v] : 0.f;
-      if constexpr (QUANT) gm[i] = max(gm[i], __float_as_uint(r[i][v]) & 0x7fffffffu);
-    }
-    amax = max(amax, gm[i]);
-    if constexpr (!QUANT) {
-      if (in) store_v<TIO, VEC>(p.y, base + c, r[i]);
-    }
-  }
-  if constexpr (QUANT) {
-    // gm[i] becomes the group's maximum
-    if (p.group == 0) {
-      amax = group_max<(TPR < 64 ? TPR : 64)>(amax);
-      if constexpr (TPR > 64) {
-        if (lane_id() == 0) redm[wave_id()] = amax;
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < TPR / 64; ++i) amax = max(amax, redm[i]);
-      }
-#pragma unroll
-      for (int i = 0; i < NV; ++i) gm[i] = amax;
-      if (on && lane == 0) p.scales[row] = scale_of(amax);
-    } else if constexpr (VEC > 1) {
-      // a group of 128 channels is 128 / VEC neighbouring lanes
-      static_assert(TPR * VEC >= 128, "a group spans lanes of one vector index");
-      const int groups = (p.width + 127) / 128;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        gm[i] = group_max<128 / VEC>(gm[i]);
-        const int c = (i * TPR + lane) * VEC;
-        if (on && c < p.width && c % 128 == 0) p.scales[row * groups + c / 128] = scale_of(gm[i]);
-      }
-    } else {
-      const int groups = (p.width + 127) / 128;
-      for (int i = lane; i < groups; i += TPR) gmax[rw][i] = 0;
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = i * TPR + lane;
-        if (c < p.width) atomicMax(&gmax[rw][c / 128], gm[i]);
-      }
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = i * TPR + lane;
-        if (c < p.width) gm[i] = gmax[rw][c / 128];
-        if (on && c < p.width && c % 128 == 0) p.scales[row * groups + c / 128] = scale_of(gm[i]);
-      }
-    }
+  for (int u = 0; u < UNR; ++u)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * TPR + lane) * VEC;
-      if (!(on && c < p.width)) continue;
-      const float s = scale_of(gm[i]);
-      float z[VEC];
+      const int n = row0 + u * RPW < p.rows ? p.width - c : 0;
+      const int64_t o = (row0 + u * RPW) * p.width + c;
+      rx[u][i] = rr[u][i] = u32x4{0, 0, 0, 0};
+      if (n > 0) {
+        rx[u][i] = load_raw<TIO, VEC>(p.x, o, n);
+        if (p.res) rr[u][i] = load_raw<TIO, VEC>(p.res, o, n);
+      }
+    }
+  float r[UNR][NV][VEC], rstd[UNR];
+#pragma unroll
+  for (int u = 0; u < UNR; ++u) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float y[VEC];
+      unpack<TIO, VEC>(rx[u][i], r[u][i]);
+      unpack<TIO, VEC>(rr[u][i], y);
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
-        const float t = r[i][v] / s;
-        z[v] = t != t ? t : fminf(fmaxf(t, -kE4m3Max), kE4m3Max);
+        if (p.res) r[u][i][v] += y[v];
+        ss += r[u][i][v] * r[u][i][v];
       }
-      uint8_t* q = static_cast<uint8_t*>(p.q) + base + c;
-      if constexpr (VEC == 8)
-        *reinterpret_cast<uint2*>(q) = make_uint2(pack_e4m3(z[0], z[1], z[2], z[3]), pack_e4m3(z[4], z[5], z[6], z[7]));
-      else if constexpr (VEC == 4) *reinterpret_cast<uint32_t*>(q) = pack_e4m3(z[0], z[1], z[2], z[3]);
-      else q[0] = uint8_t(pack_e4m3(z[0], 0.f, 0.f, 0.f));
+    }
+    ss = group_sum<LANES>(ss);
+    if constexpr (TPR > 64) {
+      if (lane_id() == 0) red[wave_id()] = ss;
+      __syncthreads();
+      ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < TPR / 64; ++i) ss += red[i];
+    }
+    rstd[u] = rsqrtf(ss / float(p.width) + p.eps);
+  }
+  uint32_t gm[UNR][NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * TPR + lane) * VEC, n = p.width - c;
+    float w[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) w[v] = 1.f;
+    if (p.w && n > 0) load_w<VEC>(p.w, c, n, w);
+#pragma unroll
+    for (int u = 0; u < UNR; ++u) {
+      const int64_t o = (row0 + u * RPW) * p.width + c;
+      const bool on = n > 0 && row0 + u * RPW < p.rows;
+      if (on && p.res_out) store_n<TIO, VEC>(p.res_out, o, n, r[u][i]);
+      gm[u][i] = 0;
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        r[u][i][v] = r[u][i][v] * rstd[u] * w[v];
+        // places past the row's end hold 0 / rms, which may be a NaN of their own
+        if (QUANT && v < n) gm[u][i] = max(gm[u][i], __float_as_uint(r[u][i][v]) & 0x7fffffffu);
+      }
+      if constexpr (!QUANT) {
+        if (on) store_n<TIO, VEC>(p.y, o, n, r[u][i]);
+      }
+    }
+  }
+  if constexpr (QUANT) {
+    // the lanes of one vector index that hold a group of 128 channels (a row with
+    // fewer channels than that is one group)
+    constexpr int GW = TPR * VEC < 128 ? TPR : 128 / VEC;
+    static_assert(TPR * VEC >= 128 || NV == 1, "groups do not cross vector indexes");
+    const int groups = p.group ? (p.width + 127) / 128 : 1;
+#pragma unroll
+    for (int u = 0; u < UNR; ++u) {
+      const int64_t row = row0 + u * RPW;
+      if (p.group == 0) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) m = max(m, gm[u][i]);
+        m = group_max<LANES>(m);
+        if constexpr (TPR > 64) {
+          if (lane_id() == 0) redm[wave_id()] = m;
+          __syncthreads();
+#pragma unroll
+          for (int i = 0; i < TPR / 64; ++i) m = max(m, redm[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) gm[u][i] = m;
+      } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) gm[u][i] = group_max<GW>(gm[u][i]);
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * TPR + lane) * VEC, n = p.width - c;
+        if (n <= 0 || row >= p.rows) continue;
+        const float s = scale_of(gm[u][i]);
+        if (p.group ? c % 128 == 0 : c == 0) p.scales[row * groups + c / (p.group ? 128 : p.width)] = s;
+        const float inv = 1.f / s;
+        float z[VEC];
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+          const float t = r[u][i][v] * inv;   // 448 (1 + 2^-23) at most: the clamp is of rounding alone
+          z[v] = t != t ? t : fminf(fmaxf(t, -kE4m3Max), kE4m3Max);
+        }
+        uint8_t* q = static_cast<uint8_t*>(p.q) + row * p.width + c;
+        typedef uint32_t __attribute__((aligned(1))) u32u;
+        uint32_t b[VEC / 4];
+#pragma unroll
+        for (int v = 0; v < VEC / 4; ++v) b[v] = pack_e4m3(z[4 * v], z[4 * v + 1], z[4 * v + 2], z[4 * v + 3]);
+        if (n >= VEC) {
+          typedef uint32_t __attribute__((ext_vector_type(VEC / 4), aligned(1))) T;
+          if constexpr (VEC == 8) *reinterpret_cast<T*>(q) = T{b[0], b[1]};
+          else *reinterpret_cast<u32u*>(q) = b[0];
+        } else {
+#pragma unroll
+          for (int v = 0; v < VEC; ++v)
+            if (v < n) q[v] = uint8_t(b[v / 4] >> (8 * (v % 4)));
+        }
+      }
     }
   }
 }
 
-// Backward: a workgroup walks rows blockIdx.x, + gridDim.x, ... (in units of its
-// RPW rows) and keeps its share of dw in registers; the row groups are added in
-// LDS and each workgroup leaves one row of partial sums.
-template <typename TIO, int VEC, int TPR, int NV>
+// Backward: a workgroup walks the rows in steps of the whole grid and keeps its share
+// of dw in registers; the row groups are added in LDS and each workgroup leaves one
+// row of partial sums.
+template <typename TIO, int TPR, int NV, int UNR>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm_bwd(const NormParams p) {
-  constexpr int BS = TPR > 256 ? TPR : 256, RPW = BS / TPR;
+  constexpr int VEC = kVec<TIO>, BS = TPR > 256 ? TPR : 256, RPW = BS / TPR;
+  constexpr int LANES = TPR < 64 ? TPR : 64;
+  static_assert(UNR == 1 || TPR <= 64, "several rows a thread only within a wave");
   __shared__ float red[2][2][BS / 64];
   __shared__ float sw[RPW > 1 ? RPW : 1][RPW > 1 ? TPR * NV * VEC : 1];
   const int lane = threadIdx.x % TPR, rw = threadIdx.x / TPR;
@@ -199,59 +248,68 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm_bwd(const NormPa
     const int c = (i * TPR + lane) * VEC;
 #pragma unroll
     for (int v = 0; v < VEC; ++v) { w[i][v] = 1.f; acc[i][v] = 0.f; }
-    if (c < p.width && p.w) load_v<float, VEC>(p.w, c, w[i]);
+    if (p.w && c < p.width) load_w<VEC>(p.w, c, p.width - c, w[i]);
   }
+  const float inv_width = 1.f / float(p.width);
   int flip = 0;
-  for (int64_t row0 = int64_t(blockIdx.x) * RPW; row0 < p.rows; row0 += int64_t(gridDim.x) * RPW, flip ^= 1) {
-    const int64_t row = row0 + rw;
-    const bool on = row < p.rows;
-    const int64_t base = row * p.width;
-    float r[NV][VEC], dy[NV][VEC], ss = 0.f, sd = 0.f;
+  for (int64_t first = int64_t(blockIdx.x) * RPW * UNR; first < p.rows; first += int64_t(gridDim.x) * RPW * UNR) {
+    const int64_t row0 = first + rw;
+    u32x4 rr[UNR][NV], rdy[UNR][NV], rdr[UNR][NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * TPR + lane) * VEC;
-      if (on && c < p.width) {
-        load_v<TIO, VEC>(p.x, base + c, r[i]);
-        load_v<TIO, VEC>(p.dy, base + c, dy[i]);
-      } else {
+    for (int u = 0; u < UNR; ++u)
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) r[i][v] = dy[i][v] = 0.f;
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * TPR + lane) * VEC;
+        const int n = row0 + u * RPW < p.rows ? p.width - c : 0;
+        const int64_t o = (row0 + u * RPW) * p.width + c;
+        rr[u][i] = rdy[u][i] = rdr[u][i] = u32x4{0, 0, 0, 0};
+        if (n > 0) {
+          rr[u][i] = load_raw<TIO, VEC>(p.x, o, n);
+          rdy[u][i] = load_raw<TIO, VEC>(p.dy, o, n);
+          if (p.dres) rdr[u][i] = load_raw<TIO, VEC>(p.dres, o, n);
+        }
       }
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        ss += r[i][v] * r[i][v];
-        sd += r[i][v] * dy[i][v] * w[i][v];
+    for (int u = 0; u < UNR; ++u) {
+      float r[NV][VEC], dy[NV][VEC], ss = 0.f, sd = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        unpack<TIO, VEC>(rr[u][i], r[i]);
+        unpack<TIO, VEC>(rdy[u][i], dy[i]);
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+          ss += r[i][v] * r[i][v];
+          sd += r[i][v] * dy[i][v] * w[i][v];
+        }
       }
-    }
-    // two sums a row; the LDS slots alternate, so one barrier per row is enough
-    ss = group_sum<(TPR < 64 ? TPR : 64)>(ss);
-    sd = group_sum<(TPR < 64 ? TPR : 64)>(sd);
-    if constexpr (TPR > 64) {
-      if (lane_id() == 0) { red[flip][0][wave_id()] = ss; red[flip][1][wave_id()] = sd; }
-      __syncthreads();
-      ss = sd = 0.f;
+      ss = group_sum<LANES>(ss);
+      sd = group_sum<LANES>(sd);
+      if constexpr (TPR > 64) {
+        // the LDS slots alternate, so one barrier a row is enough
+        if (lane_id() == 0) { red[flip][0][wave_id()] = ss; red[flip][1][wave_id()] = sd; }
+        __syncthreads();
+        ss = sd = 0.f;
 #pragma unroll
-      for (int i = 0; i < TPR / 64; ++i) { ss += red[flip][0][i]; sd += red[flip][1][i]; }
-    }
-    const float rstd = rsqrtf(ss / float(p.width) + p.eps);
-    const float m = rstd * rstd * (sd / float(p.width));
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * TPR + lane) * VEC;
-      if (!(on && c < p.width)) continue;
-      float d[VEC];
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        d[v] = rstd * (w[i][v] * dy[i][v] - r[i][v] * m);
-        acc[i][v] += dy[i][v] * (r[i][v] * rstd);
+        for (int i = 0; i < TPR / 64; ++i) { ss += red[flip][0][i]; sd += red[flip][1][i]; }
+        flip ^= 1;
       }
-      if (p.dres) {
-        float y[VEC];
-        load_v<TIO, VEC>(p.dres, base + c, y);
+      const float rstd = rsqrtf(ss * inv_width + p.eps);
+      const float m = rstd * rstd * (sd * inv_width);
+      if (row0 + u * RPW >= p.rows) continue;   // 1 / rms of nothing may be infinite
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) d[v] += y[v];
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * TPR + lane) * VEC, n = p.width - c;
+        if (n <= 0) continue;
+        float d[VEC], y[VEC];
+        unpack<TIO, VEC>(rdr[u][i], y);
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+          d[v] = rstd * (w[i][v] * dy[i][v] - r[i][v] * m);
+          if (p.dres) d[v] += y[v];
+          acc[i][v] += dy[i][v] * (r[i][v] * rstd);
+        }
+        store_n<TIO, VEC>(p.dx, (row0 + u * RPW) * p.width + c, n, d);
       }
-      store_v<TIO, VEC>(p.dx, base + c, d);
     }
   }
   if (!p.part) return;
@@ -279,88 +337,100 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm_bwd(const NormPa
   }
 }
 
-// dw: the sum of the workgroups' rows, 64 columns a workgroup, four runs of rows
-// each added in order
-__global__ __launch_bounds__(256) void k_norm_dw(const float* part, float* dw, int width, int n) {
-  __shared__ double s[4][64];
-  const int c = blockIdx.x * 64 + (threadIdx.x & 63), g = threadIdx.x >> 6;
+// dw: the sum of the workgroups' rows, 16 columns a workgroup (so that a narrow
+// weight still spreads), 64 runs of rows each added in order
+__global__ __launch_bounds__(1024) void k_norm_dw(const float* part, float* dw, int width, int n) {
+  __shared__ double s[64][16];
+  const int col = threadIdx.x & 15, g = threadIdx.x >> 4;
+  const int c = blockIdx.x * 16 + col;
   double d = 0.0;
-  if (c < width)
-    for (int i = g; i < n; i += 4) d += part[int64_t(i) * width + c];
-  s[g][threadIdx.x & 63] = d;
+  if (c < width) {
+#pragma unroll 8
+    for (int i = g; i < n; i += 64) d += part[int64_t(i) * width + c];
+  }
+  s[g][col] = d;
   __syncthreads();
-  if (g == 0 && c < width) dw[c] = float(s[0][threadIdx.x] + s[1][threadIdx.x] + s[2][threadIdx.x] + s[3][threadIdx.x]);
+  for (int m = 32; m; m >>= 1) {
+    if (g < m) s[g][col] += s[g + m][col];
+    __syncthreads();
+  }
+  if (g == 0 && c < width) dw[c] = float(s[0][col]);
 }
 
-// Threads per row and vectors per thread for a width: whole waves once a row
-// fills one, four vectors a thread before more threads.
+// Threads per row for a width of n vectors.
 struct Plan { int tpr, nv; };
-Plan plan_for(int width, int vec) {
-  const int n = (width + vec - 1) / vec;
+Plan plan_for(int n) {
+  if (n <= 8) return {8, 1};
+  if (n <= 16) return {16, 1};
   if (n <= 32) return {32, 1};
   if (n <= 64) return {64, 1};
   if (n <= 128) return {64, 2};
   if (n <= 256) return {64, 4};
+  if (n <= 512) return {256, 2};
   if (n <= 1024) return {256, 4};
+  if (n <= 2048) return {1024, 2};
   if (n <= 4096) return {1024, 4};
-  return {1024, vec == 1 ? 32 : 8};
+  return {1024, 8};
 }
-
-int vec_of(int width, int dtype) {
-  const int v = dtype == GDR_BF16 ? 8 : 4;
-  return width % v == 0 ? v : 1;
+int vectors_of(int width, int dtype) {
+  const int v = dtype == GDR_BF16 ? kVec<bf16> : kVec<float>;
+  return (width + v - 1) / v;
 }
+constexpr int unr_for(int tpr, int nv) { return tpr > 64 ? 1 : 4 / nv; }
 
-template <typename TIO, int VEC, int TPR, int NV>
+template <typename TIO, int TPR, int NV>
 int launch_fwd(const NormParams& p, hipStream_t s) {
-  constexpr int BS = TPR > 256 ? TPR : 256, RPW = BS / TPR;
-  const dim3 grid(unsigned((p.rows + RPW - 1) / RPW));
-  if (p.q) k_norm<TIO, VEC, TPR, NV, true><<<grid, BS, 0, s>>>(p);
-  else k_norm<TIO, VEC, TPR, NV, false><<<grid, BS, 0, s>>>(p);
+  constexpr int BS = TPR > 256 ? TPR : 256, UNR = unr_for(TPR, NV), ROWS = BS / TPR * UNR;
+  const dim3 grid(unsigned((p.rows + ROWS - 1) / ROWS));
+  if (p.q) k_norm<TIO, TPR, NV, UNR, true><<<grid, BS, 0, s>>>(p);
+  else k_norm<TIO, TPR, NV, UNR, false><<<grid, BS, 0, s>>>(p);
   return static_cast<int>(hipGetLastError());
 }
 
-int partials_for(int64_t rows, int rpw) {
-  const int64_t n = (rows + rpw - 1) / rpw;
+// Workgroups of the backward: as many as stay resident, fewer for few rows.
+int partials_for(int64_t rows, int tpr, int nv) {
+  const int64_t per = int64_t(tpr > 256 ? 1 : 256 / tpr) * unr_for(tpr, nv);
+  const int64_t n = (rows + per - 1) / per;
   return int(n < kNormPartials ? n : kNormPartials);
 }
 
-template <typename TIO, int VEC, int TPR, int NV>
+template <typename TIO, int TPR, int NV>
 int launch_bwd(const NormParams& p, hipStream_t s) {
-  constexpr int BS = TPR > 256 ? TPR : 256, RPW = BS / TPR;
-  k_norm_bwd<TIO, VEC, TPR, NV><<<dim3(partials_for(p.rows, RPW)), BS, 0, s>>>(p);
+  constexpr int BS = TPR > 256 ? TPR : 256;
+  k_norm_bwd<TIO, TPR, NV, unr_for(TPR, NV)><<<dim3(partials_for(p.rows, TPR, NV)), BS, 0, s>>>(p);
   return static_cast<int>(hipGetLastError());
 }
 
-template <typename TIO, int VEC, bool BWD>
+template <typename TIO, bool BWD>
 int launch_plan(const NormParams& p, hipStream_t s) {
-  const Plan pl = plan_for(p.width, VEC);
+  const Plan pl = plan_for(vectors_of(p.width, p.dtype));
 #define GDR_NORM_CASE(T, N) \
-  if (pl.tpr == T && pl.nv == N) return BWD ? launch_bwd<TIO, VEC, T, N>(p, s) : launch_fwd<TIO, VEC, T, N>(p, s);
+  if (pl.tpr == T && pl.nv == N) return BWD ? launch_bwd<TIO, T, N>(p, s) : launch_fwd<TIO, T, N>(p, s);
+  GDR_NORM_CASE(8, 1)
+  GDR_NORM_CASE(16, 1)
   GDR_NORM_CASE(32, 1)
   GDR_NORM_CASE(64, 1)
   GDR_NORM_CASE(64, 2)
   GDR_NORM_CASE(64, 4)
+  GDR_NORM_CASE(256, 2)
   GDR_NORM_CASE(256, 4)
+  GDR_NORM_CASE(1024, 2)
   GDR_NORM_CASE(1024, 4)
-  if constexpr (VEC == 1) { GDR_NORM_CASE(1024, 32) }
-  else if constexpr (VEC == 4) { GDR_NORM_CASE(1024, 8) }
+  if constexpr (sizeof(TIO) == 4) { GDR_NORM_CASE(1024, 8) }
 #undef GDR_NORM_CASE
   return static_cast<int>(hipErrorInvalidConfiguration);
 }
 
 template <bool BWD>
 int launch_any(const NormParams& p, hipStream_t s) {
-  if (p.dtype == GDR_BF16)
-    return p.width % 8 == 0 ? launch_plan<bf16, 8, BWD>(p, s) : launch_plan<bf16, 1, BWD>(p, s);
-  return p.width % 4 == 0 ? launch_plan<float, 4, BWD>(p, s) : launch_plan<float, 1, BWD>(p, s);
+  return p.dtype == GDR_BF16 ? launch_plan<bf16, BWD>(p, s) : launch_plan<float, BWD>(p, s);
 }
 
 }  // namespace
 
 int norm_bwd_partials(int64_t rows, int32_t width, int32_t dtype) {
-  const Plan pl = plan_for(width, vec_of(width, dtype));
-  return partials_for(rows, pl.tpr > 256 ? 1 : 256 / pl.tpr);
+  const Plan pl = plan_for(vectors_of(width, dtype));
+  return partials_for(rows, pl.tpr, pl.nv);
 }
 
 int launch_norm(const NormParams& p, void* stream) {
@@ -374,7 +444,7 @@ int launch_norm_bwd(const NormParams& p, void* stream) {
   (void)hipGetLastError();
   int e = p.rows ? launch_any<true>(p, s) : 0;
   if (e || !p.dw) return e;
-  k_norm_dw<<<dim3((p.width + 63) / 64), 256, 0, s>>>(p.part, p.dw, p.width,
+  k_norm_dw<<<dim3((p.width + 15) / 16), 1024, 0, s>>>(p.part, p.dw, p.width,
                                                        norm_bwd_partials(p.rows, p.width, p.dtype));
   return static_cast<int>(hipGetLastError());
 }
