@@ -137,8 +137,14 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+# the current stream's handle without building a torch.cuda.Stream around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -258,25 +264,29 @@ def _bad(message: str) -> None:
 def _check_tensors(specs) -> None:
     """specs: (name, tensor or None, numel, dtype).  Every tensor given has that type
     and size, is contiguous, and lies on the current GPU, where the call is enqueued."""
-    devices = set()
+    first = other = None
     for name, t, numel, dtype in specs:
         if t is None:
             continue
-        if t.dtype != dtype:
+        if t.dtype is not dtype:
             _bad(f"{name} is {t.dtype}, expected {dtype}")
         if t.numel() != numel:
             _bad(f"{name} has {t.numel()} elements, expected {numel}")
         if not t.is_contiguous():
             _bad(f"{name} is not contiguous")
-        devices.add(t.device)
-    for d in devices:
-        if d.type != "cuda":
-            _bad(f"tensors are on {d}, expected a GPU")
-    if len(devices) > 1:
-        _bad(f"tensors are on several devices: {sorted(map(str, devices))}")
-    for d in devices:
-        if d.index != torch.cuda.current_device():
-            _bad(f"tensors are on {d}, the current device is cuda:{torch.cuda.current_device()}")
+        d = t.get_device()
+        if first is None:
+            first = d
+        elif d != first:
+            other = d
+    if first is None:
+        return
+    if other is not None:
+        _bad(f"tensors are on several devices: {first} and {other} (-1: the CPU)")
+    if first < 0:
+        _bad("tensors are on the CPU, expected a GPU")
+    if first != torch.cuda.current_device():
+        _bad(f"tensors are on cuda:{first}, the current device is cuda:{torch.cuda.current_device()}")
 
 
 def _check_workspace(ws: Optional[torch.Tensor], like: Optional[torch.Tensor]) -> int:
@@ -284,7 +294,7 @@ def _check_workspace(ws: Optional[torch.Tensor], like: Optional[torch.Tensor]) -
         return 0
     if not ws.is_contiguous():
         _bad("the workspace is not contiguous")
-    if like is not None and ws.device != like.device:
+    if like is not None and ws.get_device() != like.get_device():
         _bad(f"the workspace is on {ws.device}, the tensors are on {like.device}")
     return ws.numel() * ws.element_size()
 

@@ -9,8 +9,8 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libgdr.so")
-SOURCES = [os.path.join(PKG, "csrc", n) for n in ("gdr_api.cpp", "gdr_kernels.hip", "gdr_chain.hip", "gdr_kda.hip", "gdr_out.hip", "gdr_group.hip", "gdr_tables.hip", "gdr_noalloc.hip",
-                                                   "gdr_layer.cpp", "gdr_scan.hip", "gdr_norm.hip", "gdr_step.hip")]
+SOURCES = [os.path.join(PKG, "csrc", n) for n in ("gdr_api.cpp", "gdr_kernels.hip", "gdr_chain.hip", "gdr_kda.hip", "gdr_out.hip", "gdr_group.hip", "gdr_tables.hip", "gdr_noalloc.hip")]
+SOURCES += [os.path.join(PKG, "csrc", "layer", n) for n in ("gdr_layer.cpp", "gdr_scan.hip", "gdr_norm.hip", "gdr_step.hip")]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

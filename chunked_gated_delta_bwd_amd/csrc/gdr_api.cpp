@@ -12,7 +12,6 @@
 #include <vector>
 
 #include "gdr_internal.h"
-#include "gdr_layer.h"
 
 namespace {
 
@@ -548,29 +547,6 @@ gdr_status gdr_workspace_region(const gdr_shape* shape, int32_t which, size_t* o
     default: return fail(GDR_EINVAL, "unknown workspace region %d", which);
   }
   return GDR_OK;
-}
-
-gdr_status gdr_step(const gdr_shape* shape, const gdr_inputs* in, float* state, int32_t P, const int32_t* slots,
-                    void* o, void* stream) {
-  int64_t NC = 0;
-  gdr_status st = check_shape(shape, &NC);
-  if (st != GDR_OK) return st;
-  if (shape->cu_seqlens_host || shape->T != 1) return fail(GDR_EINVAL, "a step takes a dense shape with T == 1");
-  if ((st = check_inputs(shape, in)) != GDR_OK) return st;
-  if (in->h0) return fail(GDR_EINVAL, "a step takes its states from the pool, not from h0");
-  if ((st = gdr::check_step_pool(shape->N, state, P, slots, o)) != GDR_OK) return st;
-  gdr::StepParams p;
-  std::memset(&p, 0, sizeof(p));
-  p.N = shape->N; p.H = shape->H; p.D = shape->Dk; p.P = P;
-  p.Hk = shape->Hk > 0 ? shape->Hk : shape->H;
-  p.G = p.H / p.Hk;
-  p.gate = shape->gate == GDR_GATE_SCALAR ? 0 : 1;
-  p.gate_fn = shape->gate == GDR_GATE_CHANNEL_SIGMOID ? 1 : 0;
-  p.dtype = shape->dtype; p.scale = shape->scale; p.gate_scale = shape->gate_scale;
-  p.q = in->q; p.k = in->k; p.v = in->v; p.g = in->g; p.b = in->beta_logit;
-  p.A_log = in->A_log; p.dt_bias = in->dt_bias;
-  p.slots = slots; p.state = state; p.o = o;
-  return hip_status(gdr::launch_step(p, stream), "step kernel");
 }
 
 const char* gdr_last_error(void) { return g_last_error.c_str(); }

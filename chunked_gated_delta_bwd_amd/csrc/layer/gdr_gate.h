@@ -2,7 +2,7 @@
 // recurrence, with their derivatives, in fp32 (see gdr.h for the definitions).
 #pragma once
 
-#include "gdr_device.h"
+#include "../gdr_device.h"
 
 namespace gdr {
 

@@ -7,7 +7,7 @@
 #include <cmath>
 #include <cstring>
 
-#include "gdr_internal.h"
+#include "../gdr_internal.h"
 #include "gdr_layer.h"
 
 namespace {
@@ -69,7 +69,7 @@ gdr_status check_scan_shape(const gdr_scan_shape* s, int64_t* NT_out) {
   if (s->D > 256 || (s->D != 1 && s->D % 8 != 0))
     return set_error(GDR_EUNSUPPORTED, "head dim %d must be 1 or a multiple of 8 up to 256", s->D);
   int64_t NT = 0;
-  const int tile = gdr::bwd_tile(scan_gate(s));
+  const int tile = gdr::bwd_tile(scan_gate(s), s->D > 128);
   if (s->cu_seqlens_host == nullptr) {
     if (s->N != s->B) return set_error(GDR_EINVAL, "dense shape needs N == B (N=%d, B=%d)", s->N, s->B);
     NT = int64_t(s->B) * tiles_of(s->T, tile);
@@ -123,9 +123,9 @@ gdr_status check_scan_inputs(const gdr_scan_shape* s, const gdr_scan_inputs* in,
 }
 
 int64_t fwd_tiles(const gdr_scan_shape* s) {
-  if (!s->cu_seqlens_host) return int64_t(s->B) * tiles_of(s->T, gdr::fwd_tile(scan_gate(s)));
+  if (!s->cu_seqlens_host) return int64_t(s->B) * tiles_of(s->T, gdr::fwd_tile(scan_gate(s), s->D > 128));
   int64_t n = 0;
-  for (int i = 0; i < s->N; ++i) n += tiles_of(s->cu_seqlens_host[i + 1] - s->cu_seqlens_host[i], gdr::fwd_tile(scan_gate(s)));
+  for (int i = 0; i < s->N; ++i) n += tiles_of(s->cu_seqlens_host[i + 1] - s->cu_seqlens_host[i], gdr::fwd_tile(scan_gate(s), s->D > 128));
   return n;
 }
 
@@ -171,7 +171,7 @@ gdr_status scan_prologue(const gdr_scan_shape* s, const gdr::ScanParams& p, int 
       b.tile0[i] = int32_t(row);
       b.saved0[i] = int32_t(saved);
       row += tiles_of(len, tile);
-      saved += tiles_of(len, gdr::bwd_tile(p.gate));
+      saved += tiles_of(len, gdr::bwd_tile(p.gate, p.D > 128));
     }
     const gdr_status st = hip_status(gdr::launch_scan_tables(p, tile, b, stream), "tile table kernel");
     if (st != GDR_OK) return st;
@@ -227,19 +227,6 @@ size_t norm_ws(const gdr_norm_shape* s) {
 
 }  // namespace
 
-namespace gdr {
-
-// gdr_step's own arguments (its shape and inputs are checked where the delta
-// rule's are, in gdr_api.cpp).
-gdr_status check_step_pool(int32_t N, const float* state, int32_t P, const int32_t* slots, const void* o) {
-  const gdr_status st = check_pool(N, state, P, slots);
-  if (st != GDR_OK) return st;
-  const Arg a[] = {{o, "o", true}};
-  return check_ptrs(a, 1);
-}
-
-}  // namespace gdr
-
 extern "C" {
 
 gdr_status gdr_scan_workspace_bytes(const gdr_scan_shape* shape, size_t* bytes) {
@@ -265,7 +252,7 @@ gdr_status gdr_scan_fwd(const gdr_scan_shape* shape, const gdr_scan_inputs* in, 
   gdr::ScanParams p = scan_params(shape, in, fwd_tiles(shape), L, ws);
   p.y = y;
   p.ht = ht;
-  if ((st = scan_prologue(shape, p, gdr::fwd_tile(p.gate), stream)) != GDR_OK) return st;
+  if ((st = scan_prologue(shape, p, gdr::fwd_tile(p.gate, p.D > 128), stream)) != GDR_OK) return st;
   return hip_status(gdr::launch_scan(p, false, stream), "scan kernel");
 }
 
@@ -289,7 +276,7 @@ gdr_status gdr_scan_bwd(const gdr_scan_shape* shape, const gdr_scan_inputs* in, 
   gdr::ScanParams p = scan_params(shape, in, NT, L, ws);
   p.dy = dy; p.dht = dht;
   p.dx = grads->dx; p.dg = grads->dg; p.dh0 = grads->dh0; p.dA_log = grads->dA_log; p.ddt_bias = grads->ddt_bias;
-  if ((st = scan_prologue(shape, p, gdr::bwd_tile(p.gate), stream)) != GDR_OK) return st;
+  if ((st = scan_prologue(shape, p, gdr::bwd_tile(p.gate, p.D > 128), stream)) != GDR_OK) return st;
   if ((st = hip_status(gdr::launch_scan(p, true, stream), "scan gradient kernel")) != GDR_OK) return st;
   return par ? hip_status(gdr::launch_scan_params(p, stream), "parameter reduction kernel") : GDR_OK;
 }
@@ -312,6 +299,36 @@ gdr_status gdr_scan_step(const gdr_scan_shape* shape, const gdr_scan_inputs* in,
   p.x = in->x; p.g = in->g; p.A_log = in->A_log; p.dt_bias = in->dt_bias;
   p.slots = slots; p.state = state; p.y = y;
   return hip_status(gdr::launch_scan_step(p, stream), "scan step kernel");
+}
+
+gdr_status gdr_step(const gdr_shape* shape, const gdr_inputs* in, float* state, int32_t P, const int32_t* slots,
+                    void* o, void* stream) {
+  size_t bytes = 0;
+  gdr_status st = gdr_workspace_bytes(shape, &bytes);   // checks the shape; a step needs no workspace
+  if (st != GDR_OK) return st;
+  if (shape->cu_seqlens_host || shape->T != 1) return set_error(GDR_EINVAL, "a step takes a dense shape with T == 1");
+  if (!in) return set_error(GDR_EINVAL, "inputs is NULL");
+  const bool par = shape->gate != GDR_GATE_SCALAR;
+  if (!par && (in->A_log || in->dt_bias)) return set_error(GDR_EINVAL, "scalar gate takes no A_log/dt_bias");
+  if (par && (!in->A_log || !in->dt_bias)) return set_error(GDR_EINVAL, "per-channel gate needs A_log and dt_bias");
+  if (in->h0) return set_error(GDR_EINVAL, "a step takes its states from the pool, not from h0");
+  const Arg a[] = {{in->q, "input q", true}, {in->k, "input k", true}, {in->v, "input v", true}, {in->g, "input g", true},
+                   {in->beta_logit, "input beta_logit", true}, {in->A_log, "A_log", false},
+                   {in->dt_bias, "dt_bias", false}, {o, "o", true}};
+  if ((st = check_ptrs(a, 8)) != GDR_OK) return st;
+  if ((st = check_pool(shape->N, state, P, slots)) != GDR_OK) return st;
+  gdr::StepParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.N = shape->N; p.H = shape->H; p.D = shape->Dk; p.P = P;
+  p.Hk = shape->Hk > 0 ? shape->Hk : shape->H;
+  p.G = p.H / p.Hk;
+  p.gate = par ? 1 : 0;
+  p.gate_fn = shape->gate == GDR_GATE_CHANNEL_SIGMOID ? 1 : 0;
+  p.dtype = shape->dtype; p.scale = shape->scale; p.gate_scale = shape->gate_scale;
+  p.q = in->q; p.k = in->k; p.v = in->v; p.g = in->g; p.b = in->beta_logit;
+  p.A_log = in->A_log; p.dt_bias = in->dt_bias;
+  p.slots = slots; p.state = state; p.o = o;
+  return hip_status(gdr::launch_step(p, stream), "step kernel");
 }
 
 gdr_status gdr_norm_fwd(const gdr_norm_shape* shape, const void* x, const void* res, const float* w, void* y,

@@ -6,7 +6,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
-#include "../../include/gdr.h"
+#include "../../../include/gdr.h"
 
 namespace gdr {
 
@@ -18,9 +18,12 @@ enum ScanGate {
   kScanSigmoid = 3,
 };
 
-// Tokens per tile of the recurrence, backward and forward.
-constexpr int bwd_tile(int gate) { return gate == kScanHeadLog ? 128 : 64; }
-constexpr int fwd_tile(int gate) { return gate == kScanHeadLog ? 256 : 128; }
+// Tokens per tile of the recurrence, backward and forward.  One decay per head
+// needs fewer registers a token, which go into longer tiles, unless the head is so
+// wide (over 128 channels) that a tile holds twice the channels.
+constexpr bool scan_long(int gate, bool wide) { return gate == kScanHeadLog && !wide; }
+constexpr int bwd_tile(int gate, bool wide) { return scan_long(gate, wide) ? 128 : 64; }
+constexpr int fwd_tile(int gate, bool wide) { return scan_long(gate, wide) ? 256 : 128; }
 
 // One row per tile: at most a tile's tokens of one sequence.  A sequence without
 // tokens has one empty tile, so that its states are passed through.
@@ -110,7 +113,5 @@ struct StepParams {
   void* o;
 };
 int launch_step(const StepParams& p, void* stream);
-// gdr_step's pool, slots and output (gdr_layer.cpp).
-gdr_status check_step_pool(int32_t N, const float* state, int32_t P, const int32_t* slots, const void* o);
 
 }  // namespace gdr

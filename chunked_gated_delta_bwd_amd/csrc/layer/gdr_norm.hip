@@ -10,19 +10,15 @@
 // elements' own alignment); only a last partial vector goes element by element.
 #include <hip/hip_runtime.h>
 
-#include "gdr_device.h"
+#include "../gdr_device.h"
 #include "gdr_layer.h"
+#include "gdr_wide.h"
 
 namespace gdr {
 namespace {
 
 constexpr float kE4m3Max = 448.f;
 constexpr float kMinScale = 1.17549435e-38f;   // 2^-126: 1 / scale stays finite
-
-// 16 bytes at the alignment of the elements
-template <typename TIO> struct Wide;
-template <> struct Wide<bf16> { typedef u32x4 __attribute__((aligned(2))) T; };
-template <> struct Wide<float> { typedef u32x4 __attribute__((aligned(4))) T; };
 
 template <typename TIO> constexpr int kVec = 16 / int(sizeof(TIO));
 

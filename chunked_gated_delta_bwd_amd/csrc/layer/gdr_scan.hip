@@ -28,9 +28,10 @@
 
 #include <algorithm>
 
-#include "gdr_device.h"
+#include "../gdr_device.h"
 #include "gdr_gate.h"
 #include "gdr_layer.h"
+#include "gdr_wide.h"
 
 namespace gdr {
 namespace {
@@ -136,21 +137,37 @@ __device__ __forceinline__ float look_back(const uint64_t* w, int64_t step, int 
   return S;
 }
 
-// VEC consecutive elements: one vector access for VEC > 1
+// VEC consecutive elements, 16 bytes (or one element): one access at the elements'
+// own alignment, which the device allows, so that rows may start anywhere.
 template <typename TIO, int VEC>
 struct Vec {
-  typedef typename IO<TIO>::Raw8 Raw;
-  static __device__ __forceinline__ Raw load(const void* b, int64_t o) { return IO<TIO>::load_raw8(b, o); }
-  static __device__ __forceinline__ void unpack(const Raw& r, float (&x)[VEC]) { IO<TIO>::unpack8(r, x); }
-  static __device__ __forceinline__ void store(void* b, int64_t o, const float (&x)[VEC]) { IO<TIO>::store8(b, o, x); }
-};
-template <typename TIO>
-struct Vec<TIO, 4> {
-  typedef typename IO<TIO>::Raw4 Raw;
-  static __device__ __forceinline__ Raw load(const void* b, int64_t o) { return IO<TIO>::load_raw4(b, o); }
-  static __device__ __forceinline__ void unpack(const Raw& r, float (&x)[4]) { IO<TIO>::unpack4(r, x); }
-  static __device__ __forceinline__ void store(void* b, int64_t o, const float (&x)[4]) {
-    IO<TIO>::store4(b, o, x[0], x[1], x[2], x[3]);
+  static_assert(VEC * sizeof(TIO) == 16, "16-byte vectors");
+  typedef u32x4 Raw;
+  typedef typename Wide<TIO>::T Any;
+  static __device__ __forceinline__ Raw load(const void* b, int64_t o) {
+    return *reinterpret_cast<const Any*>(static_cast<const TIO*>(b) + o);
+  }
+  static __device__ __forceinline__ void unpack(const Raw& u, float (&x)[VEC]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (VEC == 8) {
+        x[2 * i] = __uint_as_float(u[i] << 16);
+        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+      } else {
+        x[i] = __uint_as_float(u[i]);
+      }
+    }
+  }
+  static __device__ __forceinline__ void store(void* b, int64_t o, const float (&x)[VEC]) {
+    Raw u;
+    if constexpr (VEC == 8) {
+      const uint2 lo = pack4_bf16(x[0], x[1], x[2], x[3]), hi = pack4_bf16(x[4], x[5], x[6], x[7]);
+      u = Raw{lo.x, lo.y, hi.x, hi.y};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i] = __float_as_uint(x[i]);
+    }
+    *reinterpret_cast<Any*>(static_cast<TIO*>(b) + o) = u;
   }
 };
 template <typename TIO>
@@ -171,11 +188,25 @@ struct Geo {
   static_assert(PARTS >= 1 && L >= 1, "tile geometry");
 };
 
-// Channels a tile advances by: CT, or with one gate per head the whole heads that
-// fit (the head's gate gradient is summed inside the workgroup).
+// Channel tiles of CT channels or fewer: with one gate per head the whole heads that
+// fit (the head's gate gradient is summed inside the workgroup), else CT.  Where
+// rows do not start on a vector, tiles share the channels evenly instead, so that
+// each has at least one vector's worth (a last vector overlaps the one before).
 template <int GM>
-__host__ __device__ __forceinline__ int tile_channels(int CT, int D) {
-  return GM == kScanHeadLog ? CT / D * D : CT;
+__host__ __device__ __forceinline__ int channel_tiles(int CT, int C, int D) {
+  const int step = GM == kScanHeadLog ? CT / D * D : CT;
+  return (C + step - 1) / step;
+}
+template <int GM, int VEC>
+__device__ __forceinline__ void channel_tile(int CT, int C, int D, int nct, int ct, int& base, int& n) {
+  if (GM != kScanHeadLog && C % VEC) {
+    base = int(int64_t(C) * ct / nct);
+    n = int(int64_t(C) * (ct + 1) / nct) - base;
+  } else {
+    const int step = GM == kScanHeadLog ? CT / D * D : CT;
+    base = ct * step;
+    n = min(C - base, step);
+  }
 }
 
 // The place of a tile (its row of the published words) in the order in which the
@@ -251,7 +282,7 @@ struct GateRaw<TIO, VEC, kScanHeadLog> {
 // tiles skip.
 template <typename TIO, int VEC, int LX, int GM, bool CONVEX>
 __global__ __launch_bounds__(kFwdThreads) void k_scan_fwd(const ScanParams p) {
-  constexpr int TT = fwd_tile(GM);
+  constexpr int TT = fwd_tile(GM, LX * VEC > 128), kSaved = bwd_tile(GM, LX * VEC > 128);
   typedef Geo<VEC, LX, kFwdThreads, TT> G;
   typedef Vec<TIO, VEC> V;
   typedef GateRaw<TIO, VEC, GM> GR;
@@ -259,11 +290,10 @@ __global__ __launch_bounds__(kFwdThreads) void k_scan_fwd(const ScanParams p) {
   __shared__ float sA[LY][CT], sS[LY][CT], pA[kFwdThreads], pS[kFwdThreads];
   __shared__ int slot;
   const int tid = threadIdx.x, lx = tid % LX, ly = tid / LX;
-  const int cstep = tile_channels<GM>(CT, p.D);
-  const int nct = (p.C + cstep - 1) / cstep, ct = blockIdx.x % nct;
-  const int cbase = ct * cstep, nc = min(p.C - cbase, cstep);
-  int row;
-  const ScanTile tile = tile_at<TT, bwd_tile(GM)>(p, take_order(p, ct, nct, &slot), false, row);
+  const int nct = channel_tiles<GM>(CT, p.C, p.D), ct = blockIdx.x % nct;
+  int cbase, nc, row;
+  channel_tile<GM, VEC>(CT, p.C, p.D, nct, ct, cbase, nc);
+  const ScanTile tile = tile_at<TT, kSaved>(p, take_order(p, ct, nct, &slot), false, row);
   const int c = tid % CT, part = tid / CT;   // the channel this thread composes, and its share
   const bool lead = part == 0 && c < nc;
   const int64_t sc = int64_t(tile.seq) * p.C + cbase + c;
@@ -273,7 +303,7 @@ __global__ __launch_bounds__(kFwdThreads) void k_scan_fwd(const ScanParams p) {
     return;
   }
   const bool on = lx * VEC < nc;
-  const int c0 = cbase + (on ? lx * VEC : 0);
+  const int v0 = min(lx * VEC, nc - VEC), c0 = cbase + v0;   // idle lanes repeat the last vector
   float a[L][VEC], u[L][VEC];
   {
     typename GR::Raw rg[L];
@@ -318,7 +348,7 @@ __global__ __launch_bounds__(kFwdThreads) void k_scan_fwd(const ScanParams p) {
         A[v] *= a[i][v];
       }
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) { sA[ly][lx * VEC + v] = A[v]; sS[ly][lx * VEC + v] = S[v]; }
+    for (int v = 0; v < VEC; ++v) { sA[ly][v0 + v] = A[v]; sS[ly][v0 + v] = S[v]; }
   }
   __syncthreads();
   // one thread per channel composes the groups; the other threads of the channel
@@ -343,8 +373,8 @@ __global__ __launch_bounds__(kFwdThreads) void k_scan_fwd(const ScanParams p) {
     float* saved = p.carry + int64_t(tile.saved) * p.C + cbase + c;
 #pragma unroll
     for (int y = 0; y < LY; ++y) {
-      constexpr int kPer = bwd_tile(GM) / L;   // groups per backward tile
-      static_assert(kPer * L == bwd_tile(GM) && TT % bwd_tile(GM) == 0, "saved states at group borders");
+      constexpr int kPer = kSaved / L;   // groups per backward tile
+      static_assert(kPer * L == kSaved && TT % kSaved == 0, "saved states at group borders");
       if (y % kPer == 0 && y * L < tile.len) saved[int64_t(y / kPer) * p.C] = s;
       const float Sy = sS[y][c];
       sS[y][c] = s;
@@ -356,7 +386,7 @@ __global__ __launch_bounds__(kFwdThreads) void k_scan_fwd(const ScanParams p) {
   __syncthreads();
   float y[VEC];
 #pragma unroll
-  for (int v = 0; v < VEC; ++v) y[v] = sS[ly][lx * VEC + v];
+  for (int v = 0; v < VEC; ++v) y[v] = sS[ly][v0 + v];
 #pragma unroll
   for (int i = 0; i < L; ++i) {
     const int r = ly * L + i;
@@ -368,7 +398,7 @@ __global__ __launch_bounds__(kFwdThreads) void k_scan_fwd(const ScanParams p) {
 
 template <typename TIO, int VEC, int LX, int GM, bool CONVEX>
 __global__ __launch_bounds__(kBwdThreads, 2) void k_scan_bwd(const ScanParams p) {
-  constexpr int TT = bwd_tile(GM);
+  constexpr int TT = bwd_tile(GM, LX * VEC > 128);
   typedef Geo<VEC, LX, kBwdThreads, TT> G;
   typedef Vec<TIO, VEC> V;
   typedef GateRaw<TIO, VEC, GM> GR;
@@ -379,10 +409,9 @@ __global__ __launch_bounds__(kBwdThreads, 2) void k_scan_bwd(const ScanParams p)
   __shared__ float sG[GM == kScanHeadLog ? TT : 1][LX + 1];
   __shared__ int slot;
   const int tid = threadIdx.x, lx = tid % LX, ly = tid / LX;
-  const int cstep = tile_channels<GM>(CT, p.D);
-  const int nct = (p.C + cstep - 1) / cstep, ct = blockIdx.x % nct;
-  const int cbase = ct * cstep, nc = min(p.C - cbase, cstep);
-  int row;
+  const int nct = channel_tiles<GM>(CT, p.C, p.D), ct = blockIdx.x % nct;
+  int cbase, nc, row;
+  channel_tile<GM, VEC>(CT, p.C, p.D, nct, ct, cbase, nc);
   const ScanTile tile = tile_at<TT, TT>(p, take_order(p, ct, nct, &slot), true, row);
   const int c = tid % CT, part = tid / CT;
   const bool lead = part == 0 && c < nc;
@@ -394,7 +423,7 @@ __global__ __launch_bounds__(kBwdThreads, 2) void k_scan_bwd(const ScanParams p)
     return;
   }
   const bool on = lx * VEC < nc;
-  const int c0 = cbase + (on ? lx * VEC : 0);
+  const int v0 = min(lx * VEC, nc - VEC), c0 = cbase + v0;   // idle lanes repeat the last vector
   // per token: the decay, its base-2 logarithm, the gate's slope, the input; `u`
   // becomes the state before the token
   float a[L][VEC], l[kLog ? L : 1][VEC], dz[kPar ? L : 1][VEC], u[L][VEC];
@@ -459,9 +488,9 @@ __global__ __launch_bounds__(kBwdThreads, 2) void k_scan_bwd(const ScanParams p)
     }
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
-      sA[ly][lx * VEC + v] = A[v];
-      sS[ly][lx * VEC + v] = S[v];
-      sE[ly][lx * VEC + v] = E[v];
+      sA[ly][v0 + v] = A[v];
+      sS[ly][v0 + v] = S[v];
+      sE[ly][v0 + v] = E[v];
     }
   }
   __syncthreads();
@@ -506,8 +535,8 @@ __global__ __launch_bounds__(kBwdThreads, 2) void k_scan_bwd(const ScanParams p)
     float s[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
-      s[v] = sS[ly][lx * VEC + v];
-      e[v] = sE[ly][lx * VEC + v];
+      s[v] = sS[ly][v0 + v];
+      e[v] = sE[ly][v0 + v];
       sumz[v] = sumA[v] = 0.f;
     }
 #pragma unroll
@@ -575,7 +604,7 @@ __global__ __launch_bounds__(kBwdThreads, 2) void k_scan_bwd(const ScanParams p)
   if constexpr (kPar) {
     __syncthreads();
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) { sS[ly][lx * VEC + v] = sumz[v]; sE[ly][lx * VEC + v] = sumA[v]; }
+    for (int v = 0; v < VEC; ++v) { sS[ly][v0 + v] = sumz[v]; sE[ly][v0 + v] = sumA[v]; }
     __syncthreads();
     if (lead) {
       float z = 0.f, zA = 0.f;
@@ -720,8 +749,7 @@ __global__ __launch_bounds__(256) void k_scan_step(const ScanStepParams p) {
 
 template <typename TIO, int VEC, int LX, int GM, bool CONVEX>
 int launch_convex(const ScanParams& p, bool backward, hipStream_t s) {
-  const int cstep = tile_channels<GM>(LX * VEC, p.D);
-  const int64_t blocks = int64_t(p.NT) * ((p.C + cstep - 1) / cstep);
+  const int64_t blocks = int64_t(p.NT) * channel_tiles<GM>(LX * VEC, p.C, p.D);
   if (backward) k_scan_bwd<TIO, VEC, LX, GM, CONVEX><<<dim3(unsigned(blocks)), kBwdThreads, 0, s>>>(p);
   else k_scan_fwd<TIO, VEC, LX, GM, CONVEX><<<dim3(unsigned(blocks)), kFwdThreads, 0, s>>>(p);
   return static_cast<int>(hipGetLastError());
@@ -733,16 +761,16 @@ int launch_variant(const ScanParams& p, bool backward, hipStream_t s) {
                   : launch_convex<TIO, VEC, LX, GM, false>(p, backward, s);
 }
 
-// Vectors of 16 bytes where every row starts on one; one channel a lane otherwise
-// (only D = 1 layers with an odd channel count).
 template <typename TIO, int GM>
 int launch_gate(const ScanParams& p, bool backward, hipStream_t s) {
-  constexpr int VEC = sizeof(TIO) == 2 ? 8 : 4;
+  constexpr int VEC = 16 / sizeof(TIO);
   if constexpr (GM == kScanHeadLog) {
+    // heads wider than 128 channels need a tile that holds one
     if (p.D > 128) return launch_variant<TIO, VEC, 256 / VEC, GM>(p, backward, s);
     return launch_variant<TIO, VEC, 128 / VEC, GM>(p, backward, s);
   } else {
-    if (p.C % VEC) return launch_variant<TIO, 1, 64, GM>(p, backward, s);
+    // less than a vector of channels in all: one channel a lane
+    if (p.C < VEC) return launch_variant<TIO, 1, 64, GM>(p, backward, s);
     return launch_variant<TIO, VEC, 128 / VEC, GM>(p, backward, s);
   }
 }
@@ -817,7 +845,7 @@ int launch_scan_tables(const ScanParams& p, int TT, const ScanBatch& b, void* st
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   (void)hipGetLastError();
   if (b.n <= 0) return 0;
-  k_scan_tables<<<dim3(b.n), 64, 0, s>>>(p.tab, TT, bwd_tile(p.gate), b);
+  k_scan_tables<<<dim3(b.n), 64, 0, s>>>(p.tab, TT, bwd_tile(p.gate, p.D > 128), b);
   return static_cast<int>(hipGetLastError());
 }
 
