@@ -69,7 +69,7 @@ gdr_status check_scan_shape(const gdr_scan_shape* s, int64_t* NT_out) {
   if (s->D > 256 || (s->D != 1 && s->D % 8 != 0))
     return set_error(GDR_EUNSUPPORTED, "head dim %d must be 1 or a multiple of 8 up to 256", s->D);
   int64_t NT = 0;
-  const int tile = gdr::bwd_tile(scan_gate(s), s->D > 128);
+  const int tile = gdr::bwd_tile(scan_gate(s), s->D > 128, s->convex);
   if (s->cu_seqlens_host == nullptr) {
     if (s->N != s->B) return set_error(GDR_EINVAL, "dense shape needs N == B (N=%d, B=%d)", s->N, s->B);
     NT = int64_t(s->B) * tiles_of(s->T, tile);
@@ -86,7 +86,7 @@ gdr_status check_scan_shape(const gdr_scan_shape* s, int64_t* NT_out) {
     if (cu[s->N] != s->T) return set_error(GDR_EINVAL, "cu_seqlens[N] = %lld != T = %d", (long long)cu[s->N], s->T);
   }
   const int64_t C = int64_t(s->H) * s->D, tokens = int64_t(s->B) * s->T;
-  if (C >= (int64_t(1) << 24) || tokens >= (int64_t(1) << 31) || tokens * C >= (int64_t(1) << 40) ||
+  if (C > (int64_t(1) << 21) || tokens >= (int64_t(1) << 31) || tokens * C >= (int64_t(1) << 40) ||
       NT * ((C + 63) / 64) >= (int64_t(1) << 31))
     return set_error(GDR_EUNSUPPORTED, "problem too large for 32-bit tile indexing");
   *NT_out = NT;
@@ -171,7 +171,7 @@ gdr_status scan_prologue(const gdr_scan_shape* s, const gdr::ScanParams& p, int 
       b.tile0[i] = int32_t(row);
       b.saved0[i] = int32_t(saved);
       row += tiles_of(len, tile);
-      saved += tiles_of(len, gdr::bwd_tile(p.gate, p.D > 128));
+      saved += tiles_of(len, gdr::bwd_tile(p.gate, p.D > 128, p.convex));
     }
     const gdr_status st = hip_status(gdr::launch_scan_tables(p, tile, b, stream), "tile table kernel");
     if (st != GDR_OK) return st;
@@ -276,7 +276,7 @@ gdr_status gdr_scan_bwd(const gdr_scan_shape* shape, const gdr_scan_inputs* in, 
   gdr::ScanParams p = scan_params(shape, in, NT, L, ws);
   p.dy = dy; p.dht = dht;
   p.dx = grads->dx; p.dg = grads->dg; p.dh0 = grads->dh0; p.dA_log = grads->dA_log; p.ddt_bias = grads->ddt_bias;
-  if ((st = scan_prologue(shape, p, gdr::bwd_tile(p.gate, p.D > 128), stream)) != GDR_OK) return st;
+  if ((st = scan_prologue(shape, p, gdr::bwd_tile(p.gate, p.D > 128, p.convex), stream)) != GDR_OK) return st;
   if ((st = hip_status(gdr::launch_scan(p, true, stream), "scan gradient kernel")) != GDR_OK) return st;
   return par ? hip_status(gdr::launch_scan_params(p, stream), "parameter reduction kernel") : GDR_OK;
 }

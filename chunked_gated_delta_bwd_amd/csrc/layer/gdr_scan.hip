@@ -29,6 +29,7 @@
 #include <algorithm>
 
 #include "../gdr_device.h"
+#include "../gdr_lds.h"
 #include "gdr_gate.h"
 #include "gdr_layer.h"
 #include "gdr_wide.h"
@@ -68,14 +69,14 @@ __device__ __forceinline__ float lo_of(uint64_t w) { return __uint_as_float(uint
 // there (the nearest is the last to come): the states' front advances by up to W
 // tiles, over all threads of a channel, per trip to memory.
 template <int W>
-__device__ __forceinline__ bool fold_words(const uint64_t* w, int64_t step, int count, int k0, int c, float& A, float& S) {
+__device__ __forceinline__ bool fold_words(const uint64_t* w, int step, int count, int k0, int c, float& A, float& S) {
   uint64_t x[W];
   for (int polls = 0;; ++polls) {
     // one word a poll: polling all W of them slows the stores that are waited for
-    if (hi_of(get(w + step * k0 + c)) != kNothing) {
+    if (hi_of(get(w + int64_t(step) * k0 + c)) != kNothing) {
       bool ready = true;
 #pragma unroll
-      for (int i = 0; i < W; ++i) x[i] = get(w + step * min(k0 + i, count - 1) + c);
+      for (int i = 0; i < W; ++i) x[i] = get(w + int64_t(step) * min(k0 + i, count - 1) + c);
 #pragma unroll
       for (int i = 0; i < W; ++i) ready &= hi_of(x[i]) != kNothing;
       if (ready) break;
@@ -117,7 +118,7 @@ __device__ __forceinline__ float look_back(const uint64_t* w, int64_t step, int 
       pA[part * CT + c] = done ? __uint_as_float(kState) : A;
       pS[part * CT + c] = S;
     }
-    __syncthreads();
+    chain_barrier();
   }
   if (part > 0 || !on) return 0.f;
 #pragma unroll
@@ -144,9 +145,7 @@ struct Vec {
   static_assert(VEC * sizeof(TIO) == 16, "16-byte vectors");
   typedef u32x4 Raw;
   typedef typename Wide<TIO>::T Any;
-  static __device__ __forceinline__ Raw load(const void* b, int64_t o) {
-    return *reinterpret_cast<const Any*>(static_cast<const TIO*>(b) + o);
-  }
+  static __device__ __forceinline__ Raw load(const TIO* b, uint32_t o) { return *reinterpret_cast<const Any*>(b + o); }
   static __device__ __forceinline__ void unpack(const Raw& u, float (&x)[VEC]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -158,7 +157,7 @@ struct Vec {
       }
     }
   }
-  static __device__ __forceinline__ void store(void* b, int64_t o, const float (&x)[VEC]) {
+  static __device__ __forceinline__ void store(TIO* b, uint32_t o, const float (&x)[VEC]) {
     Raw u;
     if constexpr (VEC == 8) {
       const uint2 lo = pack4_bf16(x[0], x[1], x[2], x[3]), hi = pack4_bf16(x[4], x[5], x[6], x[7]);
@@ -167,15 +166,15 @@ struct Vec {
 #pragma unroll
       for (int i = 0; i < 4; ++i) u[i] = __float_as_uint(x[i]);
     }
-    *reinterpret_cast<Any*>(static_cast<TIO*>(b) + o) = u;
+    *reinterpret_cast<Any*>(b + o) = u;
   }
 };
 template <typename TIO>
 struct Vec<TIO, 1> {
   typedef float Raw;
-  static __device__ __forceinline__ Raw load(const void* b, int64_t o) { return IO<TIO>::load1(b, o); }
+  static __device__ __forceinline__ Raw load(const TIO* b, uint32_t o) { return IO<TIO>::load1(b, o); }
   static __device__ __forceinline__ void unpack(const Raw& r, float (&x)[1]) { x[0] = r; }
-  static __device__ __forceinline__ void store(void* b, int64_t o, const float (&x)[1]) { IO<TIO>::store1(b, o, x[0]); }
+  static __device__ __forceinline__ void store(TIO* b, uint32_t o, const float (&x)[1]) { IO<TIO>::store1(b, o, x[0]); }
 };
 
 // Geometry of a variant.
@@ -231,8 +230,8 @@ __device__ __forceinline__ ScanTile tile_at(const ScanParams& p, int order, bool
 __device__ __forceinline__ int take_order(const ScanParams& p, int ct, int nct, int* slot) {
   if (!p.words) return blockIdx.x / nct;
   if (threadIdx.x == 0) *slot = int(atomicAdd(p.counters + int64_t(ct) * kScanCounterStep, 1u));
-  __syncthreads();
-  return *slot;
+  chain_barrier();
+  return __builtin_amdgcn_readfirstlane(*slot);   // the same for all: keep it scalar
 }
 
 // The gate of VEC channels: base-2 log decays, and what its gradient needs.
@@ -241,10 +240,16 @@ struct Gate {
   float eA[VEC], bias[VEC];
   __device__ __forceinline__ void init(const ScanParams& p, int c0) {
     if constexpr (GM == kScanSoftplus || GM == kScanSigmoid) {
+      // heads of several channels hold whole vectors: one A_log a thread
+      const float e0 = fast_exp2(p.A_log[c0 / p.D] * kLog2e);
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
-        eA[v] = expf(p.A_log[(c0 + v) / p.D]);
+        eA[v] = e0;
         bias[v] = p.dt_bias[c0 + v] * kLog2e;
+      }
+      if (p.D == 1) {
+#pragma unroll
+        for (int v = 1; v < VEC; ++v) eA[v] = fast_exp2(p.A_log[c0 + v] * kLog2e);
       }
     }
   }
@@ -255,20 +260,27 @@ struct Gate {
   }
 };
 
-// Raw gate values of one token: VEC of them, or the head's one.
+// Raw gate values of row r of a tile: VEC of them, or the head's one.  `first`: the
+// gate's first element of the tile.
 template <typename TIO, int VEC, int GM>
 struct GateRaw {
   typedef typename Vec<TIO, VEC>::Raw Raw;
-  static __device__ __forceinline__ Raw load(const ScanParams& p, int64_t t, int c0) {
-    return Vec<TIO, VEC>::load(p.g, t * p.C + c0);
+  static __device__ __forceinline__ const TIO* first(const void* g, int64_t t, int C, int H) {
+    return static_cast<const TIO*>(g) + t * C;
+  }
+  static __device__ __forceinline__ Raw load(const TIO* first, uint32_t r, int C, int H, int c0, int h) {
+    return Vec<TIO, VEC>::load(first, r * C + c0);
   }
   static __device__ __forceinline__ void unpack(const Raw& r, float (&g)[VEC]) { Vec<TIO, VEC>::unpack(r, g); }
 };
 template <typename TIO, int VEC>
 struct GateRaw<TIO, VEC, kScanHeadLog> {
   typedef float Raw;
-  static __device__ __forceinline__ Raw load(const ScanParams& p, int64_t t, int c0) {
-    return IO<TIO>::load1(p.g, t * p.H + c0 / p.D);
+  static __device__ __forceinline__ const TIO* first(const void* g, int64_t t, int C, int H) {
+    return static_cast<const TIO*>(g) + t * H;
+  }
+  static __device__ __forceinline__ Raw load(const TIO* first, uint32_t r, int C, int H, int c0, int h) {
+    return IO<TIO>::load1(first, r * H + h);
   }
   static __device__ __forceinline__ void unpack(const Raw& r, float (&g)[VEC]) {
 #pragma unroll
@@ -276,13 +288,24 @@ struct GateRaw<TIO, VEC, kScanHeadLog> {
   }
 };
 
+// First element of token row t of a [tokens][C] tensor.
+template <typename TIO> __device__ __forceinline__ const TIO* row_at(const void* b, int64_t t, int C) {
+  return static_cast<const TIO*>(b) + t * C;
+}
+template <typename TIO> __device__ __forceinline__ TIO* row_at(void* b, int64_t t, int C) {
+  return static_cast<TIO*>(b) + t * C;
+}
+
 // Both kernels keep their loads in bounds without branches: rows past the tile's
 // end and lanes past its channels load a valid neighbour's values, and the rows past
 // the end are then made neutral (a = 1, no input), in a loop of its own that full
-// tiles skip.
+// tiles skip.  Barriers order LDS only.  A workgroup handles one tile; workgroups that
+// stay and load their next tile's inputs ahead measured no faster (117 us at best for
+// the forward of T = 32768, 16 heads of 128: the registers halve the tile) and are
+// not kept.
 template <typename TIO, int VEC, int LX, int GM, bool CONVEX>
 __global__ __launch_bounds__(kFwdThreads) void k_scan_fwd(const ScanParams p) {
-  constexpr int TT = fwd_tile(GM, LX * VEC > 128), kSaved = bwd_tile(GM, LX * VEC > 128);
+  constexpr int TT = fwd_tile(GM, LX * VEC > 128), kSaved = bwd_tile(GM, LX * VEC > 128, CONVEX);
   typedef Geo<VEC, LX, kFwdThreads, TT> G;
   typedef Vec<TIO, VEC> V;
   typedef GateRaw<TIO, VEC, GM> GR;
@@ -291,31 +314,39 @@ __global__ __launch_bounds__(kFwdThreads) void k_scan_fwd(const ScanParams p) {
   __shared__ int slot;
   const int tid = threadIdx.x, lx = tid % LX, ly = tid / LX;
   const int nct = channel_tiles<GM>(CT, p.C, p.D), ct = blockIdx.x % nct;
-  int cbase, nc, row;
+  int cbase, nc;
   channel_tile<GM, VEC>(CT, p.C, p.D, nct, ct, cbase, nc);
-  const ScanTile tile = tile_at<TT, kSaved>(p, take_order(p, ct, nct, &slot), false, row);
   const int c = tid % CT, part = tid / CT;   // the channel this thread composes, and its share
   const bool lead = part == 0 && c < nc;
-  const int64_t sc = int64_t(tile.seq) * p.C + cbase + c;
-  if (tile.len == 0) {
-    // a sequence without tokens: its state passes through
-    if (lead && p.ht) p.ht[sc] = p.h0 ? p.h0[sc] : 0.f;
-    return;
-  }
   const bool on = lx * VEC < nc;
   const int v0 = min(lx * VEC, nc - VEC), c0 = cbase + v0;   // idle lanes repeat the last vector
-  float a[L][VEC], u[L][VEC];
+  const int head = GM == kScanHeadLog ? c0 / p.D : 0;
+  Gate<VEC, GM> gate;
+  gate.init(p, c0);
+  int row;
+  const ScanTile tile = tile_at<TT, kSaved>(p, take_order(p, ct, nct, &slot), false, row);
+  const int64_t sc = int64_t(tile.seq) * p.C + cbase + c;
+  float s = 0.f;   // the tile's starting state, known to the lead threads
+  if (tile.idx == 0 && p.h0 && lead) s = p.h0[sc];
+  if (tile.len == 0) {
+    // a sequence without tokens: its state passes through
+    if (lead && p.ht) p.ht[sc] = s;
+    return;
+  }
+  typename GR::Raw rg[L];
+  typename V::Raw rx[L];
   {
-    typename GR::Raw rg[L];
-    typename V::Raw rx[L];
+    const TIO* g = GR::first(p.g, tile.t_start, p.C, p.H);
+    const TIO* x = row_at<TIO>(p.x, tile.t_start, p.C);
 #pragma unroll
     for (int i = 0; i < L; ++i) {
-      const int64_t t = int64_t(tile.t_start) + min(ly * L + i, tile.len - 1);
-      rg[i] = GR::load(p, t, c0);
-      rx[i] = V::load(p.x, t * p.C + c0);
+      const uint32_t r = min(ly * L + i, tile.len - 1);
+      rg[i] = GR::load(g, r, p.C, p.H, c0, head);
+      rx[i] = V::load(x, r * p.C + c0);
     }
-    Gate<VEC, GM> gate;
-    gate.init(p, c0);
+  }
+  float a[L][VEC], u[L][VEC];
+  {
 #pragma unroll
     for (int i = 0; i < L; ++i) {
       float g[VEC];
@@ -350,7 +381,7 @@ __global__ __launch_bounds__(kFwdThreads) void k_scan_fwd(const ScanParams p) {
 #pragma unroll
     for (int v = 0; v < VEC; ++v) { sA[ly][v0 + v] = A[v]; sS[ly][v0 + v] = S[v]; }
   }
-  __syncthreads();
+  chain_barrier();
   // one thread per channel composes the groups; the other threads of the channel
   // (PARTS in all) share the look back
   uint64_t* w = p.words + int64_t(row) * p.C + cbase;
@@ -363,12 +394,7 @@ __global__ __launch_bounds__(kFwdThreads) void k_scan_fwd(const ScanParams p) {
     }
     put_fold(w + c, At, St);
   }
-  float s = 0.f;
-  if (tile.idx == 0) {
-    if (p.h0 && lead) s = p.h0[sc];
-  } else {
-    s = look_back<CT, G::PARTS>(w - p.C, -int64_t(p.C), tile.idx, c, c < nc, part, pA, pS);
-  }
+  if (tile.idx > 0) s = look_back<CT, G::PARTS>(w - p.C, -int64_t(p.C), tile.idx, c, c < nc, part, pA, pS);
   if (lead) {
     float* saved = p.carry + int64_t(tile.saved) * p.C + cbase + c;
 #pragma unroll
@@ -383,7 +409,8 @@ __global__ __launch_bounds__(kFwdThreads) void k_scan_fwd(const ScanParams p) {
     if (tile.after > 0) put_state(w + c, s);
     else if (p.ht) p.ht[sc] = s;
   }
-  __syncthreads();
+  chain_barrier();
+  TIO* out = row_at<TIO>(p.y, tile.t_start, p.C);
   float y[VEC];
 #pragma unroll
   for (int v = 0; v < VEC; ++v) y[v] = sS[ly][v0 + v];
@@ -392,13 +419,13 @@ __global__ __launch_bounds__(kFwdThreads) void k_scan_fwd(const ScanParams p) {
     const int r = ly * L + i;
 #pragma unroll
     for (int v = 0; v < VEC; ++v) y[v] = fmaf(a[i][v], y[v], u[i][v]);
-    if (on && r < tile.len) V::store(p.y, (int64_t(tile.t_start) + r) * p.C + c0, y);
+    if (on && r < tile.len) V::store(out, uint32_t(r) * p.C + c0, y);
   }
 }
 
 template <typename TIO, int VEC, int LX, int GM, bool CONVEX>
 __global__ __launch_bounds__(kBwdThreads, 2) void k_scan_bwd(const ScanParams p) {
-  constexpr int TT = bwd_tile(GM, LX * VEC > 128);
+  constexpr int TT = bwd_tile(GM, LX * VEC > 128, CONVEX);
   typedef Geo<VEC, LX, kBwdThreads, TT> G;
   typedef Vec<TIO, VEC> V;
   typedef GateRaw<TIO, VEC, GM> GR;
@@ -410,49 +437,62 @@ __global__ __launch_bounds__(kBwdThreads, 2) void k_scan_bwd(const ScanParams p)
   __shared__ int slot;
   const int tid = threadIdx.x, lx = tid % LX, ly = tid / LX;
   const int nct = channel_tiles<GM>(CT, p.C, p.D), ct = blockIdx.x % nct;
-  int cbase, nc, row;
+  int cbase, nc;
   channel_tile<GM, VEC>(CT, p.C, p.D, nct, ct, cbase, nc);
-  const ScanTile tile = tile_at<TT, TT>(p, take_order(p, ct, nct, &slot), true, row);
   const int c = tid % CT, part = tid / CT;
   const bool lead = part == 0 && c < nc;
+  const bool on = lx * VEC < nc;
+  const int v0 = min(lx * VEC, nc - VEC), c0 = cbase + v0;
+  const int head = GM == kScanHeadLog ? c0 / p.D : 0;
+  Gate<VEC, GM> gate;
+  gate.init(p, c0);
+  int row;
+  const ScanTile tile = tile_at<TT, TT>(p, take_order(p, ct, nct, &slot), true, row);
+  // the state before the tile, and what the reverse recurrence brings from after it
   const int64_t sc = int64_t(tile.seq) * p.C + cbase + c;
   float* partial = p.part + int64_t(row) * 2 * p.C + cbase + c;
+  float s0 = 0.f, e0 = 0.f;
+  if (tile.after == 0 && p.dht && lead) e0 = p.dht[sc];
   if (tile.len == 0) {
-    if (lead && p.dh0) p.dh0[sc] = p.dht ? p.dht[sc] : 0.f;
+    if (lead && p.dh0) p.dh0[sc] = e0;
     if (kPar && lead) partial[0] = partial[p.C] = 0.f;
     return;
   }
-  const bool on = lx * VEC < nc;
-  const int v0 = min(lx * VEC, nc - VEC), c0 = cbase + v0;   // idle lanes repeat the last vector
+  if (lead) s0 = p.carry[int64_t(tile.saved) * p.C + cbase + c];
+  typename GR::Raw rg[L];
+  typename V::Raw rx[L], rdy[L];
+  {
+    const TIO* g = GR::first(p.g, tile.t_start, p.C, p.H);
+    const TIO* x = row_at<TIO>(p.x, tile.t_start, p.C);
+    const TIO* dy = row_at<TIO>(p.dy, tile.t_start, p.C);
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+      const uint32_t r = min(ly * L + i, tile.len - 1);
+      rg[i] = GR::load(g, r, p.C, p.H, c0, head);
+      rx[i] = V::load(x, r * p.C + c0);
+      rdy[i] = V::load(dy, r * p.C + c0);
+    }
+  }
   // per token: the decay, its base-2 logarithm, the gate's slope, the input; `u`
   // becomes the state before the token
   float a[L][VEC], l[kLog ? L : 1][VEC], dz[kPar ? L : 1][VEC], u[L][VEC];
-  typename GR::Raw rg[L];
-  typename V::Raw rx[L], rdy[L];
+  {
 #pragma unroll
-  for (int i = 0; i < L; ++i) {
-    const int64_t t = int64_t(tile.t_start) + min(ly * L + i, tile.len - 1);
-    rg[i] = GR::load(p, t, c0);
-    rx[i] = V::load(p.x, t * p.C + c0);
-    rdy[i] = V::load(p.dy, t * p.C + c0);
-  }
-  Gate<VEC, GM> gate;
-  gate.init(p, c0);
+    for (int i = 0; i < L; ++i) {
+      float g[VEC];
+      GR::unpack(rg[i], g);
+      V::unpack(rx[i], u[i]);
 #pragma unroll
-  for (int i = 0; i < L; ++i) {
-    float g[VEC];
-    GR::unpack(rg[i], g);
-    V::unpack(rx[i], u[i]);
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-      float l2;
-      if constexpr (kPar)
-        gate_log2_grad<GM == kScanSoftplus ? 0 : 1>(fmaf(g[v], kLog2e, gate.bias[v]), gate.eA[v], p.gate_scale, l2,
-                                                     dz[i][v]);
-      else l2 = g[v] * kLog2e;
-      a[i][v] = fast_exp2(l2);
-      if constexpr (kLog) l[i][v] = l2;
-      if constexpr (CONVEX) u[i][v] *= one_minus_exp2(l2, a[i][v]);
+      for (int v = 0; v < VEC; ++v) {
+        float l2;
+        if constexpr (kPar)
+          gate_log2_grad<GM == kScanSoftplus ? 0 : 1>(fmaf(g[v], kLog2e, gate.bias[v]), gate.eA[v], p.gate_scale, l2,
+                                                       dz[i][v]);
+        else l2 = g[v] * kLog2e;
+        a[i][v] = fast_exp2(l2);
+        if constexpr (kLog) l[i][v] = l2;
+        if constexpr (CONVEX) u[i][v] *= one_minus_exp2(l2, a[i][v]);
+      }
     }
   }
   if (tile.len < TT) {
@@ -465,6 +505,7 @@ __global__ __launch_bounds__(kBwdThreads, 2) void k_scan_bwd(const ScanParams p)
           a[i][v] = 1.f;
           u[i][v] = 0.f;
           if constexpr (kPar) dz[i][v] = 0.f;
+          if constexpr (kLog) l[i][v] = 0.f;
         }
       }
   }
@@ -493,26 +534,18 @@ __global__ __launch_bounds__(kBwdThreads, 2) void k_scan_bwd(const ScanParams p)
       sE[ly][v0 + v] = E[v];
     }
   }
-  __syncthreads();
+  chain_barrier();
   uint64_t* w = p.words + int64_t(row) * p.C + cbase;
-  float s0 = 0.f, e0 = 0.f;
-  if (lead) {
-    s0 = p.carry[int64_t(tile.saved) * p.C + cbase + c];
-    if (tile.idx > 0 && tile.after > 0) {
-      float At = 1.f, Et = 0.f;
+  if (lead && tile.idx > 0 && tile.after > 0) {
+    float At = 1.f, Et = 0.f;
 #pragma unroll
-      for (int y = LY - 1; y >= 0; --y) {
-        Et = fmaf(sA[y][c], Et, sE[y][c]);
-        At *= sA[y][c];
-      }
-      put_fold(w + c, At, Et);
+    for (int y = LY - 1; y >= 0; --y) {
+      Et = fmaf(sA[y][c], Et, sE[y][c]);
+      At *= sA[y][c];
     }
+    put_fold(w + c, At, Et);
   }
-  if (tile.after == 0) {
-    if (p.dht && lead) e0 = p.dht[sc];
-  } else {
-    e0 = look_back<CT, G::PARTS>(w + p.C, p.C, tile.after, c, c < nc, part, pA, pS);
-  }
+  if (tile.after > 0) e0 = look_back<CT, G::PARTS>(w + p.C, p.C, tile.after, c, c < nc, part, pA, pS);
   if (lead) {
 #pragma unroll
     for (int y = LY - 1; y >= 0; --y) {
@@ -529,7 +562,7 @@ __global__ __launch_bounds__(kBwdThreads, 2) void k_scan_bwd(const ScanParams p)
       s0 = fmaf(sA[y][c], s0, Sy);
     }
   }
-  __syncthreads();
+  chain_barrier();
   float e[VEC], sumz[VEC], sumA[VEC];
   {
     float s[VEC];
@@ -571,13 +604,11 @@ __global__ __launch_bounds__(kBwdThreads, 2) void k_scan_bwd(const ScanParams p)
       if constexpr (kPar) {
         dg[v] = dl * dz[i][v];
         // d lambda / d A_log: lambda, or the slope by z times z; rows past the end
-        // have a slope of zero, and a lambda to be left out
-        if constexpr (GM == kScanSoftplus) {
-          const float lam = fmaxf(l[i][v], -3.0e38f);
-          sumA[v] = fmaf(r < tile.len ? dl : 0.f, lam, sumA[v]);
-        } else {
+        // have neither
+        if constexpr (GM == kScanSoftplus)
+          sumA[v] = fmaf(dl, fmaxf(l[i][v], -3.0e38f), sumA[v]);
+        else
           sumA[v] = fmaf(dg[v], fminf(fmaxf(fmaf(g[v], kLog2e, gate.bias[v]), -3.0e38f), 3.0e38f), sumA[v]);
-        }
         sumz[v] += dg[v];
       } else {
         dg[v] = dl;
@@ -585,14 +616,13 @@ __global__ __launch_bounds__(kBwdThreads, 2) void k_scan_bwd(const ScanParams p)
       }
     }
     if (on && r < tile.len) {
-      const int64_t t = int64_t(tile.t_start) + r;
-      V::store(p.dx, t * p.C + c0, dx);
-      if constexpr (GM != kScanHeadLog) V::store(p.dg, t * p.C + c0, dg);
+      V::store(row_at<TIO>(p.dx, tile.t_start, p.C), uint32_t(r) * p.C + c0, dx);
+      if constexpr (GM != kScanHeadLog) V::store(row_at<TIO>(p.dg, tile.t_start, p.C), uint32_t(r) * p.C + c0, dg);
     }
     if constexpr (GM == kScanHeadLog) sG[r][lx] = dsum;
   }
   if constexpr (GM == kScanHeadLog) {
-    __syncthreads();
+    chain_barrier();
     const int heads = nc / p.D, lanes = p.D / VEC, h0 = cbase / p.D;
     for (int i = tid; i < tile.len * heads; i += kBwdThreads) {
       const int r = i / heads, h = i - r * heads;
@@ -602,10 +632,10 @@ __global__ __launch_bounds__(kBwdThreads, 2) void k_scan_bwd(const ScanParams p)
     }
   }
   if constexpr (kPar) {
-    __syncthreads();
+    chain_barrier();
 #pragma unroll
     for (int v = 0; v < VEC; ++v) { sS[ly][v0 + v] = sumz[v]; sE[ly][v0 + v] = sumA[v]; }
-    __syncthreads();
+    chain_barrier();
     if (lead) {
       float z = 0.f, zA = 0.f;
 #pragma unroll
@@ -729,15 +759,16 @@ __global__ __launch_bounds__(256) void k_scan_step(const ScanStepParams p) {
   else IO<float>::load8(st, 0, s);
   for (;;) {
     float g[VEC], x[VEC];
-    GateRaw<TIO, VEC, GM>::unpack(GateRaw<TIO, VEC, GM>::load(q, n, c0), g);
-    Vec<TIO, VEC>::unpack(Vec<TIO, VEC>::load(p.x, int64_t(n) * p.C + c0), x);
+    typedef GateRaw<TIO, VEC, GM> GR;
+    GR::unpack(GR::load(GR::first(p.g, n, p.C, p.H), 0, p.C, p.H, c0, GM == kScanHeadLog ? c0 / p.D : 0), g);
+    Vec<TIO, VEC>::unpack(Vec<TIO, VEC>::load(row_at<TIO>(p.x, n, p.C), c0), x);
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
       const float l = gate.log2_decay(g[v], v, p.gate_scale);
       const float a = fast_exp2(l);
       s[v] = a * s[v] + (p.convex ? one_minus_exp2(l, a) * x[v] : x[v]);
     }
-    Vec<TIO, VEC>::store(p.y, int64_t(n) * p.C + c0, s);
+    Vec<TIO, VEC>::store(row_at<TIO>(p.y, n, p.C), c0, s);
     if (!later) break;
     do ++n; while (n < p.N && p.slots[n] != slot);
     if (n >= p.N) break;
@@ -749,9 +780,9 @@ __global__ __launch_bounds__(256) void k_scan_step(const ScanStepParams p) {
 
 template <typename TIO, int VEC, int LX, int GM, bool CONVEX>
 int launch_convex(const ScanParams& p, bool backward, hipStream_t s) {
-  const int64_t blocks = int64_t(p.NT) * channel_tiles<GM>(LX * VEC, p.C, p.D);
-  if (backward) k_scan_bwd<TIO, VEC, LX, GM, CONVEX><<<dim3(unsigned(blocks)), kBwdThreads, 0, s>>>(p);
-  else k_scan_fwd<TIO, VEC, LX, GM, CONVEX><<<dim3(unsigned(blocks)), kFwdThreads, 0, s>>>(p);
+  const dim3 grid(unsigned(int64_t(p.NT) * channel_tiles<GM>(LX * VEC, p.C, p.D)));
+  if (backward) k_scan_bwd<TIO, VEC, LX, GM, CONVEX><<<grid, kBwdThreads, 0, s>>>(p);
+  else k_scan_fwd<TIO, VEC, LX, GM, CONVEX><<<grid, kFwdThreads, 0, s>>>(p);
   return static_cast<int>(hipGetLastError());
 }
 
@@ -845,7 +876,7 @@ int launch_scan_tables(const ScanParams& p, int TT, const ScanBatch& b, void* st
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   (void)hipGetLastError();
   if (b.n <= 0) return 0;
-  k_scan_tables<<<dim3(b.n), 64, 0, s>>>(p.tab, TT, bwd_tile(p.gate, p.D > 128), b);
+  k_scan_tables<<<dim3(b.n), 64, 0, s>>>(p.tab, TT, bwd_tile(p.gate, p.D > 128, p.convex), b);
   return static_cast<int>(hipGetLastError());
 }
 
