@@ -72,8 +72,9 @@ template <int W>
 __device__ __forceinline__ bool fold_words(const uint64_t* w, int step, int count, int k0, int c, float& A, float& S) {
   uint64_t x[W];
   for (int polls = 0;; ++polls) {
-    // one word a poll: polling all W of them slows the stores that are waited for
-    if (hi_of(get(w + int64_t(step) * k0 + c)) != kNothing) {
+    // after the first try one word a poll, the nearest: polling all W of them slows
+    // the stores that are waited for (to a hundredth at W = 16)
+    if (polls == 0 || hi_of(get(w + int64_t(step) * k0 + c)) != kNothing) {
       bool ready = true;
 #pragma unroll
       for (int i = 0; i < W; ++i) x[i] = get(w + int64_t(step) * min(k0 + i, count - 1) + c);
@@ -101,7 +102,7 @@ __device__ __forceinline__ bool fold_words(const uint64_t* w, int step, int coun
   return done;
 }
 
-constexpr int kWindow = 4;   // words a thread loads at a time
+constexpr int kWindow = 2;   // words a thread loads at a time
 
 // The state that reaches a tile's channel c, known to its thread of part 0.  The
 // PARTS threads of the channel fold a window of words each, the nearest part 0's;
