@@ -60,83 +60,42 @@ __device__ __forceinline__ void put_state(uint64_t* w, float s) { put(w, kState,
 __device__ __forceinline__ uint32_t hi_of(uint64_t w) { return uint32_t(w >> 32); }
 __device__ __forceinline__ float lo_of(uint64_t w) { return __uint_as_float(uint32_t(w)); }
 
-// Folds W words of the `count` (at least one) before a tile (after it, in the
-// backward): from the k0-th nearest on.  w (the same for the whole workgroup) is the
-// nearest tile's row, each next row is `step` words on.  The farthest of the `count`
-// always publishes a state, and words past it stand for it.  With a state among the W
-// words S is the state that reaches the k0-th tile's far end and true is returned;
-// else (A, S) is their fold.  All words are loaded at once and again until all are
-// there (the nearest is the last to come): the states' front advances by up to W
-// tiles, over all threads of a channel, per trip to memory.
-template <int W>
-__device__ __forceinline__ bool fold_words(const uint64_t* w, int step, int count, int k0, int c, float& A, float& S) {
-  uint64_t x[W];
+// The state that reaches a tile of one channel from the `count` (at least one) tiles
+// before it (after it, in the backward): w + c is the nearest one's word and each
+// next one is `step` words on.  It waits for a published state among the nearest
+// kWindow and then takes it through the folds of the tiles between, one by one: the
+// same sums as if each tile had taken its neighbour's state, so how far the look back
+// went does not show in the result.  The states' front advances by up to kWindow
+// tiles per trip to memory.
+constexpr int kWindow = 8;   // 4: 117 us for T = 32768, 16 heads of 128; 8: 113; 16: 117 (twice the words)
+
+__device__ __forceinline__ float look_back(const uint64_t* w, int64_t step, int count, int c) {
+  const int n = min(kWindow, count);
+  uint64_t x[kWindow];
   for (int polls = 0;; ++polls) {
-    // after the first try one word a poll, the nearest: polling all W of them slows
-    // the stores that are waited for (to a hundredth at W = 16)
-    if (polls == 0 || hi_of(get(w + int64_t(step) * k0 + c)) != kNothing) {
-      bool ready = true;
+    // after the first try, two words a poll, the nearest fold (the last to come) and the
+    // farthest state (the first): polling all words slows the stores waited for, to a
+    // hundredth of the speed
+    if (polls == 0 ||
+        (hi_of(get(w + c)) != kNothing && hi_of(get(w + step * (n - 1) + c)) == kState)) {
+      bool state = false, hole = false;
 #pragma unroll
-      for (int i = 0; i < W; ++i) x[i] = get(w + int64_t(step) * min(k0 + i, count - 1) + c);
+      for (int i = 0; i < kWindow; ++i) x[i] = get(w + step * min(i, n - 1) + c);
 #pragma unroll
-      for (int i = 0; i < W; ++i) ready &= hi_of(x[i]) != kNothing;
-      if (ready) break;
+      for (int i = 0; i < kWindow; ++i) {
+        hole |= !state && hi_of(x[i]) == kNothing;
+        state |= hi_of(x[i]) == kState;
+      }
+      if (state && !hole) break;
     }
-    if (polls > kMaxPolls) {
-      S = __builtin_nanf("");
-      return true;
-    }
+    if (polls > kMaxPolls) return __builtin_nanf("");
     __builtin_amdgcn_s_sleep(4);
   }
-  A = 1.f;
-  S = 0.f;
-  bool done = false;
+  float s = 0.f;   // what lies beyond the nearest state is overwritten by it
 #pragma unroll
-  for (int i = W - 1; i >= 0; --i) {
-    const bool state = hi_of(x[i]) == kState;
-    const float a = __uint_as_float(hi_of(x[i]));
-    S = state ? lo_of(x[i]) : fmaf(a, S, lo_of(x[i]));
-    A *= a;
-    done |= state;
-  }
-  return done;
-}
-
-constexpr int kWindow = 2;   // words a thread loads at a time
-
-// The state that reaches a tile's channel c, known to its thread of part 0.  The
-// PARTS threads of the channel fold a window of words each, the nearest part 0's;
-// beyond their windows part 0 goes on alone.  Every thread of the workgroup calls
-// this; `on`: the channel exists; pA, pS hold a float per thread.
-template <int CT, int PARTS>
-__device__ __forceinline__ float look_back(const uint64_t* w, int64_t step, int count, int c, bool on, int part,
-                                           float* pA, float* pS) {
-  float A = 1.f, S = 0.f;
-  bool done = false;
-  if (on && part * kWindow < count) done = fold_words<kWindow>(w, step, count, part * kWindow, c, A, S);
-  if constexpr (PARTS > 1) {
-    if (part > 0) {
-      pA[part * CT + c] = done ? __uint_as_float(kState) : A;
-      pS[part * CT + c] = S;
-    }
-    chain_barrier();
-  }
-  if (part > 0 || !on) return 0.f;
-#pragma unroll
-  for (int i = 1; i < PARTS; ++i) {
-    if (done) break;
-    S = fmaf(A, pS[i * CT + c], S);
-    const float Ai = pA[i * CT + c];
-    done = __float_as_uint(Ai) == kState;
-    A *= Ai;
-  }
-  for (int k = PARTS * kWindow; !done && k < count; k += kWindow) {
-    float Ak, Sk;
-    done = fold_words<kWindow>(w, step, count, k, c, Ak, Sk);
-    S = fmaf(A, Sk, S);
-    A *= Ak;
-  }
-  return S;
+  for (int i = kWindow - 1; i >= 0; --i)
+    s = hi_of(x[i]) == kState ? lo_of(x[i]) : fmaf(__uint_as_float(hi_of(x[i])), s, lo_of(x[i]));
+  return s;
 }
 
 // VEC consecutive elements, 16 bytes (or one element): one access at the elements'
@@ -184,8 +143,7 @@ struct Geo {
   static constexpr int LY = TH / LX;
   static constexpr int L = TT / LY;       // tokens per thread
   static constexpr int CT = LX * VEC;     // channels per tile
-  static constexpr int PARTS = TH / CT;   // threads per channel
-  static_assert(PARTS >= 1 && L >= 1, "tile geometry");
+  static_assert(CT <= TH && L >= 1, "a thread for every channel");
 };
 
 // Channel tiles of CT channels or fewer: with one gate per head the whole heads that
@@ -305,20 +263,20 @@ template <typename TIO> __device__ __forceinline__ TIO* row_at(void* b, int64_t 
 // the forward of T = 32768, 16 heads of 128: the registers halve the tile) and are
 // not kept.
 template <typename TIO, int VEC, int LX, int GM, bool CONVEX>
-__global__ __launch_bounds__(kFwdThreads) void k_scan_fwd(const ScanParams p) {
+__global__ __launch_bounds__(kFwdThreads, 2) void k_scan_fwd(const ScanParams p) {
   constexpr int TT = fwd_tile(GM, LX * VEC > 128), kSaved = bwd_tile(GM, LX * VEC > 128, CONVEX);
   typedef Geo<VEC, LX, kFwdThreads, TT> G;
   typedef Vec<TIO, VEC> V;
   typedef GateRaw<TIO, VEC, GM> GR;
   constexpr int L = G::L, LY = G::LY, CT = G::CT;
-  __shared__ float sA[LY][CT], sS[LY][CT], pA[kFwdThreads], pS[kFwdThreads];
+  __shared__ float sA[LY][CT], sS[LY][CT];
   __shared__ int slot;
   const int tid = threadIdx.x, lx = tid % LX, ly = tid / LX;
   const int nct = channel_tiles<GM>(CT, p.C, p.D), ct = blockIdx.x % nct;
   int cbase, nc;
   channel_tile<GM, VEC>(CT, p.C, p.D, nct, ct, cbase, nc);
-  const int c = tid % CT, part = tid / CT;   // the channel this thread composes, and its share
-  const bool lead = part == 0 && c < nc;
+  const int c = tid;   // the channel this thread composes
+  const bool lead = c < nc;
   const bool on = lx * VEC < nc;
   const int v0 = min(lx * VEC, nc - VEC), c0 = cbase + v0;   // idle lanes repeat the last vector
   const int head = GM == kScanHeadLog ? c0 / p.D : 0;
@@ -383,20 +341,22 @@ __global__ __launch_bounds__(kFwdThreads) void k_scan_fwd(const ScanParams p) {
     for (int v = 0; v < VEC; ++v) { sA[ly][v0 + v] = A[v]; sS[ly][v0 + v] = S[v]; }
   }
   chain_barrier();
-  // one thread per channel composes the groups; the other threads of the channel
-  // (PARTS in all) share the look back
-  uint64_t* w = p.words + int64_t(row) * p.C + cbase;
-  if (lead && tile.idx > 0 && tile.after > 0) {
+  // one thread per channel composes the groups, and publishes before it does more
+  if (lead) {
+    uint64_t* w = p.words + int64_t(row) * p.C + cbase;
     float At = 1.f, St = 0.f;
 #pragma unroll
     for (int y = 0; y < LY; ++y) {
       St = fmaf(sA[y][c], St, sS[y][c]);
       At *= sA[y][c];
     }
-    put_fold(w + c, At, St);
-  }
-  if (tile.idx > 0) s = look_back<CT, G::PARTS>(w - p.C, -int64_t(p.C), tile.idx, c, c < nc, part, pA, pS);
-  if (lead) {
+    if (tile.idx > 0) {
+      if (tile.after > 0) put_fold(w + c, At, St);
+      s = look_back(w - p.C, -int64_t(p.C), tile.idx, c);
+    }
+    const float end = fmaf(At, s, St);
+    if (tile.after > 0) put_state(w + c, end);
+    else if (p.ht) p.ht[sc] = end;
     float* saved = p.carry + int64_t(tile.saved) * p.C + cbase + c;
 #pragma unroll
     for (int y = 0; y < LY; ++y) {
@@ -407,8 +367,6 @@ __global__ __launch_bounds__(kFwdThreads) void k_scan_fwd(const ScanParams p) {
       sS[y][c] = s;
       s = fmaf(sA[y][c], s, Sy);
     }
-    if (tile.after > 0) put_state(w + c, s);
-    else if (p.ht) p.ht[sc] = s;
   }
   chain_barrier();
   TIO* out = row_at<TIO>(p.y, tile.t_start, p.C);
@@ -433,15 +391,15 @@ __global__ __launch_bounds__(kBwdThreads, 2) void k_scan_bwd(const ScanParams p)
   constexpr int L = G::L, LY = G::LY, CT = G::CT;
   constexpr bool kPar = GM == kScanSoftplus || GM == kScanSigmoid;
   constexpr bool kLog = GM == kScanSoftplus || CONVEX;   // the logarithm is needed again
-  __shared__ float sA[LY][CT], sS[LY][CT], sE[LY][CT], pA[kBwdThreads], pS[kBwdThreads];
+  __shared__ float sA[LY][CT], sS[LY][CT], sE[LY][CT];
   __shared__ float sG[GM == kScanHeadLog ? TT : 1][LX + 1];
   __shared__ int slot;
   const int tid = threadIdx.x, lx = tid % LX, ly = tid / LX;
   const int nct = channel_tiles<GM>(CT, p.C, p.D), ct = blockIdx.x % nct;
   int cbase, nc;
   channel_tile<GM, VEC>(CT, p.C, p.D, nct, ct, cbase, nc);
-  const int c = tid % CT, part = tid / CT;
-  const bool lead = part == 0 && c < nc;
+  const int c = tid;
+  const bool lead = c < nc;
   const bool on = lx * VEC < nc;
   const int v0 = min(lx * VEC, nc - VEC), c0 = cbase + v0;
   const int head = GM == kScanHeadLog ? c0 / p.D : 0;
@@ -536,26 +494,27 @@ __global__ __launch_bounds__(kBwdThreads, 2) void k_scan_bwd(const ScanParams p)
     }
   }
   chain_barrier();
-  uint64_t* w = p.words + int64_t(row) * p.C + cbase;
-  if (lead && tile.idx > 0 && tile.after > 0) {
+  if (lead) {
+    uint64_t* w = p.words + int64_t(row) * p.C + cbase;
     float At = 1.f, Et = 0.f;
 #pragma unroll
     for (int y = LY - 1; y >= 0; --y) {
       Et = fmaf(sA[y][c], Et, sE[y][c]);
       At *= sA[y][c];
     }
-    put_fold(w + c, At, Et);
-  }
-  if (tile.after > 0) e0 = look_back<CT, G::PARTS>(w + p.C, p.C, tile.after, c, c < nc, part, pA, pS);
-  if (lead) {
+    if (tile.after > 0) {
+      if (tile.idx > 0) put_fold(w + c, At, Et);
+      e0 = look_back(w + p.C, p.C, tile.after, c);
+    }
+    const float end = fmaf(At, e0, Et);
+    if (tile.idx > 0) put_state(w + c, end);
+    else if (p.dh0) p.dh0[sc] = end;
 #pragma unroll
     for (int y = LY - 1; y >= 0; --y) {
       const float Ey = sE[y][c];
       sE[y][c] = e0;
       e0 = fmaf(sA[y][c], e0, Ey);
     }
-    if (tile.idx > 0) put_state(w + c, e0);
-    else if (p.dh0) p.dh0[sc] = e0;
 #pragma unroll
     for (int y = 0; y < LY; ++y) {
       const float Sy = sS[y][c];

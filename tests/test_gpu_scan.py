@@ -295,3 +295,34 @@ def test_steps_continue_the_forward():
         B.gdr_scan_step(one, {**d, "x": d["x"][i].contiguous(), "g": d["g"][i].contiguous(), "h0": None}, state, yi)
         R.check(f"y[{i}]", yi[0], ref["y"][0][i], ref["y"][1][i])
     R.check("state", state, *ref["ht"])
+
+
+@pytest.mark.parametrize("kind,dtype,H,D,convex", [(0, "bf16", 4, 64, True), (0, "f32", 200, 1, False),
+                                                   (1, "bf16", 3, 128, False), (2, "bf16", 2, 128, True)])
+def test_slow_decays_give_the_same_bits_every_time(kind, dtype, H, D, convex):
+    """Decays so slow that every tile's state reaches far: how far a tile looked back over
+    its predecessors, which is a matter of timing, must not show in the result."""
+    lengths = [9000, 1, 3000]
+    t, dy, dht = make(71, kind, dtype, lengths, H, D)
+    if kind == 0:
+        t["g"] = (t["g"].double() * 1e-3).to(DT[dtype])
+    elif kind == 1:
+        t["A_log"] = t["A_log"] - 7
+    else:
+        t["dt_bias"] = t["dt_bias"] - 8
+    prob, d = problem(kind, dtype, lengths, H, D, convex, False), dev(t)
+    dyc, dhtc = dy.cuda(), dht.cuda()
+    first = run(prob, d, dyc, dhtc, kind, 3, H, D)
+    for _ in range(10):
+        again = run(prob, d, dyc, dhtc, kind, 3, H, D)
+        for k in first:
+            assert torch.equal(first[k], again[k]), k
+    # few channels against the recurrence
+    part = {k: v if v is None or k == "A_log" else v[..., :1, :] if v.dim() == 3 and k != "dt_bias" else v
+            for k, v in t.items()}
+    part["g"], part["A_log"] = t["g"][:, :1], None if t["A_log"] is None else t["A_log"][:1]
+    part["dt_bias"] = None if t["dt_bias"] is None else t["dt_bias"][:1]
+    ref = R.scan(kind, part["x"], part["g"], part["A_log"], part["dt_bias"], part["h0"], lengths, GS, convex,
+                 dy[:, :1], dht[:, :1])
+    for k in ("y", "ht", "dx", "dg", "dh0"):
+        R.check(k, first[k][:, :1], *ref[k])
