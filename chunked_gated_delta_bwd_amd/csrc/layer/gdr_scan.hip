@@ -304,13 +304,22 @@ __global__ __launch_bounds__(kFwdThreads, 2) void k_scan_fwd(const ScanParams p)
       rx[i] = V::load(x, r * p.C + c0);
     }
   }
-  float a[L][VEC], u[L][VEC];
+  // the tokens' decays and, in the convex form, inputs (else they stay packed)
+  float a[L][VEC], u[CONVEX ? L : 1][VEC];
+  auto input = [&](int i, float (&x)[VEC]) {
+    if constexpr (CONVEX) {
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) x[v] = u[i][v];
+    } else {
+      V::unpack(rx[i], x);
+    }
+  };
   {
 #pragma unroll
     for (int i = 0; i < L; ++i) {
       float g[VEC];
       GR::unpack(rg[i], g);
-      V::unpack(rx[i], u[i]);
+      if constexpr (CONVEX) V::unpack(rx[i], u[i]);
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
         const float l = gate.log2_decay(g[v], v, p.gate_scale);
@@ -322,21 +331,29 @@ __global__ __launch_bounds__(kFwdThreads, 2) void k_scan_fwd(const ScanParams p)
   if (tile.len < TT) {
 #pragma unroll
     for (int i = 0; i < L; ++i)
-      if (ly * L + i >= tile.len)
+      if (ly * L + i >= tile.len) {
+        rx[i] = {};
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) { a[i][v] = 1.f; u[i][v] = 0.f; }
+        for (int v = 0; v < VEC; ++v) {
+          a[i][v] = 1.f;
+          if constexpr (CONVEX) u[i][v] = 0.f;
+        }
+      }
   }
   {
-    float A[VEC], S[VEC];
+    float A[VEC], S[VEC], x[VEC];
+    input(0, S);
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) { A[v] = a[0][v]; S[v] = u[0][v]; }
+    for (int v = 0; v < VEC; ++v) A[v] = a[0][v];
 #pragma unroll
-    for (int i = 1; i < L; ++i)
+    for (int i = 1; i < L; ++i) {
+      input(i, x);
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
-        S[v] = fmaf(a[i][v], S[v], u[i][v]);
+        S[v] = fmaf(a[i][v], S[v], x[v]);
         A[v] *= a[i][v];
       }
+    }
 #pragma unroll
     for (int v = 0; v < VEC; ++v) { sA[ly][v0 + v] = A[v]; sS[ly][v0 + v] = S[v]; }
   }
@@ -376,8 +393,10 @@ __global__ __launch_bounds__(kFwdThreads, 2) void k_scan_fwd(const ScanParams p)
 #pragma unroll
   for (int i = 0; i < L; ++i) {
     const int r = ly * L + i;
+    float x[VEC];
+    input(i, x);
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) y[v] = fmaf(a[i][v], y[v], u[i][v]);
+    for (int v = 0; v < VEC; ++v) y[v] = fmaf(a[i][v], y[v], x[v]);
     if (on && r < tile.len) V::store(out, uint32_t(r) * p.C + c0, y);
   }
 }
