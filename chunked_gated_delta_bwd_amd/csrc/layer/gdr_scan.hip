@@ -24,6 +24,16 @@
 // waiting for anybody, so every wait ends.  (Waits are
 // bounded all the same: should the workspace be overwritten by someone else during
 // the call, the states become NaN and the kernel ends.)
+//
+// What bounds it: HBM bytes (6 a channel and token forward, 10 backward, with bf16 and
+// a gate per channel) while few sequences are long: then the tiles in flight, two
+// workgroups a compute unit by registers, and what they wait for each other.  T = 32768,
+// bf16, on a card whose large copy moves 4.9 TB/s:
+//   4096 channels, a decay each:          180 us (4.5 TB/s), backward 276 us (4.9 TB/s)
+//   16 heads of 128, softplus gate:       112 us (3.6 TB/s),          202 us (3.3 TB/s)
+//   32 heads of 128, a decay per head, convex: 128 us (4.2 TB/s),     204 us (4.0 TB/s)
+// Without the look back (wrong results, timing alone) the softplus case took 103 and
+// 167 us, and without its gate functions the forward took 102 us.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -146,6 +156,18 @@ struct Geo {
   static_assert(CT <= TH && L >= 1, "a thread for every channel");
 };
 
+// Where a channel's values sit in a row of the LDS arrays: channel VEC x + v at v PV
+// + x, so that a wave's threads write consecutive words (one v at a time), and PV and
+// the row pitch are such that neither those writes (of 64 / LX rows) nor the reads of
+// 64 consecutive channels of a row meet in the 64 banks.  Plain [LY][CT] rows cost the
+// backward a fifth of its cycles in bank conflicts.
+template <int VEC, int LX>
+struct Cols {
+  static constexpr int PV = VEC == 1 ? LX : VEC == 8 ? (LX == 16 ? 24 : 40) : (LX == 32 ? 48 : 80);
+  static constexpr int PITCH = VEC * PV + (LX < 64 ? LX : 0);
+  static __device__ __forceinline__ int at(int c) { return c % VEC * PV + c / VEC; }
+};
+
 // Channel tiles of CT channels or fewer: with one gate per head the whole heads that
 // fit (the head's gate gradient is summed inside the workgroup), else CT.  Where
 // rows do not start on a vector, tiles share the channels evenly instead, so that
@@ -155,9 +177,9 @@ __host__ __device__ __forceinline__ int channel_tiles(int CT, int C, int D) {
   const int step = GM == kScanHeadLog ? CT / D * D : CT;
   return (C + step - 1) / step;
 }
-template <int GM, int VEC>
+template <int GM, bool WHOLE>
 __device__ __forceinline__ void channel_tile(int CT, int C, int D, int nct, int ct, int& base, int& n) {
-  if (GM != kScanHeadLog && C % VEC) {
+  if (!WHOLE) {
     base = int(int64_t(C) * ct / nct);
     n = int(int64_t(C) * (ct + 1) / nct) - base;
   } else {
@@ -259,26 +281,31 @@ template <typename TIO> __device__ __forceinline__ TIO* row_at(void* b, int64_t 
 // end and lanes past its channels load a valid neighbour's values, and the rows past
 // the end are then made neutral (a = 1, no input), in a loop of its own that full
 // tiles skip.  Barriers order LDS only.  A workgroup handles one tile; workgroups that
-// stay and load their next tile's inputs ahead measured no faster (117 us at best for
-// the forward of T = 32768, 16 heads of 128: the registers halve the tile) and are
-// not kept.
-template <typename TIO, int VEC, int LX, int GM, bool CONVEX>
+// stay and load their next tile's inputs ahead measured slower (117 us against 106 for
+// the forward of T = 32768, 16 heads of 128: the registers halve the tile), as did
+// three workgroups a compute unit (126 us: spills).
+template <typename TIO, int VEC, int LX, int GM, bool CONVEX, bool WHOLE>
 __global__ __launch_bounds__(kFwdThreads, 2) void k_scan_fwd(const ScanParams p) {
   constexpr int TT = fwd_tile(GM, LX * VEC > 128), kSaved = bwd_tile(GM, LX * VEC > 128, CONVEX);
   typedef Geo<VEC, LX, kFwdThreads, TT> G;
   typedef Vec<TIO, VEC> V;
   typedef GateRaw<TIO, VEC, GM> GR;
+  typedef Cols<VEC, LX> K;
   constexpr int L = G::L, LY = G::LY, CT = G::CT;
-  __shared__ float sA[LY][CT], sS[LY][CT];
+  __shared__ float sA[LY][K::PITCH], sS[LY][K::PITCH];
   __shared__ int slot;
   const int tid = threadIdx.x, lx = tid % LX, ly = tid / LX;
   const int nct = channel_tiles<GM>(CT, p.C, p.D), ct = blockIdx.x % nct;
   int cbase, nc;
-  channel_tile<GM, VEC>(CT, p.C, p.D, nct, ct, cbase, nc);
+  channel_tile<GM, WHOLE>(CT, p.C, p.D, nct, ct, cbase, nc);
   const int c = tid;   // the channel this thread composes
   const bool lead = c < nc;
   const bool on = lx * VEC < nc;
   const int v0 = min(lx * VEC, nc - VEC), c0 = cbase + v0;   // idle lanes repeat the last vector
+  // LDS column of this thread's channel v, and of the channel it composes; whole vectors
+  // (WHOLE) have columns of their own, overlapping ones share them
+  auto col = [&](int v) { return WHOLE ? v * K::PV + lx : K::at(v0 + v); };
+  const int cc = K::at(c);
   const int head = GM == kScanHeadLog ? c0 / p.D : 0;
   Gate<VEC, GM> gate;
   gate.init(p, c0);
@@ -355,7 +382,7 @@ __global__ __launch_bounds__(kFwdThreads, 2) void k_scan_fwd(const ScanParams p)
       }
     }
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) { sA[ly][v0 + v] = A[v]; sS[ly][v0 + v] = S[v]; }
+    for (int v = 0; v < VEC; ++v) { sA[ly][col(v)] = A[v]; sS[ly][col(v)] = S[v]; }
   }
   chain_barrier();
   // one thread per channel composes the groups, and publishes before it does more
@@ -364,8 +391,8 @@ __global__ __launch_bounds__(kFwdThreads, 2) void k_scan_fwd(const ScanParams p)
     float At = 1.f, St = 0.f;
 #pragma unroll
     for (int y = 0; y < LY; ++y) {
-      St = fmaf(sA[y][c], St, sS[y][c]);
-      At *= sA[y][c];
+      St = fmaf(sA[y][cc], St, sS[y][cc]);
+      At *= sA[y][cc];
     }
     if (tile.idx > 0) {
       if (tile.after > 0) put_fold(w + c, At, St);
@@ -380,16 +407,16 @@ __global__ __launch_bounds__(kFwdThreads, 2) void k_scan_fwd(const ScanParams p)
       constexpr int kPer = kSaved / L;   // groups per backward tile
       static_assert(kPer * L == kSaved && TT % kSaved == 0, "saved states at group borders");
       if (y % kPer == 0 && y * L < tile.len) saved[int64_t(y / kPer) * p.C] = s;
-      const float Sy = sS[y][c];
-      sS[y][c] = s;
-      s = fmaf(sA[y][c], s, Sy);
+      const float Sy = sS[y][cc];
+      sS[y][cc] = s;
+      s = fmaf(sA[y][cc], s, Sy);
     }
   }
   chain_barrier();
   TIO* out = row_at<TIO>(p.y, tile.t_start, p.C);
   float y[VEC];
 #pragma unroll
-  for (int v = 0; v < VEC; ++v) y[v] = sS[ly][v0 + v];
+  for (int v = 0; v < VEC; ++v) y[v] = sS[ly][col(v)];
 #pragma unroll
   for (int i = 0; i < L; ++i) {
     const int r = ly * L + i;
@@ -401,26 +428,31 @@ __global__ __launch_bounds__(kFwdThreads, 2) void k_scan_fwd(const ScanParams p)
   }
 }
 
-template <typename TIO, int VEC, int LX, int GM, bool CONVEX>
+template <typename TIO, int VEC, int LX, int GM, bool CONVEX, bool WHOLE>
 __global__ __launch_bounds__(kBwdThreads, 2) void k_scan_bwd(const ScanParams p) {
   constexpr int TT = bwd_tile(GM, LX * VEC > 128, CONVEX);
   typedef Geo<VEC, LX, kBwdThreads, TT> G;
   typedef Vec<TIO, VEC> V;
   typedef GateRaw<TIO, VEC, GM> GR;
+  typedef Cols<VEC, LX> K;
   constexpr int L = G::L, LY = G::LY, CT = G::CT;
   constexpr bool kPar = GM == kScanSoftplus || GM == kScanSigmoid;
   constexpr bool kLog = GM == kScanSoftplus || CONVEX;   // the logarithm is needed again
-  __shared__ float sA[LY][CT], sS[LY][CT], sE[LY][CT];
+  __shared__ float sA[LY][K::PITCH], sS[LY][K::PITCH], sE[LY][K::PITCH];
   __shared__ float sG[GM == kScanHeadLog ? TT : 1][LX + 1];
   __shared__ int slot;
   const int tid = threadIdx.x, lx = tid % LX, ly = tid / LX;
   const int nct = channel_tiles<GM>(CT, p.C, p.D), ct = blockIdx.x % nct;
   int cbase, nc;
-  channel_tile<GM, VEC>(CT, p.C, p.D, nct, ct, cbase, nc);
+  channel_tile<GM, WHOLE>(CT, p.C, p.D, nct, ct, cbase, nc);
   const int c = tid;
   const bool lead = c < nc;
   const bool on = lx * VEC < nc;
-  const int v0 = min(lx * VEC, nc - VEC), c0 = cbase + v0;
+  const int v0 = min(lx * VEC, nc - VEC), c0 = cbase + v0;   // idle lanes repeat the last vector
+  // LDS column of this thread's channel v, and of the channel it composes; whole vectors
+  // (WHOLE) have columns of their own, overlapping ones share them
+  auto col = [&](int v) { return WHOLE ? v * K::PV + lx : K::at(v0 + v); };
+  const int cc = K::at(c);
   const int head = GM == kScanHeadLog ? c0 / p.D : 0;
   Gate<VEC, GM> gate;
   gate.init(p, c0);
@@ -507,9 +539,9 @@ __global__ __launch_bounds__(kBwdThreads, 2) void k_scan_bwd(const ScanParams p)
     }
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
-      sA[ly][v0 + v] = A[v];
-      sS[ly][v0 + v] = S[v];
-      sE[ly][v0 + v] = E[v];
+      sA[ly][col(v)] = A[v];
+      sS[ly][col(v)] = S[v];
+      sE[ly][col(v)] = E[v];
     }
   }
   chain_barrier();
@@ -518,8 +550,8 @@ __global__ __launch_bounds__(kBwdThreads, 2) void k_scan_bwd(const ScanParams p)
     float At = 1.f, Et = 0.f;
 #pragma unroll
     for (int y = LY - 1; y >= 0; --y) {
-      Et = fmaf(sA[y][c], Et, sE[y][c]);
-      At *= sA[y][c];
+      Et = fmaf(sA[y][cc], Et, sE[y][cc]);
+      At *= sA[y][cc];
     }
     if (tile.after > 0) {
       if (tile.idx > 0) put_fold(w + c, At, Et);
@@ -530,15 +562,15 @@ __global__ __launch_bounds__(kBwdThreads, 2) void k_scan_bwd(const ScanParams p)
     else if (p.dh0) p.dh0[sc] = end;
 #pragma unroll
     for (int y = LY - 1; y >= 0; --y) {
-      const float Ey = sE[y][c];
-      sE[y][c] = e0;
-      e0 = fmaf(sA[y][c], e0, Ey);
+      const float Ey = sE[y][cc];
+      sE[y][cc] = e0;
+      e0 = fmaf(sA[y][cc], e0, Ey);
     }
 #pragma unroll
     for (int y = 0; y < LY; ++y) {
-      const float Sy = sS[y][c];
-      sS[y][c] = s0;
-      s0 = fmaf(sA[y][c], s0, Sy);
+      const float Sy = sS[y][cc];
+      sS[y][cc] = s0;
+      s0 = fmaf(sA[y][cc], s0, Sy);
     }
   }
   chain_barrier();
@@ -547,8 +579,8 @@ __global__ __launch_bounds__(kBwdThreads, 2) void k_scan_bwd(const ScanParams p)
     float s[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
-      s[v] = sS[ly][v0 + v];
-      e[v] = sE[ly][v0 + v];
+      s[v] = sS[ly][col(v)];
+      e[v] = sE[ly][col(v)];
       sumz[v] = sumA[v] = 0.f;
     }
 #pragma unroll
@@ -613,12 +645,12 @@ __global__ __launch_bounds__(kBwdThreads, 2) void k_scan_bwd(const ScanParams p)
   if constexpr (kPar) {
     chain_barrier();
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) { sS[ly][v0 + v] = sumz[v]; sE[ly][v0 + v] = sumA[v]; }
+    for (int v = 0; v < VEC; ++v) { sS[ly][col(v)] = sumz[v]; sE[ly][col(v)] = sumA[v]; }
     chain_barrier();
     if (lead) {
       float z = 0.f, zA = 0.f;
 #pragma unroll
-      for (int y = 0; y < LY; ++y) { z += sS[y][c]; zA += sE[y][c]; }
+      for (int y = 0; y < LY; ++y) { z += sS[y][cc]; zA += sE[y][cc]; }
       partial[0] = z;
       partial[p.C] = zA * 0.6931471805599453f;   // lambda and z are in base-2 units
     }
@@ -757,12 +789,20 @@ __global__ __launch_bounds__(256) void k_scan_step(const ScanStepParams p) {
   else IO<float>::store8(st, 0, s);
 }
 
+template <typename TIO, int VEC, int LX, int GM, bool CONVEX, bool WHOLE>
+int launch_whole(const ScanParams& p, bool backward, hipStream_t s) {
+  const dim3 grid(unsigned(int64_t(p.NT) * channel_tiles<GM>(LX * VEC, p.C, p.D)));
+  if (backward) k_scan_bwd<TIO, VEC, LX, GM, CONVEX, WHOLE><<<grid, kBwdThreads, 0, s>>>(p);
+  else k_scan_fwd<TIO, VEC, LX, GM, CONVEX, WHOLE><<<grid, kFwdThreads, 0, s>>>(p);
+  return static_cast<int>(hipGetLastError());
+}
+
 template <typename TIO, int VEC, int LX, int GM, bool CONVEX>
 int launch_convex(const ScanParams& p, bool backward, hipStream_t s) {
-  const dim3 grid(unsigned(int64_t(p.NT) * channel_tiles<GM>(LX * VEC, p.C, p.D)));
-  if (backward) k_scan_bwd<TIO, VEC, LX, GM, CONVEX><<<grid, kBwdThreads, 0, s>>>(p);
-  else k_scan_fwd<TIO, VEC, LX, GM, CONVEX><<<grid, kFwdThreads, 0, s>>>(p);
-  return static_cast<int>(hipGetLastError());
+  // heads of several channels are whole vectors of them
+  if constexpr (VEC > 1 && GM != kScanHeadLog)
+    if (p.C % VEC) return launch_whole<TIO, VEC, LX, GM, CONVEX, false>(p, backward, s);
+  return launch_whole<TIO, VEC, LX, GM, CONVEX, true>(p, backward, s);
 }
 
 template <typename TIO, int VEC, int LX, int GM>
