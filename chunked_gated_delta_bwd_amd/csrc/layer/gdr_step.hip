@@ -6,7 +6,9 @@
 // eight lanes hold a row in registers, both products with the row reduce over
 // those lanes alone, and the state is read and written once.  Each group of eight
 // lanes forms the norms of q and k itself from its share of the channels: no LDS
-// and no barrier.  The state's bytes bound the step.
+// and no barrier but for the search for rows that share a slot.  The state's bytes
+// bound the step: 250 rows of 32 heads, D = 128, move 1 GB in 187 us (5.5 TB/s; a
+// large copy moves 4.9); one row of 16 heads takes 3.5 us in a graph.
 #include <hip/hip_runtime.h>
 
 #include "../gdr_device.h"
