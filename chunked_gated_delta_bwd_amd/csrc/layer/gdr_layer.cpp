@@ -150,16 +150,15 @@ gdr::ScanParams scan_params(const gdr_scan_shape* s, const gdr_scan_inputs* in, 
   return p;
 }
 
-// What a call's main kernel finds: the words cleared, and the tile table of a
-// packed problem (sequences by value, kScanBatch a launch).
+// What a call's main kernel finds: the words cleared where tiles wait for others, and
+// the tile table of a packed problem (sequences by value, kScanBatch a launch).
 gdr_status scan_prologue(const gdr_scan_shape* s, const gdr::ScanParams& p, int tile, void* stream) {
-  if (p.words) {
-    const gdr_status st = hip_status(gdr::launch_scan_clear(p, stream), "scan clear kernel");
-    if (st != GDR_OK) return st;
-  }
-  if (!s->cu_seqlens_host) return GDR_OK;
   gdr::ScanBatch b;
   std::memset(&b, 0, sizeof(b));
+  bool clear = p.words != nullptr;
+  if (!s->cu_seqlens_host)
+    return clear ? hip_status(gdr::launch_scan_prologue(p, tile, b, true, stream), "scan prologue kernel") : GDR_OK;
+  const int saved_tile = gdr::bwd_tile(p.gate, p.D > 128, p.convex);
   int64_t row = 0, saved = 0;
   for (int n0 = 0; n0 < s->N; n0 += gdr::kScanBatch) {
     b.n = std::min(gdr::kScanBatch, s->N - n0);
@@ -171,10 +170,11 @@ gdr_status scan_prologue(const gdr_scan_shape* s, const gdr::ScanParams& p, int 
       b.tile0[i] = int32_t(row);
       b.saved0[i] = int32_t(saved);
       row += tiles_of(len, tile);
-      saved += tiles_of(len, gdr::bwd_tile(p.gate, p.D > 128, p.convex));
+      saved += tiles_of(len, saved_tile);
     }
-    const gdr_status st = hip_status(gdr::launch_scan_tables(p, tile, b, stream), "tile table kernel");
+    const gdr_status st = hip_status(gdr::launch_scan_prologue(p, tile, b, clear, stream), "scan prologue kernel");
     if (st != GDR_OK) return st;
+    clear = false;
   }
   return GDR_OK;
 }

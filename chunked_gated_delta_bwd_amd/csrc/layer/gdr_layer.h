@@ -73,9 +73,9 @@ struct ScanParams {
   double* runs;                // [kParamSplit][2][C] sums of runs of tiles; NULL: few tiles
 };
 
-int launch_scan_tables(const ScanParams& p, int TT, const ScanBatch& b, void* stream);
+// The tile rows of a batch (of TT tokens) and, with `clear`, the counters and words.
+int launch_scan_prologue(const ScanParams& p, int TT, const ScanBatch& b, bool clear, void* stream);
 int launch_scan(const ScanParams& p, bool backward, void* stream);
-int launch_scan_clear(const ScanParams& p, void* stream);
 int launch_scan_params(const ScanParams& p, void* stream);
 
 struct ScanStepParams {

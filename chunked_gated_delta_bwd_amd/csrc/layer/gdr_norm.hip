@@ -362,6 +362,8 @@ __global__ __launch_bounds__(1024) void k_norm_dw(const float* part, float* dw, 
 // Threads per row for a width of n vectors.
 struct Plan { int tpr, nv; };
 Plan plan_for(int n) {
+  if (n <= 2) return {2, 1};
+  if (n <= 4) return {4, 1};
   if (n <= 8) return {8, 1};
   if (n <= 16) return {16, 1};
   if (n <= 32) return {32, 1};
@@ -408,6 +410,8 @@ int launch_plan(const NormParams& p, hipStream_t s) {
   const Plan pl = plan_for(vectors_of(p.width, p.dtype));
 #define GDR_NORM_CASE(T, N) \
   if (pl.tpr == T && pl.nv == N) return BWD ? launch_bwd<TIO, T, N>(p, s) : launch_fwd<TIO, T, N>(p, s);
+  GDR_NORM_CASE(2, 1)
+  GDR_NORM_CASE(4, 1)
   GDR_NORM_CASE(8, 1)
   GDR_NORM_CASE(16, 1)
   GDR_NORM_CASE(32, 1)

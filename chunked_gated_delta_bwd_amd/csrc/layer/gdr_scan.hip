@@ -720,22 +720,24 @@ __global__ __launch_bounds__(kParamThreads) void k_scan_params(const ScanParams 
   }
 }
 
-// The tile rows of up to kScanBatch sequences, TT tokens a tile.
-__global__ __launch_bounds__(64) void k_scan_tables(ScanTile* tab, int TT, int saved, const ScanBatch b) {
+// What a call's main kernel finds: the counters cleared and the words marked as not
+// published, and the tile rows of up to kScanBatch sequences (workgroup i: sequence i),
+// TT tokens a tile.
+__global__ __launch_bounds__(256) void k_scan_prologue(uint32_t* counters, int nc, uint64_t* words, int64_t n,
+                                                       ScanTile* tab, int TT, int saved, const ScanBatch b) {
+  if (words) {
+    const int64_t t = int64_t(blockIdx.x) * 256 + threadIdx.x, all = int64_t(gridDim.x) * 256;
+    for (int64_t i = t; i < nc; i += all) counters[i * kScanCounterStep] = 0;
+    ulonglong2* w = reinterpret_cast<ulonglong2*>(words);
+    constexpr uint64_t kNo = uint64_t(kNothing) << 32;
+    for (int64_t i = t; 2 * i < n; i += all) w[i] = ulonglong2{kNo, kNo};
+  }
   const int i = blockIdx.x;
+  if (i >= b.n) return;
   const int len = b.len[i], tiles = max(1, (len + TT - 1) / TT);
-  for (int j = threadIdx.x; j < tiles; j += 64)
+  for (int j = threadIdx.x; j < tiles; j += 256)
     tab[b.tile0[i] + j] = ScanTile{b.t_start[i] + j * TT, min(TT, len - j * TT), b.seq0 + i, j, tiles - 1 - j,
                                    b.saved0[i] + j * (TT / saved)};
-}
-
-// Clears the counters and marks the words as not published.
-__global__ __launch_bounds__(256) void k_scan_clear(uint32_t* counters, int nc, uint64_t* words, int64_t n) {
-  const int64_t t = int64_t(blockIdx.x) * 256 + threadIdx.x, all = int64_t(gridDim.x) * 256;
-  for (int64_t i = t; i < nc; i += all) counters[i * kScanCounterStep] = 0;
-  ulonglong2* w = reinterpret_cast<ulonglong2*>(words);
-  constexpr uint64_t kNo = uint64_t(kNothing) << 32;
-  for (int64_t i = t; 2 * i < n; i += all) w[i] = ulonglong2{kNo, kNo};
 }
 
 // One token a row: a workgroup takes 256 VEC channels of one row, and where later
@@ -882,20 +884,14 @@ int launch_scan_params(const ScanParams& p, void* stream) {
   return static_cast<int>(hipGetLastError());
 }
 
-int launch_scan_clear(const ScanParams& p, void* stream) {
+int launch_scan_prologue(const ScanParams& p, int TT, const ScanBatch& b, bool clear, void* stream) {
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   (void)hipGetLastError();
-  const int64_t n = int64_t(p.NT) * p.C;
-  k_scan_clear<<<dim3(unsigned(std::min<int64_t>((n + 511) / 512, 2048))), 256, 0, s>>>(
-      p.counters, scan_counters(p.C), p.words, n);
-  return static_cast<int>(hipGetLastError());
-}
-
-int launch_scan_tables(const ScanParams& p, int TT, const ScanBatch& b, void* stream) {
-  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  (void)hipGetLastError();
-  if (b.n <= 0) return 0;
-  k_scan_tables<<<dim3(b.n), 64, 0, s>>>(p.tab, TT, bwd_tile(p.gate, p.D > 128, p.convex), b);
+  const int64_t n = clear ? int64_t(p.NT) * p.C : 0;
+  const int64_t blocks = std::max<int64_t>(b.n, std::min<int64_t>((n + 511) / 512, 2048));
+  if (blocks == 0) return 0;
+  k_scan_prologue<<<dim3(unsigned(blocks)), 256, 0, s>>>(p.counters, scan_counters(p.C), clear ? p.words : nullptr, n,
+                                                         p.tab, TT, bwd_tile(p.gate, p.D > 128, p.convex), b);
   return static_cast<int>(hipGetLastError());
 }
 

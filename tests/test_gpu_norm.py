@@ -15,7 +15,7 @@ CODE = {"bf16": B.GDR_BF16, "f32": B.GDR_F32}
 EPS = 1e-6
 
 # every number of threads and vectors a row can take, their borders, and odd widths
-WIDTHS = [1, 7, 8, 64, 100, 128, 136, 200, 256, 260, 512, 520, 1000, 1024, 1028, 2040, 2048, 2056, 4096, 4100, 8192, 8200, 16384,
+WIDTHS = [1, 7, 8, 13, 16, 24, 64, 100, 128, 136, 200, 256, 260, 512, 520, 1000, 1024, 1028, 2040, 2048, 2056, 4096, 4100, 8192, 8200, 16384,
           16392, 32767, 32768]
 
 
