@@ -87,8 +87,8 @@ gdr_status check_scan_shape(const gdr_scan_shape* s, int64_t* NT_out) {
   }
   const int64_t C = int64_t(s->H) * s->D, tokens = int64_t(s->B) * s->T;
   if (C > (int64_t(1) << 21) || tokens >= (int64_t(1) << 31) || tokens * C >= (int64_t(1) << 40) ||
-      NT * ((C + 63) / 64) >= (int64_t(1) << 31))
-    return set_error(GDR_EUNSUPPORTED, "problem too large for 32-bit tile indexing");
+      NT * ((C + 63) / 64) * 256 >= gdr::kMaxThreads)
+    return set_error(GDR_EUNSUPPORTED, "problem too large for one launch and 32-bit tile indexing");
   *NT_out = NT;
   return GDR_OK;
 }
@@ -201,7 +201,9 @@ gdr_status check_norm_shape(const gdr_norm_shape* s) {
   if (!(s->eps >= 0.f && s->eps < 1e30f)) return set_error(GDR_EINVAL, "eps %g must be finite and >= 0", double(s->eps));
   if (s->width > gdr::kNormMaxWidth)
     return set_error(GDR_EUNSUPPORTED, "width %d above %d", s->width, gdr::kNormMaxWidth);
-  if (s->rows >= (int64_t(1) << 31)) return set_error(GDR_EUNSUPPORTED, "too many rows for 32-bit row indexing");
+  if (s->rows >= (int64_t(1) << 31) ||
+      gdr::norm_fwd_blocks(s->rows, s->width, s->dtype) * gdr::norm_fwd_threads(s->width, s->dtype) >= gdr::kMaxThreads)
+    return set_error(GDR_EUNSUPPORTED, "too many rows (%lld of width %d) for one launch", (long long)s->rows, s->width);
   return GDR_OK;
 }
 
@@ -307,6 +309,8 @@ gdr_status gdr_step(const gdr_shape* shape, const gdr_inputs* in, float* state, 
   gdr_status st = gdr_workspace_bytes(shape, &bytes);   // checks the shape; a step needs no workspace
   if (st != GDR_OK) return st;
   if (shape->cu_seqlens_host || shape->T != 1) return set_error(GDR_EINVAL, "a step takes a dense shape with T == 1");
+  if (int64_t(shape->N) * shape->H * (shape->Dk / 32) * 256 >= gdr::kMaxThreads)
+    return set_error(GDR_EUNSUPPORTED, "too many rows (%d of %d heads) for one launch", shape->N, shape->H);
   if (!in) return set_error(GDR_EINVAL, "inputs is NULL");
   const bool par = shape->gate != GDR_GATE_SCALAR;
   if (!par && (in->A_log || in->dt_bias)) return set_error(GDR_EINVAL, "scalar gate takes no A_log/dt_bias");

@@ -10,6 +10,10 @@
 
 namespace gdr {
 
+// Threads of a launch: a launch of as many is refused by the runtime, so the shape
+// checks refuse it before anything is enqueued.
+constexpr int64_t kMaxThreads = int64_t(1) << 32;
+
 // How the recurrence's kernels read the gate.
 enum ScanGate {
   kScanLog = 0,       // one log decay per channel (scalar gate, D = 1)
@@ -105,6 +109,8 @@ struct NormParams {
 int launch_norm(const NormParams& p, void* stream);        // y, or q and scales
 int launch_norm_bwd(const NormParams& p, void* stream);
 int norm_bwd_partials(int64_t rows, int32_t width, int32_t dtype);
+int64_t norm_fwd_blocks(int64_t rows, int32_t width, int32_t dtype);
+int norm_fwd_threads(int32_t width, int32_t dtype);   // of a workgroup
 
 struct StepParams {
   int32_t N, H, Hk, G, D, P;

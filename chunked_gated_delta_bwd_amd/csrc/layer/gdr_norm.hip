@@ -381,10 +381,13 @@ int vectors_of(int width, int dtype) {
   return (width + v - 1) / v;
 }
 constexpr int unr_for(int tpr, int nv) { return tpr > 64 ? 1 : 4 / nv; }
+constexpr int threads_for(int tpr) { return tpr > 256 ? tpr : 256; }
+// Rows of a workgroup at a time.
+constexpr int rows_for(int tpr, int nv) { return threads_for(tpr) / tpr * unr_for(tpr, nv); }
 
 template <typename TIO, int TPR, int NV>
 int launch_fwd(const NormParams& p, hipStream_t s) {
-  constexpr int BS = TPR > 256 ? TPR : 256, UNR = unr_for(TPR, NV), ROWS = BS / TPR * UNR;
+  constexpr int BS = threads_for(TPR), UNR = unr_for(TPR, NV), ROWS = rows_for(TPR, NV);
   const dim3 grid(unsigned((p.rows + ROWS - 1) / ROWS));
   if (p.q) k_norm<TIO, TPR, NV, UNR, true><<<grid, BS, 0, s>>>(p);
   else k_norm<TIO, TPR, NV, UNR, false><<<grid, BS, 0, s>>>(p);
@@ -393,15 +396,13 @@ int launch_fwd(const NormParams& p, hipStream_t s) {
 
 // Workgroups of the backward: as many as stay resident, fewer for few rows.
 int partials_for(int64_t rows, int tpr, int nv) {
-  const int64_t per = int64_t(tpr > 256 ? 1 : 256 / tpr) * unr_for(tpr, nv);
-  const int64_t n = (rows + per - 1) / per;
+  const int64_t n = (rows + rows_for(tpr, nv) - 1) / rows_for(tpr, nv);
   return int(n < kNormPartials ? n : kNormPartials);
 }
 
 template <typename TIO, int TPR, int NV>
 int launch_bwd(const NormParams& p, hipStream_t s) {
-  constexpr int BS = TPR > 256 ? TPR : 256;
-  k_norm_bwd<TIO, TPR, NV, unr_for(TPR, NV)><<<dim3(partials_for(p.rows, TPR, NV)), BS, 0, s>>>(p);
+  k_norm_bwd<TIO, TPR, NV, unr_for(TPR, NV)><<<dim3(partials_for(p.rows, TPR, NV)), threads_for(TPR), 0, s>>>(p);
   return static_cast<int>(hipGetLastError());
 }
 
@@ -433,6 +434,13 @@ int launch_any(const NormParams& p, hipStream_t s) {
 }
 
 }  // namespace
+
+int64_t norm_fwd_blocks(int64_t rows, int32_t width, int32_t dtype) {
+  const Plan pl = plan_for(vectors_of(width, dtype));
+  return (rows + rows_for(pl.tpr, pl.nv) - 1) / rows_for(pl.tpr, pl.nv);
+}
+
+int norm_fwd_threads(int32_t width, int32_t dtype) { return threads_for(plan_for(vectors_of(width, dtype)).tpr); }
 
 int norm_bwd_partials(int64_t rows, int32_t width, int32_t dtype) {
   const Plan pl = plan_for(vectors_of(width, dtype));

@@ -234,8 +234,10 @@ gdr_status gdr_fwd_bwd_noalloc(const gdr_shape* shape, const gdr_inputs* in, con
  * A row whose slot is outside [0, P) is padding: no state is touched and its row
  * of o is left as it was.  Rows with the same slot are successive tokens of one
  * sequence, taken in the order of n.  o: [N,1,H,Dv] dtype.  No workspace.
- * No output may overlap an input.  Errors as gdr_fwd_recompute, and GDR_EINVAL
- * for T != 1, a varlen shape, an h0, a NULL state, P < 0 or P < N without slots. */
+ * No output may overlap an input.  Each row reads all of `slots` (N^2 reads in
+ * all).  Errors as gdr_fwd_recompute, and GDR_EINVAL for T != 1, a varlen shape, an
+ * h0, a NULL state, P < 0 or P < N without slots, and GDR_EUNSUPPORTED from N H Dk /
+ * 32 = 2^24 on. */
 gdr_status gdr_step(const gdr_shape* shape, const gdr_inputs* in, float* state, int32_t P, const int32_t* slots,
                     void* o, void* stream);
 
@@ -253,7 +255,9 @@ gdr_status gdr_step(const gdr_shape* shape, const gdr_inputs* in, float* state, 
  * The backward returns the gradients of L = sum_t <dy_t, y_t> + <dht, s_T>.
  * x, y: [B,T,H,D] (or packed [1,T,H,D]), 1 <= D <= 256 with D == 1 or a multiple
  * of 8; B, T, N, cu_seqlens_host, dtype and alignment as in gdr_shape.  States,
- * products and sums are fp32; y, dx and dg are rounded once to dtype. */
+ * products and sums are fp32; y, dx and dg are rounded once to dtype.  Counting
+ * a tile for every 64 tokens of a sequence (at least one), GDR_EUNSUPPORTED from
+ * 2^24 tiles times ceil(H D / 64) on. */
 typedef struct {
   int32_t B, T, H, D;               /* dense: [B,T,H,D]; varlen: B == 1, T == total tokens */
   int32_t N;                        /* sequences, as in gdr_shape */
@@ -308,7 +312,11 @@ gdr_status gdr_scan_step(const gdr_scan_shape* shape, const gdr_scan_inputs* in,
  * x, res, y, res_out: [rows,width] dtype; w: [width] fp32 or NULL (ones).  r is
  * kept in fp32 for y; res_out (required with res, NULL without) is r rounded to
  * dtype and may be res or x itself; y may be x or res itself unless that is
- * res_out.  1 <= width <= 32768. */
+ * res_out.  1 <= width <= 32768; fewer than 2^31 rows, and so many that a launch
+ * stays under 2^32 threads (fewer than 2^22 rows of any width do, fewer than 2^24
+ * of up to 16 KiB), else GDR_EUNSUPPORTED.  Squares are summed in fp32: a row whose
+ * sum of squares leaves that range gives zeros or NaN; with eps 0 a row of zeros
+ * gives NaN. */
 typedef struct {
   int64_t rows;
   int32_t width;

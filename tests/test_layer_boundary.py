@@ -280,3 +280,35 @@ def test_binding_checks_step_tensors():
     refused(B.GDR_EINVAL, "o is torch.bfloat16", B.gdr_step, p, t, st, o.to(BF))
     refused(B.GDR_EINVAL, "state is not contiguous", B.gdr_step, p, t, st.transpose(2, 3), o)
     refused(B.GDR_EINVAL, "slots has 4", B.gdr_step, p, t, st, o, slots=torch.zeros(4, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("kw,fits", [
+    (dict(T=1, D=1, H=64, B=(1 << 24) - 1, N=(1 << 24) - 1), True),
+    (dict(T=1, D=1, H=64, B=1 << 24, N=1 << 24), False),
+    (dict(T=64, D=128, H=32, B=(1 << 18) - 1, N=(1 << 18) - 1, gate=1), True),
+    (dict(T=64, D=128, H=32, B=1 << 18, N=1 << 18, gate=1), False),
+])
+def test_scan_launches_under_two_to_the_32_threads(kw, fits):
+    """256 threads a tile: 2^24 tiles are one launch too many."""
+    if fits:
+        assert B.gdr_scan_workspace_bytes(scan(**kw)) > 0
+    else:
+        refused(B.GDR_EUNSUPPORTED, "too large", B.gdr_scan_workspace_bytes, scan(**kw))
+
+
+@pytest.mark.parametrize("width,dtype,rows", [
+    (32768, B.GDR_BF16, 1 << 22),    # 1024 threads a row
+    (4100, B.GDR_F32, 1 << 22),
+    (8192, B.GDR_BF16, 1 << 24),     # 256
+    (2048, B.GDR_BF16, 1 << 26),     # 64
+])
+def test_norm_launches_under_two_to_the_32_threads(width, dtype, rows):
+    assert B.gdr_norm_workspace_bytes(B.NormProblem(rows - 4, width, dtype)) > 0
+    refused(B.GDR_EUNSUPPORTED, "too many rows", B.gdr_norm_workspace_bytes, B.NormProblem(rows, width, dtype))
+
+
+def test_step_launches_under_two_to_the_32_threads():
+    """128 / 32 workgroups of 256 threads a row and head; 2^22 rows and heads are too many."""
+    n = 1 << 18
+    prob = B.Problem(B=n, T=1, H=16, D=128, N=n, gate=0, dtype=B.GDR_BF16, scale=1.0)
+    refused(B.GDR_EUNSUPPORTED, "too many rows", step_call, prob)
