@@ -13,10 +13,11 @@
 // the inputs once and recomputes the states from the tile's starting state that
 // the forward left in the workspace.
 //
-// Between tiles: every tile publishes its fold (A, S) and, once it knows the state
-// it starts from, the state it ends with.  A tile looks back over its predecessors,
-// composing folds, until it meets a published end state; so the inputs cross HBM
-// once and no tile waits for a chain of others to finish.  What a tile publishes of
+// Between tiles: every tile publishes its fold (A, S); the last of each group of kGroup
+// composes the group's folds, publishes the whole, looks back over the groups before
+// it to the nearest whose end state is known, and publishes its own group's.  A tile
+// takes that state through the folds of its own group; so the inputs cross HBM once
+// and no tile waits for a chain of others to finish.  What a tile publishes of
 // a channel is one 64-bit word, stored and loaded as one atomic access at device
 // scope, so no fence is needed.  The workgroups of a channel tile take their tiles
 // in an order (by a counter of that channel tile) in which a tile's predecessors
@@ -29,9 +30,9 @@
 // a gate per channel) while few sequences are long: then the tiles in flight, two
 // workgroups a compute unit by registers, and what they wait for each other.  T = 32768,
 // bf16, on a card whose large copy moves 4.9 TB/s:
-//   4096 channels, a decay each:          180 us (4.5 TB/s), backward 276 us (4.9 TB/s)
-//   16 heads of 128, softplus gate:       112 us (3.6 TB/s),          202 us (3.3 TB/s)
-//   32 heads of 128, a decay per head, convex: 128 us (4.2 TB/s),     204 us (4.0 TB/s)
+//   4096 channels, a decay each:          184 us (4.4 TB/s), backward 278 us (4.8 TB/s)
+//   16 heads of 128, softplus gate:       110 us (3.7 TB/s),          203 us (3.3 TB/s)
+//   32 heads of 128, a decay per head, convex: 129 us (4.2 TB/s),     204 us (4.0 TB/s)
 // Without the look back (wrong results, timing alone) the softplus case took 103 and
 // 167 us, and without its gate functions the forward took 102 us.
 #include <hip/hip_runtime.h>
@@ -70,18 +71,24 @@ __device__ __forceinline__ void put_state(uint64_t* w, float s) { put(w, kState,
 __device__ __forceinline__ uint32_t hi_of(uint64_t w) { return uint32_t(w >> 32); }
 __device__ __forceinline__ float lo_of(uint64_t w) { return __uint_as_float(uint32_t(w)); }
 
-// The state that reaches a tile of one channel from the `count` (at least one) tiles
-// before it (after it, in the backward): w + c is the nearest one's word and each
-// next one is `step` words on.  It waits for a published state among the nearest
-// kWindow and then takes it through the folds of the tiles between, one by one: the
-// same sums as if each tile had taken its neighbour's state, so how far the look back
-// went does not show in the result.  The states' front advances by up to kWindow
-// tiles per trip to memory.
-constexpr int kWindow = 8;   // 4: 117 us for T = 32768, 16 heads of 128; 8: 113; 16: 117 (twice the words)
+// Tiles of a sequence, counted from its start (its end, in the backward), form groups
+// of kGroup.  A group's last tile, its leader, composes the group's folds and
+// publishes the whole in its word; the state that reaches a group comes from the
+// leaders before it, and a tile takes it through the folds of its own group, one by
+// one.  Which sums are formed depends on the tiles' places alone, not on how far
+// anybody was, and the states' front advances by up to kGroup groups per trip to
+// memory.
+// Forward and backward at T = 32768: 16 heads of 128, sigmoid gate, convex: 118, 247 us
+// with 6, 119, 286 with 8 (whose words spill registers), 118, 238 with 5; 2 heads,
+// softplus gate: 25, 43 us with 6, 23, 41 with 8, 27, 46 with 5.  Without groups, a tile
+// looking back over eight tiles at a time, the 2 heads took 52, 95 us.
+constexpr int kGroup = 6;
 
+// The state after the nearest of `count` (at least one) groups: w + c is the nearest
+// leader's word and each next one is `step` words on.
 __device__ __forceinline__ float look_back(const uint64_t* w, int64_t step, int count, int c) {
-  const int n = min(kWindow, count);
-  uint64_t x[kWindow];
+  const int n = min(kGroup, count);
+  uint64_t x[kGroup];
   for (int polls = 0;; ++polls) {
     // after the first try, two words a poll, the nearest fold (the last to come) and the
     // farthest state (the first): polling all words slows the stores waited for, to a
@@ -90,9 +97,9 @@ __device__ __forceinline__ float look_back(const uint64_t* w, int64_t step, int 
         (hi_of(get(w + c)) != kNothing && hi_of(get(w + step * (n - 1) + c)) == kState)) {
       bool state = false, hole = false;
 #pragma unroll
-      for (int i = 0; i < kWindow; ++i) x[i] = get(w + step * min(i, n - 1) + c);
+      for (int i = 0; i < kGroup; ++i) x[i] = get(w + step * min(i, n - 1) + c);
 #pragma unroll
-      for (int i = 0; i < kWindow; ++i) {
+      for (int i = 0; i < kGroup; ++i) {
         hole |= !state && hi_of(x[i]) == kNothing;
         state |= hi_of(x[i]) == kState;
       }
@@ -103,8 +110,64 @@ __device__ __forceinline__ float look_back(const uint64_t* w, int64_t step, int 
   }
   float s = 0.f;   // what lies beyond the nearest state is overwritten by it
 #pragma unroll
-  for (int i = kWindow - 1; i >= 0; --i)
+  for (int i = kGroup - 1; i >= 0; --i)
     s = hi_of(x[i]) == kState ? lo_of(x[i]) : fmaf(__uint_as_float(hi_of(x[i])), s, lo_of(x[i]));
+  return s;
+}
+
+// The state a tile of one channel starts from.  w: the tile's words; the tile before
+// it is `step` words on; `pos` tiles come before it in its sequence and `left` after
+// it; (A, S): its fold; init: the state the sequence starts from.
+__device__ __forceinline__ float start_state(uint64_t* w, int64_t step, int pos, int left, int c, float init, float A,
+                                             float S) {
+  const int j = pos % kGroup, k = pos / kGroup;
+  const bool leader = j == kGroup - 1 && left > 0;
+  if (left > 0 && !leader) put_fold(w + c, A, S);
+  if (pos == 0) return init;
+  // x[i]: the tile i + 1 before this one
+  uint64_t x[kGroup - 1];
+  const uint64_t* head = w + step * (j + 1) + c;   // the leader of the group before
+  float s = init;
+  for (int polls = 0;; ++polls) {
+    const bool wait_head = k > 0 && !leader;
+    const uint64_t h = wait_head ? get(head) : 0;
+    if (polls == 0 || (hi_of(get(w + step + c)) != kNothing && (!wait_head || hi_of(h) == kState))) {
+      bool hole = wait_head && hi_of(h) != kState;
+#pragma unroll
+      for (int i = 0; i < kGroup - 1; ++i) x[i] = get(w + step * min(i + 1, max(j, 1)) + c);
+#pragma unroll
+      for (int i = 0; i < kGroup - 1; ++i) hole |= i < j && hi_of(x[i]) == kNothing;
+      if (wait_head) s = lo_of(h);
+      if (!hole) break;
+    }
+    if (polls > kMaxPolls) {
+      if (leader) put_state(w + c, __builtin_nanf(""));
+      return __builtin_nanf("");
+    }
+    __builtin_amdgcn_s_sleep(4);
+  }
+  if (leader) {
+    float FA = 1.f, FS = 0.f;
+#pragma unroll
+    for (int i = kGroup - 2; i >= 0; --i) {
+      const float a = __uint_as_float(hi_of(x[i]));
+      FS = fmaf(a, FS, lo_of(x[i]));
+      FA *= a;
+    }
+    FS = fmaf(A, FS, S);
+    FA *= A;
+    if (k > 0) {
+      put_fold(w + c, FA, FS);
+      s = look_back(w + step * kGroup, step * kGroup, k, c);
+    }
+    put_state(w + c, fmaf(FA, s, FS));
+    // read again rather than held: the look back needs the registers
+#pragma unroll
+    for (int i = 0; i < kGroup - 1; ++i) x[i] = get(w + step * (i + 1) + c);
+  }
+#pragma unroll
+  for (int i = kGroup - 2; i >= 0; --i)
+    if (i < j) s = fmaf(__uint_as_float(hi_of(x[i])), s, lo_of(x[i]));
   return s;
 }
 
@@ -313,7 +376,7 @@ __global__ __launch_bounds__(kFwdThreads, 2) void k_scan_fwd(const ScanParams p)
   const ScanTile tile = tile_at<TT, kSaved>(p, take_order(p, ct, nct, &slot), false, row);
   const int64_t sc = int64_t(tile.seq) * p.C + cbase + c;
   float s = 0.f;   // the tile's starting state, known to the lead threads
-  if (tile.idx == 0 && p.h0 && lead) s = p.h0[sc];
+  if (tile.idx < kGroup && p.h0 && lead) s = p.h0[sc];
   if (tile.len == 0) {
     // a sequence without tokens: its state passes through
     if (lead && p.ht) p.ht[sc] = s;
@@ -394,13 +457,9 @@ __global__ __launch_bounds__(kFwdThreads, 2) void k_scan_fwd(const ScanParams p)
       St = fmaf(sA[y][cc], St, sS[y][cc]);
       At *= sA[y][cc];
     }
-    if (tile.idx > 0) {
-      if (tile.after > 0) put_fold(w + c, At, St);
-      s = look_back(w - p.C, -int64_t(p.C), tile.idx, c);
-    }
-    const float end = fmaf(At, s, St);
-    if (tile.after > 0) put_state(w + c, end);
-    else if (p.ht) p.ht[sc] = end;
+    s = start_state(w, -int64_t(p.C), tile.idx, tile.after, c, s, At, St);
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);   // the folds in LDS are read again, not held
+    if (tile.after == 0 && p.ht) p.ht[sc] = fmaf(At, s, St);
     float* saved = p.carry + int64_t(tile.saved) * p.C + cbase + c;
 #pragma unroll
     for (int y = 0; y < LY; ++y) {
@@ -462,7 +521,7 @@ __global__ __launch_bounds__(kBwdThreads, 2) void k_scan_bwd(const ScanParams p)
   const int64_t sc = int64_t(tile.seq) * p.C + cbase + c;
   float* partial = p.part + int64_t(row) * 2 * p.C + cbase + c;
   float s0 = 0.f, e0 = 0.f;
-  if (tile.after == 0 && p.dht && lead) e0 = p.dht[sc];
+  if (tile.after < kGroup && p.dht && lead) e0 = p.dht[sc];
   if (tile.len == 0) {
     if (lead && p.dh0) p.dh0[sc] = e0;
     if (kPar && lead) partial[0] = partial[p.C] = 0.f;
@@ -553,13 +612,9 @@ __global__ __launch_bounds__(kBwdThreads, 2) void k_scan_bwd(const ScanParams p)
       Et = fmaf(sA[y][cc], Et, sE[y][cc]);
       At *= sA[y][cc];
     }
-    if (tile.after > 0) {
-      if (tile.idx > 0) put_fold(w + c, At, Et);
-      e0 = look_back(w + p.C, p.C, tile.after, c);
-    }
-    const float end = fmaf(At, e0, Et);
-    if (tile.idx > 0) put_state(w + c, end);
-    else if (p.dh0) p.dh0[sc] = end;
+    e0 = start_state(w, p.C, tile.after, tile.idx, c, e0, At, Et);
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);   // the folds in LDS are read again, not held
+    if (tile.idx == 0 && p.dh0) p.dh0[sc] = fmaf(At, e0, Et);
 #pragma unroll
     for (int y = LY - 1; y >= 0; --y) {
       const float Ey = sE[y][cc];

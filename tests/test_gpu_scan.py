@@ -120,6 +120,20 @@ def test_many_tiles_and_sequences():
     compare(got, ref)
 
 
+@pytest.mark.parametrize("kind,dtype,H,D,convex", [(0, "f32", 3, 1, False), (1, "bf16", 1, 8, True),
+                                                   (0, "bf16", 1, 16, False)])
+def test_lengths_at_the_borders_of_groups(kind, dtype, H, D, convex):
+    """Tiles of 64, 128 and 256 tokens, six to a group: sequences of a group of tiles,
+    a token more or less, a tile more, and of more than six groups."""
+    lengths = [384, 385, 383, 448, 449, 768, 769, 0, 896, 897, 1, 1536, 1537, 1793, 64 * 37 + 1, 128 * 37]
+    t, dy, dht = make(61 + kind, kind, dtype, lengths, H, D)
+    ref = R.scan(kind, t["x"], t["g"], t["A_log"], t["dt_bias"], t["h0"], lengths, GS, convex, dy, dht)
+    d = dev(t)
+    got = run(problem(kind, dtype, lengths, H, D, convex, False), d, dy.cuda(), dht.cuda(), kind, len(lengths), H, D)
+    torch.cuda.synchronize()
+    compare(got, ref)
+
+
 @pytest.mark.parametrize("dense", [True, False])
 def test_no_tokens(dense):
     """T = 0: the states pass through, the parameter gradients are zero."""
