@@ -668,9 +668,11 @@ __global__ __launch_bounds__(kBwdThreads, 2) void k_scan_bwd(const ScanParams p)
         dx[v] = ds;
       }
       if constexpr (kPar) {
+        // rows past the end add nothing, whatever state or gradient passes them (an
+        // infinite one times their slope of zero would be a NaN in the sums)
+        dl = r < tile.len ? dl : 0.f;
         dg[v] = dl * dz[i][v];
-        // d lambda / d A_log: lambda, or the slope by z times z; rows past the end
-        // have neither
+        // d lambda / d A_log: lambda, or the slope by z times z
         if constexpr (GM == kScanSoftplus)
           sumA[v] = fmaf(dl, fmaxf(l[i][v], -3.0e38f), sumA[v]);
         else
