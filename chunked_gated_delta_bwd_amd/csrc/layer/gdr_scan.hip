@@ -71,6 +71,14 @@ __device__ __forceinline__ void put_state(uint64_t* w, float s) { put(w, kState,
 __device__ __forceinline__ uint32_t hi_of(uint64_t w) { return uint32_t(w >> 32); }
 __device__ __forceinline__ float lo_of(uint64_t w) { return __uint_as_float(uint32_t(w)); }
 
+// The product p of decays of which `least` is the least.  If none is zero the product
+// is not either: where it leaves fp32's range the least positive number stands for it,
+// so that an infinite state before them is infinite after them, as token by token, and
+// not 0 * inf = NaN.  A finite state gains 2^-149 of itself at most.
+__device__ __forceinline__ float decay_product(float p, float least) {
+  return p == 0.f && least != 0.f ? __uint_as_float(1) : p;
+}
+
 // Tiles of a sequence, counted from its start (its end, in the backward), form groups
 // of kGroup.  A group's last tile, its leader, composes the group's folds and
 // publishes the whole in its word; the state that reaches a group comes from the
@@ -147,15 +155,16 @@ __device__ __forceinline__ float start_state(uint64_t* w, int64_t step, int pos,
     __builtin_amdgcn_s_sleep(4);
   }
   if (leader) {
-    float FA = 1.f, FS = 0.f;
+    float FA = 1.f, FS = 0.f, least = A;
 #pragma unroll
     for (int i = kGroup - 2; i >= 0; --i) {
       const float a = __uint_as_float(hi_of(x[i]));
       FS = fmaf(a, FS, lo_of(x[i]));
       FA *= a;
+      least = fminf(least, a);
     }
     FS = fmaf(A, FS, S);
-    FA *= A;
+    FA = decay_product(FA * A, least);
     if (k > 0) {
       put_fold(w + c, FA, FS);
       s = look_back(w + step * kGroup, step * kGroup, k, c);
@@ -276,6 +285,23 @@ __device__ __forceinline__ int take_order(const ScanParams& p, int ct, int nct, 
   if (threadIdx.x == 0) *slot = int(atomicAdd(p.counters + int64_t(ct) * kScanCounterStep, 1u));
   chain_barrier();
   return __builtin_amdgcn_readfirstlane(*slot);   // the same for all: keep it scalar
+}
+
+// decay_product for a thread's L tokens of VEC channels.  So few tokens seldom underflow:
+// their decays are looked at again rather than kept track of.
+template <int L, int VEC>
+__device__ __forceinline__ void keep_nonzero(float (&A)[VEC], const float (&a)[L][VEC]) {
+  bool any = false;
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) any |= A[v] == 0.f;
+  if (!any) return;
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) {
+    bool zero = false;
+#pragma unroll
+    for (int i = 0; i < L; ++i) zero |= a[i][v] == 0.f;
+    if (A[v] == 0.f && !zero) A[v] = __uint_as_float(1);
+  }
 }
 
 // The gate of VEC channels: base-2 log decays, and what its gradient needs.
@@ -444,6 +470,7 @@ __global__ __launch_bounds__(kFwdThreads, 2) void k_scan_fwd(const ScanParams p)
         A[v] *= a[i][v];
       }
     }
+    keep_nonzero<L, VEC>(A, a);
 #pragma unroll
     for (int v = 0; v < VEC; ++v) { sA[ly][col(v)] = A[v]; sS[ly][col(v)] = S[v]; }
   }
@@ -451,12 +478,14 @@ __global__ __launch_bounds__(kFwdThreads, 2) void k_scan_fwd(const ScanParams p)
   // one thread per channel composes the groups, and publishes before it does more
   if (lead) {
     uint64_t* w = p.words + int64_t(row) * p.C + cbase;
-    float At = 1.f, St = 0.f;
+    float At = 1.f, St = 0.f, least = 1.f;
 #pragma unroll
     for (int y = 0; y < LY; ++y) {
       St = fmaf(sA[y][cc], St, sS[y][cc]);
       At *= sA[y][cc];
+      least = fminf(least, sA[y][cc]);
     }
+    At = decay_product(At, least);
     s = start_state(w, -int64_t(p.C), tile.idx, tile.after, c, s, At, St);
     __atomic_signal_fence(__ATOMIC_SEQ_CST);   // the folds in LDS are read again, not held
     if (tile.after == 0 && p.ht) p.ht[sc] = fmaf(At, s, St);
@@ -596,6 +625,7 @@ __global__ __launch_bounds__(kBwdThreads, 2) void k_scan_bwd(const ScanParams p)
 #pragma unroll
       for (int v = 0; v < VEC; ++v) E[v] = a[i][v] * (dy[v] + E[v]);
     }
+    keep_nonzero<L, VEC>(A, a);
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
       sA[ly][col(v)] = A[v];
@@ -606,12 +636,14 @@ __global__ __launch_bounds__(kBwdThreads, 2) void k_scan_bwd(const ScanParams p)
   chain_barrier();
   if (lead) {
     uint64_t* w = p.words + int64_t(row) * p.C + cbase;
-    float At = 1.f, Et = 0.f;
+    float At = 1.f, Et = 0.f, least = 1.f;
 #pragma unroll
     for (int y = LY - 1; y >= 0; --y) {
       Et = fmaf(sA[y][cc], Et, sE[y][cc]);
       At *= sA[y][cc];
+      least = fminf(least, sA[y][cc]);
     }
+    At = decay_product(At, least);
     e0 = start_state(w, p.C, tile.after, tile.idx, c, e0, At, Et);
     __atomic_signal_fence(__ATOMIC_SEQ_CST);   // the folds in LDS are read again, not held
     if (tile.idx == 0 && p.dh0) p.dh0[sc] = fmaf(At, e0, Et);

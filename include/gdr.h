@@ -250,8 +250,11 @@ gdr_status gdr_step(const gdr_shape* shape, const gdr_inputs* in, float* state, 
  * GDR_GATE_SCALAR takes one log decay per token and head, shared by the head's D
  * channels (D == 1: one per channel); the per-channel gates take g, A_log and
  * dt_bias as the delta rule does.  The log decay is meant to be <= 0; -inf is a
- * reset (a = 0).  A positive one is taken as it stands as long as the product of
- * exp(lambda) over any run of tokens stays in the fp32 range.
+ * reset (a = 0), and so is one below -87.3 (exp(lambda) < 2^-126).  A positive one is
+ * taken as it stands as long as the product of exp(lambda) over any run of tokens
+ * stays in the fp32 range.  Infinities and NaN in x, h0, dy and dht go where the
+ * formulas take them token by token, and no further (0 times infinity is NaN: an
+ * infinite state does not pass a reset unharmed).
  * The backward returns the gradients of L = sum_t <dy_t, y_t> + <dht, s_T>.
  * x, y: [B,T,H,D] (or packed [1,T,H,D]), 1 <= D <= 256 with D == 1 or a multiple
  * of 8; B, T, N, cu_seqlens_host, dtype and alignment as in gdr_shape.  States,

@@ -30,3 +30,77 @@ def test_parameter_sums_of_a_ragged_end_take_no_state_after_it(kind, dtype, bad)
         g = got[k].cpu().double()
         assert torch.equal(g.isnan() if bad != bad else g == bad, want)
         R.check(k, torch.where(want, 0.0, g), torch.where(want, 0.0, ref[k][0]), torch.where(want, 0.0, ref[k][1]), got[k].dtype)
+
+
+# kind, dtype, H, D, convex: a decay per channel, per head, softplus and sigmoid gates
+RUNS = [(0, "f32", 5, 1, False), (0, "bf16", 2, 8, False), (0, "f32", 2, 16, True), (1, "bf16", 2, 8, False),
+        (2, "f32", 2, 8, True)]
+
+
+@pytest.mark.parametrize("kind,dtype,H,D,convex", RUNS)
+@pytest.mark.parametrize("T", [60, 700, 64 * 40 + 7])
+def test_an_infinity_lasts_through_decays_whose_product_underflows(kind, dtype, H, D, convex, T):
+    """Strong decays, none of them zero in fp32 (e^-20 a token; the product of six is below
+    2^-149): an infinite state stays what it is token by token, within a thread's tokens, a
+    tile's groups, a group of tiles and beyond; so does an infinite gradient, backwards."""
+    def strong(t):
+        if kind == 0:
+            t["g"][:] = -20.0
+        elif kind == 1:      # softplus(4.5) e^1.5 = 20.2
+            t["A_log"][:], t["dt_bias"][:], t["g"][:] = 1.5, 0.0, 4.5
+        else:                # 20 sigmoid(6) = 19.95
+            t["A_log"][:], t["dt_bias"][:], t["g"][:] = 0.0, 0.0, 6.0
+        return t
+    gs = -20.0 if kind == 2 else S.GS
+    t, dy, dht = S.make(6 + kind, kind, dtype, [T], H, D)
+    strong(t)
+    prob = S.B.ScanProblem(1, T, H, D, 1, kind, S.CODE[dtype], gate_scale=gs, convex=convex)
+    inf = float("inf")
+
+    def go(name, at, value):
+        """One infinity in one input; every output against the reference."""
+        u = {**t, "dy": dy, "dht": dht}
+        u[name] = u[name].clone()
+        u[name][at] = value
+        ref = R.scan(kind, u["x"], u["g"], u["A_log"], u["dt_bias"], u["h0"], [T], gs, convex, u["dy"], u["dht"])
+        d = S.dev(u)
+        got = S.run(prob, d, d["dy"], d["dht"], kind, 1, H, D)
+        torch.cuda.synchronize()
+        for k in ("y", "ht") if name in ("x", "h0") else ("dx", "dg", "dh0"):
+            g, (want, err) = got[k].cpu().double(), ref[k]
+            assert torch.equal(g.isnan(), want.isnan()), (name, k, int(g.isnan().sum()), int(want.isnan().sum()))
+            odd = ~want.isfinite()
+            assert torch.equal(g[odd & ~want.isnan()], want[odd & ~want.isnan()]), (name, k)
+            z = torch.zeros(())
+            R.check(k, torch.where(odd, z.double(), g), torch.where(odd, z.double(), want),
+                    torch.where(odd, z.double(), err), got[k].dtype)
+        return ref
+
+    ref = go("x", (3, 0, 0), inf)
+    assert ref["y"][0][3:, 0, 0].isinf().all()
+    go("x", (T - 5, H - 1, D - 1), -inf)
+    ref = go("h0", (0, 1, 0), -inf)
+    assert ref["ht"][0].isinf().sum() == 1
+    ref = go("dy", (T - 7, 0, 0), inf)
+    assert ref["dx"][0][:T - 6, 0, 0].isinf().all()
+    ref = go("dht", (0, 1, D - 1), -inf)
+    assert ref["dh0"][0].isinf().sum() == 1
+
+
+def test_a_shut_gate_still_cuts():
+    """A decay of exactly zero among those that underflow: nothing before it is felt, and an
+    infinity before it is 0 * inf = NaN from there on, as token by token."""
+    T, H = 900, 3
+    t, dy, dht = S.make(9, 0, "f32", [T], H, 1)
+    t["g"][:] = -20.0
+    t["g"][400] = float("-inf")
+    t["x"][2, 1] = float("inf")
+    ref = R.scan(0, t["x"], t["g"], None, None, t["h0"], [T], S.GS, False, dy, dht)
+    got = S.run(S.problem(0, "f32", [T], H, 1, False, True), S.dev(t), dy.cuda(), dht.cuda(), 0, 1, H, 1)
+    torch.cuda.synchronize()
+    y = got["y"].cpu()
+    assert y[400:, 1].isnan().all() and (y[2:400, 1] == float("inf")).all()
+    keep = [0, 2]
+    for k in ("y", "dx", "dg"):
+        R.check(k, got[k][:, keep], ref[k][0][:, keep], ref[k][1][:, keep])
+    assert torch.equal(y[400, keep], t["x"][400, keep])
