@@ -261,6 +261,13 @@ def _bad(message: str) -> None:
     raise GdrError(GDR_EINVAL, message)
 
 
+def _check_range(bits: int, **fields) -> None:
+    """ctypes keeps the low bits of a number that a C integer of that width cannot hold."""
+    for name, value in fields.items():
+        if not -(1 << (bits - 1)) <= value < 1 << (bits - 1):
+            raise GdrError(GDR_EUNSUPPORTED, f"{name} ({value}) is beyond {bits} bits")
+
+
 def _check_tensors(specs) -> None:
     """specs: (name, tensor or None, numel, dtype).  Every tensor given has that type
     and size, is contiguous, and lies on the current GPU, where the call is enqueued."""
@@ -303,6 +310,7 @@ def _pool_size(state: torch.Tensor, per_state: int) -> int:
     """Number of states in a pool [P, ...] of per_state elements each."""
     if state.dim() < 1 or state.numel() != state.shape[0] * per_state:
         _bad(f"state has shape {tuple(state.shape)}, expected [P, ...] with {per_state} elements a state")
+    _check_range(32, **{"state's first dimension": state.shape[0]})
     return state.shape[0]
 
 
@@ -311,6 +319,7 @@ class ScanProblem:
 
     def __init__(self, B: int, T: int, H: int, D: int, N: int, gate: int, dtype: int, cu_seqlens=None,
                  gate_scale: float = 0.0, convex: bool = False):
+        _check_range(32, B=B, T=T, H=H, D=D, N=N, gate=gate, dtype=dtype, convex=convex)
         self.cu = None
         if cu_seqlens is not None:
             self.cu = torch.as_tensor(cu_seqlens, dtype=torch.int64).contiguous().cpu()
@@ -403,6 +412,8 @@ class NormProblem:
     """Host-side description of one row norm (gdr_norm_shape)."""
 
     def __init__(self, rows: int, width: int, dtype: int, eps: float = 1e-6, group: int = 0):
+        _check_range(64, rows=rows)
+        _check_range(32, width=width, dtype=dtype, group=group)
         self.shape = NormShape(rows, width, dtype, eps, group)
         self.ref = ctypes.byref(self.shape)
         self.numel, self.width, self.io = rows * width, width, _DTYPE.get(dtype)

@@ -1,0 +1,72 @@
+"""Arguments of the operators around the delta rule that the binding or the C ABI has to
+refuse or to ignore, checked without a GPU."""
+
+import ctypes
+import os
+
+import pytest
+import torch
+
+from chunked_gated_delta_bwd_amd import binding as B
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _library():
+    if not os.path.exists(B.library_path()):
+        from chunked_gated_delta_bwd_amd import build
+        build.build()
+    B.load_library()
+
+
+def refused(status, text, fn, *args, **kw):
+    with pytest.raises(B.GdrError) as e:
+        fn(*args, **kw)
+    assert e.value.status == status, str(e.value)
+    assert text in str(e.value), str(e.value)
+
+
+WIDE = 1 << 32
+
+
+@pytest.mark.parametrize("field", ["B", "T", "H", "D", "N", "gate", "dtype", "convex"])
+def test_a_scan_shape_beyond_32_bits_is_refused(field):
+    """A C int would keep the low bits: T = 2^32 + 300 would be 300 tokens."""
+    args = dict(B=1, T=300, H=2, D=64, N=1, gate=0, dtype=B.GDR_BF16, convex=0)
+    for add in (WIDE, 1 << 31, -WIDE):
+        refused(B.GDR_EUNSUPPORTED, field, B.ScanProblem, **{**args, field: args[field] + add})
+    B.gdr_scan_workspace_bytes(B.ScanProblem(**args))
+
+
+@pytest.mark.parametrize("field", ["width", "dtype", "group"])
+def test_a_norm_shape_beyond_32_bits_is_refused(field):
+    """group = 2^32 + 128 would be 128 with scales for one group a row."""
+    args = dict(rows=4, width=300, dtype=B.GDR_BF16, group=128)
+    for add in (WIDE, 1 << 31, -WIDE):
+        refused(B.GDR_EUNSUPPORTED, field, B.NormProblem, **{**args, field: args[field] + add})
+    B.gdr_norm_workspace_bytes(B.NormProblem(**args))
+
+
+def test_norm_rows_beyond_64_bits_are_refused():
+    refused(B.GDR_EUNSUPPORTED, "rows", B.NormProblem, (1 << 64) + 4, 128, B.GDR_BF16)
+
+
+class Pool:
+    """A state pool too large to make here."""
+
+    def __init__(self, *shape):
+        self.shape = shape
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        n = 1
+        for s in self.shape:
+            n *= s
+        return n
+
+
+def test_a_pool_of_2_to_the_31_states_is_refused():
+    assert B._pool_size(Pool((1 << 31) - 1, 1, 1), 1) == (1 << 31) - 1
+    for P in (1 << 31, WIDE + 5):
+        refused(B.GDR_EUNSUPPORTED, "state", B._pool_size, Pool(P, 1, 1), 1)
