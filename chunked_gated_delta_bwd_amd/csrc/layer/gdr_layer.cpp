@@ -306,7 +306,13 @@ gdr_status gdr_scan_step(const gdr_scan_shape* shape, const gdr_scan_inputs* in,
 gdr_status gdr_step(const gdr_shape* shape, const gdr_inputs* in, float* state, int32_t P, const int32_t* slots,
                     void* o, void* stream) {
   size_t bytes = 0;
-  gdr_status st = gdr_workspace_bytes(shape, &bytes);   // checks the shape; a step needs no workspace
+  gdr_shape unsplit;
+  if (shape) {
+    unsplit = *shape;
+    unsplit.seq_split = 1;   // there is no sequence to split, whatever the shape says
+  }
+  // checks the shape; a step needs no workspace
+  gdr_status st = gdr_workspace_bytes(shape ? &unsplit : nullptr, &bytes);
   if (st != GDR_OK) return st;
   if (shape->cu_seqlens_host || shape->T != 1) return set_error(GDR_EINVAL, "a step takes a dense shape with T == 1");
   if (int64_t(shape->N) * shape->H * (shape->Dk / 32) * 256 >= gdr::kMaxThreads)

@@ -70,3 +70,13 @@ def test_a_pool_of_2_to_the_31_states_is_refused():
     assert B._pool_size(Pool((1 << 31) - 1, 1, 1), 1) == (1 << 31) - 1
     for P in (1 << 31, WIDE + 5):
         refused(B.GDR_EUNSUPPORTED, "state", B._pool_size, Pool(P, 1, 1), 1)
+
+
+@pytest.mark.parametrize("seq_split", [-1, -7, 0, 1, 5, 1 << 20])
+def test_a_step_ignores_the_sequence_split(seq_split):
+    """Whatever seq_split holds, the refusal is the one for the missing output."""
+    prob = B.Problem(1, 1, 2, 64, 1, 0, B.GDR_BF16, 1.0, seq_split=seq_split)
+    x = 0x100000
+    inp = B.Inputs(x, x, x, x, x, None, None, None)
+    refused(B.GDR_EINVAL, "o is NULL", lambda: B._check(B.load_library().gdr_step(
+        ctypes.byref(prob.shape), ctypes.byref(inp), x, 1, None, None, None)))
