@@ -296,6 +296,14 @@ def _check_tensors(specs) -> None:
         _bad(f"tensors are on cuda:{first}, the current device is cuda:{torch.cuda.current_device()}")
 
 
+def _stream_here(stream) -> Optional[int]:
+    """The stream's handle; it has to be the current device's, where _check_tensors found the tensors."""
+    here = getattr(stream, "device_index", None)
+    if here is not None and here != torch.cuda.current_device():
+        _bad(f"the stream is on cuda:{here}, the current device is cuda:{torch.cuda.current_device()}")
+    return _stream(stream)
+
+
 def _check_workspace(ws: Optional[torch.Tensor], like: Optional[torch.Tensor]) -> int:
     if ws is None:
         return 0
@@ -362,7 +370,7 @@ def gdr_scan_fwd(prob: ScanProblem, t: Dict, ws: torch.Tensor, y: torch.Tensor, 
     _check_tensors(prob.input_specs(t) + (("y", y, prob.x_numel, prob.io), ("ht", ht, prob.state_numel, torch.float32)))
     n = _check_workspace(ws, y)
     inp = _scan_inputs(t)
-    _check(load_library().gdr_scan_fwd(prob.ref, ctypes.byref(inp), _ptr(ws), n, _ptr(y), _ptr(ht), _stream(stream)))
+    _check(load_library().gdr_scan_fwd(prob.ref, ctypes.byref(inp), _ptr(ws), n, _ptr(y), _ptr(ht), _stream_here(stream)))
 
 
 def gdr_scan_bwd(prob: ScanProblem, t: Dict, dy: torch.Tensor, dht: Optional[torch.Tensor], ws: torch.Tensor,
@@ -378,7 +386,7 @@ def gdr_scan_bwd(prob: ScanProblem, t: Dict, dy: torch.Tensor, dht: Optional[tor
     gr = ScanGrads(_ptr(out["dx"]), _ptr(out["dg"]), _ptr(out.get("dh0")), _ptr(out.get("dA_log")),
                    _ptr(out.get("ddt_bias")))
     _check(load_library().gdr_scan_bwd(prob.ref, ctypes.byref(inp), _ptr(dy), _ptr(dht), _ptr(ws), n, ctypes.byref(gr),
-                                       _stream(stream)))
+                                       _stream_here(stream)))
 
 
 def gdr_scan_step(prob: ScanProblem, t: Dict, state: torch.Tensor, y: torch.Tensor,
@@ -388,7 +396,7 @@ def gdr_scan_step(prob: ScanProblem, t: Dict, state: torch.Tensor, y: torch.Tens
                                           ("slots", slots, prob.rows, torch.int32)))
     inp = _scan_inputs(t)
     _check(load_library().gdr_scan_step(prob.ref, ctypes.byref(inp), _ptr(state), P, _ptr(slots), _ptr(y),
-                                        _stream(stream)))
+                                        _stream_here(stream)))
 
 
 def gdr_step(prob: Problem, t: Dict, state: torch.Tensor, o: torch.Tensor, slots: Optional[torch.Tensor] = None,
@@ -405,7 +413,7 @@ def gdr_step(prob: Problem, t: Dict, state: torch.Tensor, o: torch.Tensor, slots
                     ("state", state, state.numel(), torch.float32), ("slots", slots, N, torch.int32)))
     inp = _inputs(t)
     _check(load_library().gdr_step(ctypes.byref(s), ctypes.byref(inp), _ptr(state), P, _ptr(slots), _ptr(o),
-                                   _stream(stream)))
+                                   _stream_here(stream)))
 
 
 class NormProblem:
@@ -435,7 +443,7 @@ def gdr_norm_fwd(prob: NormProblem, x: torch.Tensor, w: Optional[torch.Tensor], 
     n, io = prob.numel, prob.io
     _check_tensors((("x", x, n, io), ("w", w, prob.width, torch.float32), ("y", y, n, io), ("res", res, n, io),
                     ("res_out", res_out, n, io)))
-    _check(load_library().gdr_norm_fwd(prob.ref, _ptr(x), _ptr(res), _ptr(w), _ptr(y), _ptr(res_out), _stream(stream)))
+    _check(load_library().gdr_norm_fwd(prob.ref, _ptr(x), _ptr(res), _ptr(w), _ptr(y), _ptr(res_out), _stream_here(stream)))
 
 
 def gdr_norm_quant(prob: NormProblem, x: torch.Tensor, w: Optional[torch.Tensor], q: torch.Tensor,
@@ -446,7 +454,7 @@ def gdr_norm_quant(prob: NormProblem, x: torch.Tensor, w: Optional[torch.Tensor]
                     ("scales", scales, prob.scales_numel, torch.float32), ("res", res, n, io),
                     ("res_out", res_out, n, io)))
     _check(load_library().gdr_norm_quant(prob.ref, _ptr(x), _ptr(res), _ptr(w), _ptr(q), _ptr(scales), _ptr(res_out),
-                                         _stream(stream)))
+                                         _stream_here(stream)))
 
 
 def gdr_norm_bwd(prob: NormProblem, r: torch.Tensor, w: Optional[torch.Tensor], dy: torch.Tensor, dx: torch.Tensor,
@@ -456,7 +464,7 @@ def gdr_norm_bwd(prob: NormProblem, r: torch.Tensor, w: Optional[torch.Tensor], 
     _check_tensors((("r", r, n, io), ("w", w, prob.width, torch.float32), ("dy", dy, n, io), ("dx", dx, n, io),
                     ("dw", dw, prob.width, torch.float32), ("dres", dres, n, io)))
     _check(load_library().gdr_norm_bwd(prob.ref, _ptr(r), _ptr(w), _ptr(dy), _ptr(dres), _ptr(ws),
-                                       _check_workspace(ws, dy), _ptr(dx), _ptr(dw), _stream(stream)))
+                                       _check_workspace(ws, dy), _ptr(dx), _ptr(dw), _stream_here(stream)))
 
 
 # ---------------------------------------------------------------------------

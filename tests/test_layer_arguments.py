@@ -80,3 +80,54 @@ def test_a_step_ignores_the_sequence_split(seq_split):
     inp = B.Inputs(x, x, x, x, x, None, None, None)
     refused(B.GDR_EINVAL, "o is NULL", lambda: B._check(B.load_library().gdr_step(
         ctypes.byref(prob.shape), ctypes.byref(inp), x, 1, None, None, None)))
+
+
+class Stream:
+    def __init__(self, device_index):
+        self.device_index, self.cuda_stream = device_index, 0
+
+
+class Reached(Exception):
+    pass
+
+
+class Library:
+    """Stands in for the loaded library: no call may get this far."""
+
+    def __getattr__(self, name):
+        def entry(*args):
+            raise Reached(name)
+        return entry
+
+
+def entry_points():
+    bf, f32 = torch.bfloat16, torch.float32
+    x, w, st = torch.zeros(2, 64, dtype=bf), torch.zeros(64), torch.zeros(2, 1, 64)
+    ws, S = torch.zeros(256, dtype=torch.uint8), torch.zeros(2, 1, 64, 64)
+    scan, one = B.ScanProblem(1, 2, 1, 64, 1, 0, B.GDR_BF16), B.ScanProblem(2, 1, 1, 64, 2, 0, B.GDR_BF16)
+    norm, t = B.NormProblem(2, 64, B.GDR_BF16), {"x": x, "g": torch.zeros(2, 1, dtype=bf)}
+    q = {"q": x, "k": x, "v": x, "g": t["g"], "b": t["g"]}
+    return {
+        "gdr_scan_fwd": lambda s: B.gdr_scan_fwd(scan, t, ws, x, stream=s),
+        "gdr_scan_bwd": lambda s: B.gdr_scan_bwd(scan, t, x, None, ws, {"dx": x, "dg": t["g"]}, stream=s),
+        "gdr_scan_step": lambda s: B.gdr_scan_step(one, t, st, x, stream=s),
+        "gdr_step": lambda s: B.gdr_step(B.Problem(2, 1, 1, 64, 2, 0, B.GDR_BF16, 1.0), q, S, x, stream=s),
+        "gdr_norm_fwd": lambda s: B.gdr_norm_fwd(norm, x, w, x, stream=s),
+        "gdr_norm_quant": lambda s: B.gdr_norm_quant(norm, x, w, x.to(torch.float8_e4m3fn), torch.zeros(2, 1, dtype=f32), stream=s),
+        "gdr_norm_bwd": lambda s: B.gdr_norm_bwd(norm, x, w, x, x, None, None, stream=s),
+    }
+
+
+@pytest.mark.parametrize("name", ["gdr_scan_fwd", "gdr_scan_bwd", "gdr_scan_step", "gdr_step", "gdr_norm_fwd",
+                                  "gdr_norm_quant", "gdr_norm_bwd"])
+def test_a_stream_of_another_device_is_refused(name, monkeypatch):
+    """The tensors are on the current device, so the call has to run there: on a stream of
+    another one the kernels would run on that device, on memory it may not reach."""
+    call = entry_points()[name]
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(B, "_check_tensors", lambda specs: None)     # they are on the CPU here
+    monkeypatch.setattr(B, "load_library", lambda: Library())
+    refused(B.GDR_EINVAL, "stream is on cuda:1", call, Stream(1))
+    for same in (Stream(0), 0):
+        with pytest.raises(Reached, match=name):
+            call(same)
