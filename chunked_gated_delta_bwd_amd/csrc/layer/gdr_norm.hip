@@ -207,12 +207,15 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm(const NormParams
         if (n <= 0 || row >= p.rows) continue;
         const float s = scale_of(gm[u][i]);
         if (p.group ? c % 128 == 0 : c == 0) p.scales[row * groups + c / (p.group ? 128 : p.width)] = s;
-        const float inv = 1.f / s;
+        // y / s rounded once: the product with the reciprocal and its remainder.  The
+        // product alone put one byte in four million on the other side of a border.
+        const float inv = 1.f / s, d = s == __builtin_inff() ? 3.0e38f : s;   // y / inf = 0
         float z[VEC];
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
-          const float t = r[u][i][v] * inv;   // 448 (1 + 2^-23) at most: the clamp is of rounding alone
-          z[v] = t != t ? t : fminf(fmaxf(t, -kE4m3Max), kE4m3Max);
+          const float y = r[u][i][v], p = y * inv;
+          // signs as they are so that -0 stays -0; at most 448 (1 + 2^-23), whose byte is 448's
+          z[v] = fmaf(-fmaf(p, d, -y), inv, p);
         }
         uint8_t* q = static_cast<uint8_t*>(p.q) + row * p.width + c;
         typedef uint32_t __attribute__((aligned(1))) u32u;

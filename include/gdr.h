@@ -333,7 +333,7 @@ gdr_status gdr_norm_fwd(const gdr_norm_shape* shape, const void* x, const void* 
 
 /* The same with an 8-bit output: per row and group of channels
  *   scale = max(max|y| / 448, 2^-126),  q = e4m3(y / scale)
- * (OCP e4m3, round to nearest even), so that q * scale stands for y.  q:
+ * (OCP e4m3, the fp32 quotient to nearest even), so that q * scale stands for y.  q:
  * [rows,width] bytes; scales: [rows,ceil(width / group)] fp32 (group 0: [rows,1];
  * the last group of a width that is no multiple of it is shorter).  A group that
  * holds a NaN gets a NaN scale and NaN bytes. */
