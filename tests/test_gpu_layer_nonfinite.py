@@ -104,3 +104,24 @@ def test_a_shut_gate_still_cuts():
     for k in ("y", "dx", "dg"):
         R.check(k, got[k][:, keep], ref[k][0][:, keep], ref[k][1][:, keep])
     assert torch.equal(y[400, keep], t["x"][400, keep])
+
+
+@pytest.mark.parametrize("kind,dtype", [(0, "f32"), (0, "bf16")])
+def test_a_decay_below_the_normal_numbers_is_a_reset(kind, dtype):
+    """e^-88 < 2^-126: nothing is left of a state of 1e37, by token, by tile or by step; and
+    e^-87 > 2^-126 leaves its share."""
+    T, H, B = 300, 2, S.B
+    t, dy, dht = S.make(4, kind, dtype, [T], H, 1)
+    for lam, left in ((-88.0, False), (-87.0, True)):
+        t["g"][:], t["x"][:], t["h0"][:] = 0.0, 0.0, 1e37
+        t["g"][0] = lam
+        want = torch.tensor(1e37, dtype=torch.float64) * torch.tensor(lam, dtype=torch.float64).exp() if left else 0.0
+        got = S.run(S.problem(kind, dtype, [T], H, 1, False, True), S.dev(t), dy.cuda(), dht.cuda(), kind, 1, H, 1)
+        state, y = t["h0"].cuda(), torch.full((1, H, 1), float("nan"), dtype=S.DT[dtype], device="cuda")
+        one = B.ScanProblem(1, 1, H, 1, 1, kind, S.CODE[dtype])
+        B.gdr_scan_step(one, {"x": t["x"][:1].cuda(), "g": t["g"][:1].cuda()}, state, y)
+        torch.cuda.synchronize()
+        for name, v in (("ht", got["ht"]), ("y", got["y"]), ("state", state)):
+            # e^-87: lambda's 87 carries U relative, 8 |lambda| U in the exponential
+            ref = torch.full(v.shape, float(want), dtype=torch.float64)
+            R.check(name, v, ref, (16 + 8 * 87) * R.U * ref.abs())
