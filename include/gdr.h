@@ -258,9 +258,10 @@ gdr_status gdr_step(const gdr_shape* shape, const gdr_inputs* in, float* state, 
  * The backward returns the gradients of L = sum_t <dy_t, y_t> + <dht, s_T>.
  * x, y: [B,T,H,D] (or packed [1,T,H,D]), 1 <= D <= 256 with D == 1 or a multiple
  * of 8; B, T, N, cu_seqlens_host, dtype and alignment as in gdr_shape.  States,
- * products and sums are fp32; y, dx and dg are rounded once to dtype.  Counting
- * a tile for every 64 tokens of a sequence (at least one), GDR_EUNSUPPORTED from
- * 2^24 tiles times ceil(H D / 64) on. */
+ * products and sums are fp32; y, dx and dg are rounded once to dtype.
+ * GDR_EUNSUPPORTED above 2^21 channels H D, from 2^31 tokens B T or 2^40 elements on,
+ * and where a launch would take 2^32 threads: not with fewer than 2^24 tiles times
+ * ceil(H D / 64), counting a tile for every 64 tokens of a sequence (at least one). */
 typedef struct {
   int32_t B, T, H, D;               /* dense: [B,T,H,D]; varlen: B == 1, T == total tokens */
   int32_t N;                        /* sequences, as in gdr_shape */

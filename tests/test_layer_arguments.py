@@ -131,3 +131,23 @@ def test_a_stream_of_another_device_is_refused(name, monkeypatch):
     for same in (Stream(0), 0):
         with pytest.raises(Reached, match=name):
             call(same)
+
+
+@pytest.mark.parametrize("kw,fits", [
+    (dict(H=1 << 21, D=1, T=1), True),
+    (dict(H=(1 << 21) + 1, D=1, T=1), False),
+    (dict(H=1 << 13, D=256, T=1), True),
+    (dict(H=(1 << 13) + 1, D=256, T=1), False),
+    (dict(H=1, D=1, T=(1 << 31) - 1), False),              # 2^24 tiles of 128 tokens
+    (dict(H=1, D=1, T=(1 << 31) - 128), True),
+    (dict(H=1, D=1, T=(1 << 30) - 64, convex=True), True),  # tiles of 64
+    (dict(H=1, D=1, T=1 << 30, convex=True), False),
+    (dict(H=8192, D=8, B=2, N=2, T=1 << 23), False),       # 2^40 elements
+])
+def test_the_largest_recurrences(kw, fits):
+    args = dict(B=1, N=1, gate=0, dtype=B.GDR_BF16)
+    p = B.ScanProblem(**{**args, **kw})
+    if fits:
+        assert B.gdr_scan_workspace_bytes(p) > 0
+    else:
+        refused(B.GDR_EUNSUPPORTED, "too large", B.gdr_scan_workspace_bytes, p)
