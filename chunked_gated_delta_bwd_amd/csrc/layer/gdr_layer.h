@@ -32,6 +32,8 @@ constexpr int bwd_tile(int gate, bool wide, bool convex) {
   return scan_long(gate, wide) || (gate == kScanLog && !convex) ? 128 : 64;
 }
 constexpr int fwd_tile(int gate, bool wide) { return scan_long(gate, wide) ? 256 : 128; }
+// Tiles of a sequence of `len` tokens, at least one.  (len + tile - 1 may pass 32 bits.)
+constexpr int scan_tiles(int len, int tile) { return len > 0 ? (len - 1) / tile + 1 : 1; }
 
 // One row per tile: at most a tile's tokens of one sequence.  A sequence without
 // tokens has one empty tile, so that its states are passed through.

@@ -270,10 +270,10 @@ __device__ __forceinline__ ScanTile tile_at(const ScanParams& p, int order, bool
     return p.tab[row];
   }
   // all sequences' first tiles, then all second ones, ...
-  const int per = max(1, (p.dense_T + TT - 1) / TT);
+  const int per = scan_tiles(p.dense_T, TT);
   const int level = order / p.N, seq = order - level * p.N, idx = backward ? per - 1 - level : level;
   row = seq * per + idx;
-  const int saved = max(1, (p.dense_T + SAVED - 1) / SAVED);
+  const int saved = scan_tiles(p.dense_T, SAVED);
   return ScanTile{seq * p.dense_T + idx * TT, min(TT, p.dense_T - idx * TT), seq, idx, per - 1 - idx,
                   seq * saved + idx * (TT / SAVED)};
 }
@@ -823,7 +823,7 @@ __global__ __launch_bounds__(256) void k_scan_prologue(uint32_t* counters, int n
   }
   const int i = blockIdx.x;
   if (i >= b.n) return;
-  const int len = b.len[i], tiles = max(1, (len + TT - 1) / TT);
+  const int len = b.len[i], tiles = scan_tiles(len, TT);
   for (int j = threadIdx.x; j < tiles; j += 256)
     tab[b.tile0[i] + j] = ScanTile{b.t_start[i] + j * TT, min(TT, len - j * TT), b.seq0 + i, j, tiles - 1 - j,
                                    b.saved0[i] + j * (TT / saved)};
