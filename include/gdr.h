@@ -298,7 +298,7 @@ gdr_status gdr_scan_fwd(const gdr_scan_shape* shape, const gdr_scan_inputs* in, 
 
 /* Backward, after gdr_scan_fwd on the same shape, inputs and workspace (which it
  * leaves fit for another gdr_scan_bwd).  dy as y, required unless there are no
- * tokens; dht [N,H,D] fp32 or NULL (zero). */
+ * tokens; dht [N,H,D] fp32 or NULL (zero).  Outputs must not overlap inputs. */
 gdr_status gdr_scan_bwd(const gdr_scan_shape* shape, const gdr_scan_inputs* in, const void* dy, const float* dht,
                         void* ws, size_t ws_bytes, const gdr_scan_grads* grads, void* stream);
 
