@@ -125,3 +125,61 @@ def test_a_decay_below_the_normal_numbers_is_a_reset(kind, dtype):
             # e^-87: lambda's 87 carries U relative, 8 |lambda| U in the exponential
             ref = torch.full(v.shape, float(want), dtype=torch.float64)
             R.check(name, v, ref, (16 + 8 * 87) * R.U * ref.abs())
+
+
+@pytest.mark.parametrize("kind", [0, 1, 2])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("convex", [False, True])
+def test_the_types_lowest_value_masks_as_an_infinity_does(kind, dtype, convex):
+    """A gate of the type's lowest or highest value, as masks are written, shuts or opens it
+    like -inf or inf does: the same bits in every output."""
+    T, H, D = 260, 2, 16
+    t, dy, dht = S.make(21, kind, dtype, [T], H, D)
+    at = (5, 63, 64, 130, T - 1)
+    big = torch.finfo(S.DT[dtype]).max
+    outs = []
+    for v in (big, float("inf")):
+        u = dict(t, g=t["g"].clone())
+        for i, r in enumerate(at):
+            if kind == 0:
+                u["g"][r, i % H] = -v
+            else:
+                u["g"][r, i % H, 2 * i] = -v if i % 2 else v
+        outs.append(S.run(S.problem(kind, dtype, [T], H, D, convex, True), S.dev(u), dy.cuda(), dht.cuda(), kind, 1, H, D))
+    torch.cuda.synchronize()
+    for k in outs[0]:
+        assert torch.isfinite(outs[0][k]).all(), k
+        assert torch.equal(outs[0][k], outs[1][k]), k
+
+
+def test_a_step_with_shut_and_open_gates_of_the_lowest_value():
+    """The same for the single-token steps; a beta logit of the lowest value writes nothing."""
+    B = S.B
+    N, H, D = 4, 2, 64
+    gen = torch.Generator().manual_seed(3)
+    big = torch.finfo(torch.bfloat16).max
+    bf = torch.bfloat16
+    for kind in (0, 1, 2):
+        g, A, bias = R.gate_inputs(gen, kind, N, H, D, bf)
+        t = {"q": R.rand(gen, N, H, D).to(bf), "k": R.rand(gen, N, H, D).to(bf), "v": R.rand(gen, N, H, D).to(bf),
+             "x": R.rand(gen, N, H, D).to(bf), "b": R.rand(gen, N, H).to(bf), "A_log": A, "dt_bias": bias}
+        states, state = R.rand(gen, N, H, D, D).float(), R.rand(gen, N, H, D).float()
+        outs = []
+        for v in (big, float("inf")):
+            u = {k: None if w is None else w.clone().cuda() for k, w in dict(t, g=g).items()}
+            u["g"][1, 0] = -v
+            if kind:
+                u["g"][2, 1, :8] = v
+            u["b"][3, 0] = -v
+            o, y = torch.empty(N, H, D, dtype=bf, device="cuda"), torch.empty(N, H, D, dtype=bf, device="cuda")
+            St, st = states.cuda(), state.cuda()
+            B.gdr_step(B.Problem(N, 1, H, D, N, kind, B.GDR_BF16, 0.125, gate_scale=S.GS if kind == 2 else 0.0), u, St, o)
+            B.gdr_scan_step(B.ScanProblem(N, 1, H, D, N, kind, B.GDR_BF16, gate_scale=S.GS, convex=True), u, st, y)
+            outs.append((o, y, St, st))
+        torch.cuda.synchronize()
+        for a, b in zip(*outs):
+            assert torch.isfinite(a).all() and torch.equal(a, b)
+        # beta = 0: the state only decays, one product
+        lam, _, _, rel = (v.expand(1, H, D)[0, 0] for v in R.gate(kind, g[3:], A, bias, S.GS))
+        want = states[3, 0].double() * lam.exp()
+        R.check("state", outs[0][2][3, 0], want, (rel + 2 * R.U) * want.abs())

@@ -61,3 +61,77 @@ def test_a_batch_equals_the_pack_of_the_same_sequences():
     torch.cuda.synchronize()
     for k in a:
         assert torch.equal(a[k], b[k]), k
+
+
+def test_a_pack_captured_into_a_graph():
+    """The tile table of a pack is written by the captured calls themselves: replays on new
+    inputs, between other calls on the same card, give the eager call's bits."""
+    lengths, H, D, kind = [700, 0, 3, 450], 2, 64, 2
+    prob = S.problem(kind, "bf16", lengths, H, D, True, False)
+    t, dy, dht = S.make(17, kind, "bf16", lengths, H, D)
+    d, dy, dht = S.dev(t), dy.cuda(), dht.cuda()
+    S.run(prob, d, dy, dht, kind, 4, H, D)
+    ws, y = S.B.alloc_scan_workspace(prob), torch.empty_like(d["x"])
+    ht, out = torch.empty(4, H, D, device="cuda"), S.outputs(d, kind, 4, H, D)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        S.B.gdr_scan_fwd(prob, d, ws, y, ht=ht)
+        S.B.gdr_scan_bwd(prob, d, dy, dht, ws, out)
+    for rep in range(4):
+        d["x"].copy_(d["x"].flip(0))
+        d["g"].copy_(d["g"].flip(0))
+        ref = S.run(prob, d, dy, dht, kind, 4, H, D)
+        torch.cuda.synchronize()
+        ws.fill_(rep)
+        graph.replay()
+        torch.cuda.synchronize()
+        for k, v in {"y": y, "ht": ht, **out}.items():
+            assert torch.equal(v, ref[k]), (rep, k)
+
+
+def test_a_step_captured_into_a_graph():
+    """Replays take the slots, inputs and states as they then are."""
+    N, P, H, D = 20, 24, 3, 40
+    t, _, _ = S.make(18, 1, "bf16", [N], H, D, h0=False)
+    d, gen = S.dev(t), torch.Generator().manual_seed(1)
+    prob = S.B.ScanProblem(N, 1, H, D, N, 1, S.B.GDR_BF16, convex=True)
+    state = R.rand(gen, P, H, D).float().cuda()
+    slots = (torch.randperm(P, generator=gen)[:N] - 2).to(torch.int32).cuda()     # two rows of padding at most
+    a, b = state.clone(), state.clone()
+    ya, yb = torch.zeros_like(d["x"]), torch.zeros_like(d["x"])
+    S.B.gdr_scan_step(prob, d, a, ya, slots=slots)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        S.B.gdr_scan_step(prob, d, b, yb, slots=slots)
+    a.copy_(state)
+    ya.zero_()
+    for _ in range(4):
+        slots.copy_(slots.roll(1))
+        d["x"].copy_(d["x"].flip(0))
+        S.B.gdr_scan_step(prob, d, a, ya, slots=slots)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a, b) and torch.equal(ya, yb)
+
+
+def test_a_stream_given_by_hand():
+    """stream=: another stream of the current device, as an object or as a handle."""
+    lengths, H, D, kind = [300, 40], 2, 64, 1
+    prob = S.problem(kind, "bf16", lengths, H, D, False, False)
+    t, dy, dht = S.make(19, kind, "bf16", lengths, H, D)
+    d, dy, dht = S.dev(t), dy.cuda(), dht.cuda()
+    ref = S.run(prob, d, dy, dht, kind, 2, H, D)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream):
+        ws, y = S.B.alloc_scan_workspace(prob), torch.empty_like(d["x"])
+        ht, out = torch.empty(2, H, D, device="cuda"), S.outputs(d, kind, 2, H, D)
+        torch.cuda.synchronize()
+        S.B.gdr_scan_fwd(prob, d, ws, y, ht=ht, stream=stream)
+        S.B.gdr_scan_bwd(prob, d, dy, dht, ws, out, stream=stream)
+        s.synchronize()
+        for k, v in {"y": y, "ht": ht, **out}.items():
+            assert torch.equal(v, ref[k]), k
