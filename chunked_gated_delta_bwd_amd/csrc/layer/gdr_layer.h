@@ -22,11 +22,27 @@ enum ScanGate {
   kScanSigmoid = 3,
 };
 
-// Tokens per tile of the recurrence, backward and forward.  One decay per head
-// needs fewer registers a token, which go into longer tiles, unless the head is so
-// wide (over 128 channels) that a tile holds twice the channels; so does the
-// backward of plain decays per channel (T = 32768, 4096 channels: 278 us with 128
-// tokens, 310 us with 64), but not its convex form, whose registers would spill.
+// Tokens per tile of the recurrence, backward and forward.  A decay per head is one
+// register a token, which leaves room for longer tiles, unless the head is so wide
+// (over 128 channels) that a tile holds twice the channels; plain decays per channel
+// take a longer tile in the backward, but not in its convex form, which would spill 160
+// to 220 registers.  The convex forms are at the 256-register limit: with a decay per
+// head they spill 2 (bf16) or 26 to 30 (fp32, backward), with the sigmoid gate 17 to 39
+// in the backward, and are faster so than in shorter tiles.  Forward, backward in us at
+// T = 32768 (bf16) or 16384 (fp32):
+//   32 heads of 128, decay per head      256, 128 tokens   128, 64
+//     bf16, convex                           130, 205      141, 253
+//     bf16                                   123, 202      138, 247
+//     fp32, convex                           127, 186      126, 189
+//     fp32                                   114, 168      113, 177
+//   4096 channels, backward                 128 tokens        64
+//     bf16                                     278           318
+//     fp32                                     252           258
+//     bf16, convex                             803           352
+//     fp32, convex                             494           260
+//   sigmoid, convex, bf16, backward          64 tokens        32
+//     16 heads of 128                          254           266
+//     2051 channels                            371           359
 constexpr bool scan_long(int gate, bool wide) { return gate == kScanHeadLog && !wide; }
 constexpr int bwd_tile(int gate, bool wide, bool convex) {
   return scan_long(gate, wide) || (gate == kScanLog && !convex) ? 128 : 64;

@@ -10,10 +10,15 @@
 // alignment); only a last partial vector goes element by element.
 //
 // Streaming work, bound by HBM (a large copy on the card measured here moves 4.9
-// TB/s): bf16, 8192 x 2048 with residual 29 us (4.6 TB/s), backward 33 us with dw;
+// TB/s): bf16, 8192 x 2048 with residual 28 us (4.8 TB/s), backward 33 us with dw;
 // 524288 x 128 50 us (5.4 TB/s), backward 78 us (5.2 TB/s); e4m3 of 32768 x 4096 with
-// residual 165 us (5.7 TB/s).  Before narrow rows shared a wave and many threads added
-// dw's partial rows, the 524288 x 128 backward took 223 us.
+// residual 166 us (5.7 TB/s).  Before narrow rows shared a wave and many threads added
+// dw's partial rows, the 524288 x 128 backward took 223 us.  In fp32: 8192 x 2048 with
+// residual 50 us (5.4 TB/s), backward 56 us (4.8); 262144 x 128 49 us (5.5), 76 (5.3).
+// The backward holds r, dy, dres, w and its share of dw in registers: above 16,384
+// channels (1024 threads, 128 registers each) it spills 214 (bf16) or 295 (fp32) of
+// them.  8192 x 16384, bf16: 223 us (4.8 TB/s); 8192 x 32768: 1078 us (2.0 TB/s);
+// 4096 x 32768, fp32: 886 us (2.4).
 #include <hip/hip_runtime.h>
 
 #include "../gdr_device.h"

@@ -13,7 +13,8 @@
 // the inputs once and recomputes the states from the tile's starting state that
 // the forward left in the workspace.
 //
-// Between tiles: every tile publishes its fold (A, S); the last of each group of kGroup
+// Between tiles: a single-pass scan with decoupled look-back (Merrill and Garland, 2016),
+// in two levels.  Every tile publishes its fold (A, S); the last of each group of kGroup
 // composes the group's folds, publishes the whole, looks back over the groups before
 // it to the nearest whose end state is known, and publishes its own group's.  A tile
 // takes that state through the folds of its own group; so the inputs cross HBM once
@@ -31,8 +32,12 @@
 // workgroups a compute unit by registers, and what they wait for each other.  T = 32768,
 // bf16, on a card whose large copy moves 4.9 TB/s:
 //   4096 channels, a decay each:          184 us (4.4 TB/s), backward 278 us (4.8 TB/s)
-//   16 heads of 128, softplus gate:       110 us (3.7 TB/s),          203 us (3.3 TB/s)
-//   32 heads of 128, a decay per head, convex: 129 us (4.2 TB/s),     204 us (4.0 TB/s)
+//   16 heads of 128, softplus gate:       109 us (3.7 TB/s),          203 us (3.3 TB/s)
+//   32 heads of 128, a decay per head, convex: 130 us (4.1 TB/s),     205 us (3.9 TB/s)
+// and in fp32
+//   16 heads of 128, softplus gate:       165 us (4.9 TB/s),          288 us (4.7 TB/s)
+//   32 heads of 128, a decay per head, convex: 232 us (4.6 TB/s),     348 us (4.6 TB/s)
+//   16 heads of 128, sigmoid gate, convex: 186 us (4.3 TB/s),         414 us (3.2 TB/s; spills)
 // Without the look back (wrong results, timing alone) the softplus case took 103 and
 // 167 us, and without its gate functions the forward took 102 us.
 #include <hip/hip_runtime.h>
@@ -86,10 +91,15 @@ __device__ __forceinline__ float decay_product(float p, float least) {
 // one.  Which sums are formed depends on the tiles' places alone, not on how far
 // anybody was, and the states' front advances by up to kGroup groups per trip to
 // memory.
-// Forward and backward at T = 32768: 16 heads of 128, sigmoid gate, convex: 118, 247 us
-// with 6, 119, 286 with 8 (whose words spill registers), 118, 238 with 5; 2 heads,
-// softplus gate: 25, 43 us with 6, 23, 41 with 8, 27, 46 with 5.  Without groups, a tile
-// looking back over eight tiles at a time, the 2 heads took 52, 95 us.
+// The size is a trade between few and many channels: T = 32768, bf16, forward and
+// backward in us (the words are registers: the convex sigmoid backward spills 11, 17
+// and 31 of them):
+//   groups of                                    5         6         8
+//   16 heads of 128, sigmoid gate, convex     120, 246  119, 255  123, 293
+//   16 heads of 128, softplus gate            109, 203  108, 204  109, 205
+//   2 heads of 128, softplus gate              27, 45    25, 42    22, 41
+//   4096 channels, a decay each               184, 278  184, 277  183, 277
+// Without groups, a tile looking back over eight tiles at a time, the 2 heads took 52, 95.
 constexpr int kGroup = 6;
 
 // The state after the nearest of `count` (at least one) groups: w + c is the nearest

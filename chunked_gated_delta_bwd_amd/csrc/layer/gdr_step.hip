@@ -7,8 +7,12 @@
 // those lanes alone, and the state is read and written once.  Each group of eight
 // lanes forms the norms of q and k itself from its share of the channels: no LDS
 // and no barrier but for the search for rows that share a slot.  The state's bytes
-// bound the step: 250 rows of 32 heads, D = 128, move 1 GB in 187 us (5.5 TB/s; a
-// large copy moves 4.9); one row of 16 heads takes 3.5 us in a graph.
+// bound the step: 250 rows of 32 heads, D = 128, move 1 GB in 189 us (5.5 TB/s; a
+// large copy moves 4.9).  Small batches are bound by latencies that follow each other:
+// the state's load is on its way during the search for shared slots, but q, k, the gate
+// and v are asked for only behind its two barriers.  One row of 16 heads takes 3.4 us
+// in a graph; 33 rows of 16 heads, D = 64, fp32, per-channel gate, 5.9, where the bytes
+// would take 3.6.
 #include <hip/hip_runtime.h>
 
 #include "../gdr_device.h"
@@ -120,9 +124,17 @@ __global__ __launch_bounds__(256) void k_step(const StepParams p) {
                         S[i][4 * m + 3]);
 }
 
-// Rows of the state per workgroup: 32 with one decay per head (250 rows of 32 heads,
-// D = 128: 191 us, 5.5 TB/s; 207 us with 64), 64 with per-channel gates, whose
-// functions every eight lanes work out again (197 us; 218 us with 32).
+// Rows of the state per workgroup: 32 with one decay per head, 64 with per-channel
+// gates, whose functions every eight lanes work out again.  In us, in a graph:
+//                                        per head        per channel
+//                                        32      64       32      64
+//   250 rows, 32 heads of 128, bf16     192     207      218     195
+//   250 rows, 32 heads of 64, bf16       50      52       61      54
+//   33 rows, 16 heads of 64, fp32       5.5     5.3      6.7     5.9
+//   8 rows, 16 heads of 128, bf16       5.0     5.1      6.1     5.9
+//   1 row, 16 heads of 128, bf16        3.4     3.8      4.2     4.6
+// A single row with a per-channel gate loses 0.4 us by 64, a small fp32 batch with one
+// decay per head 0.2 by 32: neither is given a rule of its own.
 template <typename TIO, int D, int GM>
 int launch_gate(const StepParams& p, hipStream_t s) {
   constexpr int R = GM == 0 ? 32 : 64;
