@@ -30,7 +30,9 @@ STAGE_NAMES = {GDR_STAGE_PREP: "prep", GDR_STAGE_CHAIN_FWD: "chain_fwd", GDR_STA
 SYMBOLS = ("gdr_workspace_bytes", "gdr_fwd_recompute", "gdr_fwd", "gdr_bwd", "gdr_fwd_bwd",
            "gdr_workspace_region", "gdr_run_stage", "gdr_fwd_bwd_noalloc", "gdr_step",
            "gdr_scan_workspace_bytes", "gdr_scan_fwd", "gdr_scan_bwd", "gdr_scan_step",
-           "gdr_norm_fwd", "gdr_norm_quant", "gdr_norm_workspace_bytes", "gdr_norm_bwd", "gdr_last_error")
+           "gdr_norm_fwd", "gdr_norm_quant", "gdr_norm_workspace_bytes", "gdr_norm_bwd",
+           "gdr_lin_workspace_bytes", "gdr_lin_fwd", "gdr_lin_bwd", "gdr_lin_step", "gdr_quant",
+           "gdr_gemm_workspace_bytes", "gdr_gemm", "gdr_last_error")
 # the device array gdr_fwd_bwd_noalloc uses as its workspace (128 MiB per GPU)
 NOALLOC_WORKSPACE_BYTES = 128 << 20
 
@@ -83,6 +85,31 @@ class NormShape(ctypes.Structure):
                 ("eps", ctypes.c_float), ("group", ctypes.c_int32)]
 
 
+class LinShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("H", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("N", ctypes.c_int32), ("cu_seqlens_host", ctypes.POINTER(ctypes.c_int64)),
+                ("dtype", ctypes.c_int32), ("scale", ctypes.c_float), ("Hk", ctypes.c_int32)]
+
+
+class LinInputs(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("log_decay", ctypes.c_void_p), ("h0", ctypes.c_void_p)]
+
+
+class LinGrads(ctypes.Structure):
+    _fields_ = [("dq", ctypes.c_void_p), ("dk", ctypes.c_void_p), ("dv", ctypes.c_void_p), ("dh0", ctypes.c_void_p)]
+
+
+class QuantShape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("block", ctypes.c_int32), ("transpose", ctypes.c_int32)]
+
+
+class GemmShape(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("block", ctypes.c_int32)]
+
+
 def library_path() -> str:
     return _LIB_PATH
 
@@ -120,6 +147,13 @@ def load_library():
     lib.gdr_norm_quant.argtypes = [P(NormShape), ptr, ptr, ptr, ptr, ptr, ptr, ptr]
     lib.gdr_norm_workspace_bytes.argtypes = [P(NormShape), P(size)]
     lib.gdr_norm_bwd.argtypes = [P(NormShape), ptr, ptr, ptr, ptr, ptr, size, ptr, ptr, ptr]
+    lib.gdr_lin_workspace_bytes.argtypes = [P(LinShape), ctypes.c_int32, P(size)]
+    lib.gdr_lin_fwd.argtypes = [P(LinShape), P(LinInputs), ptr, size, ptr, ptr, ptr]
+    lib.gdr_lin_bwd.argtypes = [P(LinShape), P(LinInputs), ptr, ptr, ptr, size, P(LinGrads), ptr]
+    lib.gdr_lin_step.argtypes = [P(LinShape), P(LinInputs), ptr, ctypes.c_int32, ptr, ptr, ptr]
+    lib.gdr_quant.argtypes = [P(QuantShape), ptr, ptr, ptr, ptr]
+    lib.gdr_gemm_workspace_bytes.argtypes = [P(GemmShape), P(size)]
+    lib.gdr_gemm.argtypes = [P(GemmShape), ptr, ptr, ptr, ptr, ptr, size, ptr, ptr]
     lib.gdr_last_error.argtypes = []
     lib.gdr_last_error.restype = ctypes.c_char_p
     for name in SYMBOLS[:-1]:
@@ -465,6 +499,137 @@ def gdr_norm_bwd(prob: NormProblem, r: torch.Tensor, w: Optional[torch.Tensor], 
                     ("dw", dw, prob.width, torch.float32), ("dres", dres, n, io)))
     _check(load_library().gdr_norm_bwd(prob.ref, _ptr(r), _ptr(w), _ptr(dy), _ptr(dres), _ptr(ws),
                                        _check_workspace(ws, dy), _ptr(dx), _ptr(dw), _stream_here(stream)))
+
+
+class LinProblem:
+    """Host-side description of one linear attention with a decay for each head (gdr_lin_shape)."""
+
+    def __init__(self, B: int, T: int, H: int, D: int, N: int, dtype: int, scale: float, cu_seqlens=None, Hk: int = 0):
+        _check_range(32, B=B, T=T, H=H, D=D, N=N, dtype=dtype, Hk=Hk)
+        self.cu = None
+        if cu_seqlens is not None:
+            self.cu = torch.as_tensor(cu_seqlens, dtype=torch.int64).contiguous().cpu()
+            if self.cu.numel() != N + 1:
+                _bad(f"cu_seqlens has {self.cu.numel()} entries, expected {N + 1}")
+        self.shape = LinShape(B, T, H, D, N,
+                              None if self.cu is None else ctypes.cast(self.cu.data_ptr(),
+                                                                       ctypes.POINTER(ctypes.c_int64)),
+                              dtype, scale, Hk)
+        self.ref = ctypes.byref(self.shape)
+        self.qk_numel, self.v_numel = B * T * (Hk or H) * D, B * T * H * D
+        self.state_numel, self.per_state, self.H = N * H * D * D, H * D * D, H
+        self.rows, self.io = N, _DTYPE.get(dtype)
+
+    def input_specs(self, t: Dict):
+        return (("q", t["q"], self.qk_numel, self.io), ("k", t["k"], self.qk_numel, self.io),
+                ("v", t["v"], self.v_numel, self.io), ("log_decay", t["log_decay"], self.H, torch.float32),
+                ("h0", t.get("h0"), self.state_numel, torch.float32))
+
+
+def _lin_inputs(t: Dict) -> LinInputs:
+    return LinInputs(_ptr(t["q"]), _ptr(t["k"]), _ptr(t["v"]), _ptr(t["log_decay"]), _ptr(t.get("h0")))
+
+
+def gdr_lin_workspace_bytes(prob: LinProblem, backward: bool = False) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load_library().gdr_lin_workspace_bytes(prob.ref, int(backward), ctypes.byref(out)))
+    return out.value
+
+
+def alloc_lin_workspace(prob: LinProblem, device="cuda", backward: bool = False) -> torch.Tensor:
+    """backward: also for the gdr_lin_bwd that follows gdr_lin_fwd."""
+    return torch.empty(max(gdr_lin_workspace_bytes(prob, backward), 256), dtype=torch.uint8, device=device)
+
+
+def gdr_lin_fwd(prob: LinProblem, t: Dict, ws: torch.Tensor, o: torch.Tensor, ht: Optional[torch.Tensor] = None,
+                stream=None) -> None:
+    """t: q k v log_decay, and optionally h0."""
+    _check_tensors(prob.input_specs(t) + (("o", o, prob.v_numel, prob.io), ("ht", ht, prob.state_numel, torch.float32)))
+    n = _check_workspace(ws, o)
+    inp = _lin_inputs(t)
+    _check(load_library().gdr_lin_fwd(prob.ref, ctypes.byref(inp), _ptr(ws), n, _ptr(o), _ptr(ht), _stream_here(stream)))
+
+
+def gdr_lin_bwd(prob: LinProblem, t: Dict, dO: torch.Tensor, dht: Optional[torch.Tensor], ws: torch.Tensor, out: Dict,
+                stream=None) -> None:
+    """out: dq, dk, dv, and optionally dh0."""
+    f32 = torch.float32
+    _check_tensors(prob.input_specs(t) + (
+        ("dO", dO, prob.v_numel, prob.io), ("dht", dht, prob.state_numel, f32), ("dq", out["dq"], prob.qk_numel, prob.io),
+        ("dk", out["dk"], prob.qk_numel, prob.io), ("dv", out["dv"], prob.v_numel, prob.io),
+        ("dh0", out.get("dh0"), prob.state_numel, f32)))
+    n = _check_workspace(ws, dO)
+    inp = _lin_inputs(t)
+    gr = LinGrads(_ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out.get("dh0")))
+    _check(load_library().gdr_lin_bwd(prob.ref, ctypes.byref(inp), _ptr(dO), _ptr(dht), _ptr(ws), n, ctypes.byref(gr),
+                                      _stream_here(stream)))
+
+
+def gdr_lin_step(prob: LinProblem, t: Dict, state: torch.Tensor, o: torch.Tensor,
+                 slots: Optional[torch.Tensor] = None, stream=None) -> None:
+    """prob: LinProblem(N, 1, H, D, N, ...); t: q k v log_decay."""
+    P = _pool_size(state, prob.per_state)
+    _check_tensors(prob.input_specs(t) + (("o", o, prob.v_numel, prob.io), ("state", state, state.numel(), torch.float32),
+                                          ("slots", slots, prob.rows, torch.int32)))
+    inp = _lin_inputs(t)
+    _check(load_library().gdr_lin_step(prob.ref, ctypes.byref(inp), _ptr(state), P, _ptr(slots), _ptr(o),
+                                       _stream_here(stream)))
+
+
+class QuantProblem:
+    """Host-side description of one quantisation to e4m3 (gdr_quant_shape).  q_shape and
+    scales_shape: what gdr_quant writes."""
+
+    def __init__(self, rows: int, cols: int, dtype: int, block: int = 1, transpose: bool = False):
+        _check_range(64, rows=rows, cols=cols)
+        _check_range(32, dtype=dtype, block=block, transpose=transpose)
+        self.shape = QuantShape(rows, cols, dtype, block, int(transpose))
+        self.ref = ctypes.byref(self.shape)
+        self.q_shape = (cols, rows) if transpose else (rows, cols)
+        self.scales_shape = (-(-self.q_shape[0] // max(block, 1)), -(-self.q_shape[1] // 128))
+        self.numel, self.scales_numel = rows * cols, self.scales_shape[0] * self.scales_shape[1]
+        self.io = _DTYPE.get(dtype)
+
+
+def gdr_quant(prob: QuantProblem, x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, stream=None) -> None:
+    _check_tensors((("x", x, prob.numel, prob.io), ("q", q, prob.numel, torch.float8_e4m3fn),
+                    ("scales", scales, prob.scales_numel, torch.float32)))
+    _check(load_library().gdr_quant(prob.ref, _ptr(x), _ptr(q), _ptr(scales), _stream_here(stream)))
+
+
+class GemmProblem:
+    """Host-side description of one e4m3 product c = a b^T (gdr_gemm_shape)."""
+
+    def __init__(self, M: int, N: int, K: int, dtype: int, block: int = 128):
+        _check_range(32, M=M, N=N, K=K, dtype=dtype, block=block)
+        self.shape = GemmShape(M, N, K, dtype, block)
+        self.ref = ctypes.byref(self.shape)
+        self.a_numel, self.b_numel, self.c_numel = M * K, N * K, M * N
+        groups = -(-K // 128)
+        self.sa_numel, self.sb_numel = M * groups, -(-N // max(block, 1)) * groups
+        self.io = _DTYPE.get(dtype)
+
+
+def gdr_gemm_workspace_bytes(prob: GemmProblem) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load_library().gdr_gemm_workspace_bytes(prob.ref, ctypes.byref(out)))
+    return out.value
+
+
+def alloc_gemm_workspace(prob: GemmProblem, device="cuda") -> Optional[torch.Tensor]:
+    """None where the product needs none."""
+    n = gdr_gemm_workspace_bytes(prob)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def gdr_gemm(prob: GemmProblem, a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_scales: torch.Tensor,
+             c: torch.Tensor, ws: Optional[torch.Tensor] = None, stream=None) -> None:
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+    _check_tensors((("a", a, prob.a_numel, f8), ("a_scales", a_scales, prob.sa_numel, f32), ("b", b, prob.b_numel, f8),
+                    ("b_scales", b_scales, prob.sb_numel, f32), ("c", c, prob.c_numel, prob.io)))
+    n = _check_workspace(ws, c)
+    _check(load_library().gdr_gemm(prob.ref, _ptr(a), _ptr(a_scales), _ptr(b), _ptr(b_scales), _ptr(ws), n, _ptr(c),
+                                   _stream_here(stream)))
 
 
 # ---------------------------------------------------------------------------

@@ -10,7 +10,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libgdr.so")
 SOURCES = [os.path.join(PKG, "csrc", n) for n in ("gdr_api.cpp", "gdr_kernels.hip", "gdr_chain.hip", "gdr_kda.hip", "gdr_out.hip", "gdr_group.hip", "gdr_tables.hip", "gdr_noalloc.hip")]
-SOURCES += [os.path.join(PKG, "csrc", "layer", n) for n in ("gdr_layer.cpp", "gdr_scan.hip", "gdr_norm.hip", "gdr_step.hip")]
+SOURCES += [os.path.join(PKG, "csrc", "layer", n) for n in ("gdr_layer.cpp", "gdr_scan.hip", "gdr_norm.hip", "gdr_step.hip", "gdr_lin.cpp", "gdr_lin.hip",
+                                                          "gdr_gemm.cpp", "gdr_gemm.hip", "gdr_quant.hip")]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

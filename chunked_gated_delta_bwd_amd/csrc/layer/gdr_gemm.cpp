@@ -1,0 +1,104 @@
+// Host side of the e4m3 product and of the quantisation that makes its operands (see
+// gdr.h): argument checks, the choice of the tiles and the launch sequences.  Nothing
+// here allocates or synchronises.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "gdr_check.h"
+#include "gdr_gemm.h"
+#include "gdr_layer.h"
+
+namespace {
+
+using namespace gdr::check;
+using gdr::set_error;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+gdr_status check_quant_shape(const gdr_quant_shape* s) {
+  if (!s) return set_error(GDR_EINVAL, "shape is NULL");
+  if (s->dtype != GDR_BF16 && s->dtype != GDR_F32) return set_error(GDR_EINVAL, "unknown dtype %d", s->dtype);
+  if (s->rows < 0 || s->cols < 0) return set_error(GDR_EINVAL, "bad rows/cols");
+  if (s->block != 1 && s->block != gdr::kGroup) return set_error(GDR_EUNSUPPORTED, "block %d not in {1, 128}", s->block);
+  if (s->transpose != 0 && s->transpose != 1) return set_error(GDR_EINVAL, "transpose %d must be 0 or 1", s->transpose);
+  constexpr int64_t most = int64_t(1) << 31;
+  if (s->rows >= most || s->cols >= most ||
+      ceil_div(s->rows, gdr::kGroup) * ceil_div(s->cols, gdr::kGroup) * 256 >= gdr::kMaxThreads)
+    return set_error(GDR_EUNSUPPORTED, "matrix too large for one launch");
+  return GDR_OK;
+}
+
+gdr_status check_gemm_shape(const gdr_gemm_shape* s) {
+  if (!s) return set_error(GDR_EINVAL, "shape is NULL");
+  if (s->dtype != GDR_BF16 && s->dtype != GDR_F32) return set_error(GDR_EINVAL, "unknown dtype %d", s->dtype);
+  if (s->M < 0 || s->N < 0 || s->K < 1) return set_error(GDR_EINVAL, "bad M/N/K");
+  if (s->block != 1 && s->block != gdr::kGroup) return set_error(GDR_EUNSUPPORTED, "block %d not in {1, 128}", s->block);
+  if (s->M > (1 << 30) || s->N > (1 << 30) || s->K > (1 << 30) ||
+      ceil_div(s->M, 128) * ceil_div(s->N, 128) >= (int64_t(1) << 19) || ceil_div(s->N, 16) * 512 >= gdr::kMaxThreads)
+    return set_error(GDR_EUNSUPPORTED, "product too large for one launch");
+  return GDR_OK;
+}
+
+gdr::GemmPlan gemm_plan(const gdr_gemm_shape* s) {
+  const int64_t groups = ceil_div(s->K, gdr::kGroup);
+  if (s->M <= 64) return {0, 1};
+  if (s->dtype == GDR_BF16 && s->K % 16 == 0 && s->K <= (1 << 22) && ceil_div(s->M, 256) * ceil_div(s->N, 256) >= 192) return {2, 1};
+  const int64_t tiles = ceil_div(s->M, 128) * ceil_div(s->N, 128);
+  if (tiles >= 256) return {1, 1};
+  const int64_t splits = std::min<int64_t>({512 / tiles, groups / 4, 16});
+  if (splits < 2) return {1, 1};
+  // no run without a group: the last one may be shorter than the others
+  return {1, int32_t(ceil_div(groups, ceil_div(groups, splits)))};
+}
+
+size_t gemm_ws(const gdr_gemm_shape* s) {
+  const gdr::GemmPlan plan = gemm_plan(s);
+  return plan.splits > 1 ? align256(size_t(plan.splits) * size_t(s->M) * size_t(s->N) * 4) : 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+gdr_status gdr_quant(const gdr_quant_shape* shape, const void* x, void* q, float* scales, void* stream) {
+  gdr_status st = check_quant_shape(shape);
+  if (st != GDR_OK) return st;
+  const bool any = shape->rows > 0 && shape->cols > 0;
+  const Arg a[] = {{x, "x", any}, {q, "q", any}, {scales, "scales", any}};
+  if ((st = check_ptrs(a, 3)) != GDR_OK) return st;
+  gdr::QuantParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.rows = shape->rows; p.cols = shape->cols;
+  p.dtype = shape->dtype; p.block = shape->block; p.transpose = shape->transpose;
+  p.x = x; p.q = q; p.scales = scales;
+  return hip_status(gdr::launch_quant(p, stream), "quantisation kernel");
+}
+
+gdr_status gdr_gemm_workspace_bytes(const gdr_gemm_shape* shape, size_t* bytes) {
+  const gdr_status st = check_gemm_shape(shape);
+  if (st != GDR_OK) return st;
+  if (!bytes) return set_error(GDR_EINVAL, "bytes is NULL");
+  *bytes = gemm_ws(shape);
+  return GDR_OK;
+}
+
+gdr_status gdr_gemm(const gdr_gemm_shape* shape, const void* a, const float* a_scales, const void* b,
+                    const float* b_scales, void* ws, size_t ws_bytes, void* c, void* stream) {
+  gdr_status st = check_gemm_shape(shape);
+  if (st != GDR_OK) return st;
+  const bool any = shape->M > 0 && shape->N > 0;
+  const Arg args[] = {{a, "a", any}, {a_scales, "a_scales", any}, {b, "b", any}, {b_scales, "b_scales", any}, {c, "c", any}};
+  if ((st = check_ptrs(args, 5)) != GDR_OK) return st;
+  if ((st = check_ws(gemm_ws(shape), ws, ws_bytes)) != GDR_OK) return st;
+  gdr::GemmParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.M = shape->M; p.N = shape->N; p.K = shape->K; p.G = int32_t(ceil_div(shape->K, gdr::kGroup));
+  p.dtype = shape->dtype; p.block = shape->block; p.plan = gemm_plan(shape);
+  p.a = static_cast<const uint8_t*>(a); p.b = static_cast<const uint8_t*>(b);
+  p.sa = a_scales; p.sb = b_scales; p.c = c; p.part = static_cast<float*>(ws);
+  return hip_status(gdr::launch_gemm(p, stream), "product kernel");
+}
+
+}  // extern "C"

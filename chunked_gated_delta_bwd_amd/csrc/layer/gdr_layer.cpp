@@ -7,41 +7,13 @@
 #include <cmath>
 #include <cstring>
 
-#include "../gdr_internal.h"
+#include "gdr_check.h"
 #include "gdr_layer.h"
 
 namespace {
 
+using namespace gdr::check;
 using gdr::set_error;
-
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-gdr_status hip_status(int err, const char* what) {
-  if (err == 0) return GDR_OK;
-  return set_error(GDR_EHIP, "%s: %s", what, gdr::hip_error_string(err));
-}
-
-struct Arg {
-  const void* ptr;
-  const char* name;
-  bool required;
-};
-
-gdr_status check_ptrs(const Arg* a, int n) {
-  for (int i = 0; i < n; ++i) {
-    if (!a[i].ptr && a[i].required) return set_error(GDR_EINVAL, "%s is NULL", a[i].name);
-    if (!aligned16(a[i].ptr)) return set_error(GDR_EINVAL, "%s is not 16-byte aligned", a[i].name);
-  }
-  return GDR_OK;
-}
-
-gdr_status check_ws(size_t need, const void* ws, size_t ws_bytes) {
-  if (ws_bytes < need) return set_error(GDR_EWORKSPACE, "workspace %zu bytes, need %zu", ws_bytes, need);
-  if (!ws && need) return set_error(GDR_EINVAL, "workspace is NULL");
-  if (reinterpret_cast<uintptr_t>(ws) & 255u) return set_error(GDR_EINVAL, "workspace is not 256-byte aligned");
-  return GDR_OK;
-}
 
 // ---------------------------------------------------------------------------
 // gated linear recurrence
@@ -176,17 +148,6 @@ gdr_status scan_prologue(const gdr_scan_shape* s, const gdr::ScanParams& p, int 
     if (st != GDR_OK) return st;
     clear = false;
   }
-  return GDR_OK;
-}
-
-// State pool and row slots of the single-token steps.
-gdr_status check_pool(int32_t N, const float* state, int32_t P, const int32_t* slots) {
-  if (P < 0) return set_error(GDR_EINVAL, "P (%d) must be >= 0", P);
-  if (!slots && P < N) return set_error(GDR_EINVAL, "%d rows need as many states without slots (P = %d)", N, P);
-  const Arg a[] = {{state, "state", P > 0}};
-  gdr_status st = check_ptrs(a, 1);
-  if (st != GDR_OK) return st;
-  if (reinterpret_cast<uintptr_t>(slots) & 3u) return set_error(GDR_EINVAL, "slots is not 4-byte aligned");
   return GDR_OK;
 }
 

@@ -1,0 +1,765 @@
+// Linear attention with a decay for each head (gdr_lin_fwd, gdr_lin_bwd, gdr_lin_step).
+//
+//   S_t = c S_{t-1} + v_t k_t^T,  o_t = scale S_t q_t,  c = e^lambda
+// In blocks of 64 tokens, i and j counted within the block, S the state before it:
+//   o_i = scale (sum_{j <= i} c^(i-j) (q_i . k_j) v_j + c^(i+1) S q_i)
+//   S' = c^n S + sum_j c^(n-1-j) v_j k_j^T
+// The gradients have the same form with other tensors in the three places (x, y, z):
+//   o:  (q, k, v)    dq: (dO, v, k) with S^T        forwards
+//   dv: (k, q, dO)   dk: (v, dO, q) with the transposed state's gradient, backwards,
+//   R' = c^n R + scale sum_i c^(i+1) dO_i q_i^T,  R being what the block's last token sees,
+// so one kernel, k_lin_out, computes all four.
+#include <hip/hip_runtime.h>
+
+#include "../gdr_device.h"
+#include "../gdr_lds.h"
+#include "gdr_lin.h"
+
+namespace gdr {
+namespace {
+
+constexpr int kB = kLinBlock;
+
+// ---------------------------------------------------------------------------
+// fragments of a type: 16 bytes of each lane, KS elements of the contraction a step
+// ---------------------------------------------------------------------------
+// Lane l = 16 g + q.  Accumulators hold rows 4 g + r, column q (see gdr_device.h).
+template <typename T> struct Lin;
+
+template <> struct Lin<bf16> {
+  typedef bf16x8 Frag;
+  static constexpr int KS = 32;      // elements of the contraction per step
+  static constexpr int E = 8;        // of them per lane
+  template <int W> static __device__ __forceinline__ int off(int r, int c) { return soff<W, 0>(r, c); }
+  template <int W> static __device__ __forceinline__ Frag rk(const char* t, int r0, int k0) {
+    return frag_rk_s<W, 0>(t, r0, k0);
+  }
+  // the order of the contraction that state() leaves
+  template <int W> static __device__ __forceinline__ Frag rk_state(const char* t, int r0, int k0) {
+    return frag_rk_split_s<W, 0>(t, r0, k0);
+  }
+  template <int W> static __device__ __forceinline__ Frag kc(const char* t, int c0, int k0) {
+    return frag_kc_s<W, 0>(t, c0, k0);
+  }
+  // Columns of a slab: with two tiles of 16, column m of tile u is 8 (m / 4) + 4 u + m % 4
+  // of the slab's 32, so that the accumulators of both hold eight neighbours per lane.
+  template <int VT> static __device__ __forceinline__ int col(int u, int m) {
+    return VT == 2 ? 8 * (m >> 2) + 4 * u + (m & 3) : m;
+  }
+  template <int W, int VT> static __device__ __forceinline__ Frag slab(const char* t, int c0, int u, int k0) {
+    if constexpr (VT == 1) return kc<W>(t, c0, k0);
+    const int l = lane_id(), q = l & 15, g = l >> 4, r = 8 * g + (q >> 2);
+    const int c = c0 + 8 * (q & 3) + 4 * u;
+    return tr_pair(t + soff<W, 0>(k0 + r, c), t + soff<W, 0>(k0 + r + 4, c));
+  }
+  static __device__ __forceinline__ void mul(Frag a, Frag b, f32x4& c) { c = mma(a, b, c); }
+  static __device__ __forceinline__ Frag state(f32x4 a, f32x4 b) {
+    const uint2 lo = pack4_bf16(a[0], a[1], a[2], a[3]), hi = pack4_bf16(b[0], b[1], b[2], b[3]);
+    return __builtin_bit_cast(Frag, u32x4{lo.x, lo.y, hi.x, hi.y});
+  }
+  static __device__ __forceinline__ void store4(char* p, float a, float b, float c, float d) {
+    *reinterpret_cast<uint2*>(p) = pack4_bf16(a, b, c, d);
+  }
+  // nonzero where one of the eight has all exponent bits set
+  static __device__ __forceinline__ uint32_t bad(const u32x4& u) {
+    uint32_t b = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b |= (u[i] & 0x7f807f80u) + 0x00800080u;
+    return b & 0x80008000u;
+  }
+  static __device__ __forceinline__ bool bad1(const char* p) {
+    return (*reinterpret_cast<const uint16_t*>(p) & 0x7f80u) == 0x7f80u;
+  }
+  static __device__ __forceinline__ void clear1(char* p) { *reinterpret_cast<uint16_t*>(p) = 0; }
+};
+
+template <> struct Lin<float> {
+  typedef f32x4 Frag;
+  static constexpr int KS = 16;
+  static constexpr int E = 4;
+  // Piece c / 4 (16 bytes) of row r at piece (c / 4) ^ (r % 16)
+  template <int W> static __device__ __forceinline__ int off(int r, int c) {
+    return r * (4 * W) + (((c >> 2) ^ (r & 15)) << 4) + ((c & 3) << 2);
+  }
+  template <int W> static __device__ __forceinline__ Frag rk(const char* t, int r0, int k0) {
+    const int l = lane_id();
+    return *reinterpret_cast<const Frag*>(t + off<W>(r0 + (l & 15), k0 + 4 * (l >> 4)));
+  }
+  template <int W> static __device__ __forceinline__ Frag rk_state(const char* t, int r0, int k0) {
+    return rk<W>(t, r0, k0);
+  }
+  template <int W> static __device__ __forceinline__ Frag kc(const char* t, int c0, int k0) {
+    const int l = lane_id();
+    Frag f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = *reinterpret_cast<const float*>(t + off<W>(k0 + 4 * (l >> 4) + e, c0 + (l & 15)));
+    return f;
+  }
+  template <int VT> static __device__ __forceinline__ int col(int u, int m) { return 16 * u + m; }
+  template <int W, int VT> static __device__ __forceinline__ Frag slab(const char* t, int c0, int u, int k0) {
+    return kc<W>(t, c0 + 16 * u, k0);
+  }
+  static __device__ __forceinline__ void mul(Frag a, Frag b, f32x4& c) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c = mma_f32(a[e], b[e], c);
+  }
+  static __device__ __forceinline__ Frag state(f32x4 a, f32x4) { return a; }
+  static __device__ __forceinline__ void store4(char* p, float a, float b, float c, float d) {
+    *reinterpret_cast<f32x4*>(p) = f32x4{a, b, c, d};
+  }
+  static __device__ __forceinline__ uint32_t bad(const u32x4& u) {
+    uint32_t b = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b |= (u[i] & 0x7f800000u) + 0x00800000u;
+    return b & 0x80000000u;
+  }
+  static __device__ __forceinline__ bool bad1(const char* p) {
+    return (*reinterpret_cast<const uint32_t*>(p) & 0x7f800000u) == 0x7f800000u;
+  }
+  static __device__ __forceinline__ void clear1(char* p) { *reinterpret_cast<uint32_t*>(p) = 0; }
+};
+
+// ---------------------------------------------------------------------------
+// segments and decays
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ LinSeg seg_at(const LinParams& p, int s) {
+  if (p.dense_T < 0) return p.tab[s];
+  LinSeg r;
+  r.nseg = p.dense_nseg;
+  r.seq = s / r.nseg;
+  r.idx = s % r.nseg;
+  r.t0 = r.seq * p.dense_T + r.idx * p.seg;
+  r.len = min(p.seg, p.dense_T - r.idx * p.seg);
+  return r;
+}
+
+// lambda in base-2 units.  A log decay of -inf counts as -1e30: c^0 is 1 and any other
+// power 0, where -inf would make c^0 a NaN.
+__device__ __forceinline__ float decay2(const LinParams& p, int h) {
+  const float l = p.log_decay[h] * kLog2e;
+  return l < -1e30f ? -1e30f : l;
+}
+// c^n - 1: a state is decayed by S + (c^n - 1) S, so that a slow decay's rounding does
+// not add up over the blocks of a long sequence
+__device__ __forceinline__ float decay_m1(float l2, int n) { return expm1f(float(n) * l2 * 0.6931471805599453f); }
+
+// 16-byte pieces of a block of 64 rows for each of 256 threads
+template <typename T, int D> constexpr int kPieces = kB * D * int(sizeof(T)) / 16 / 256;
+
+template <typename T, int D>
+__device__ __forceinline__ void load_block(const void* base, int64_t row0, int64_t stride, int n,
+                                           u32x4 (&r)[kPieces<T, D>]) {
+  constexpr int PR = D * int(sizeof(T)) / 16;   // pieces a row
+  const T* b = static_cast<const T*>(base) + row0;
+#pragma unroll
+  for (int i = 0; i < kPieces<T, D>; ++i) {
+    const int pc = i * 256 + threadIdx.x, row = pc / PR, c = pc % PR;
+    r[i] = row < n ? *reinterpret_cast<const u32x4*>(b + row * stride + c * (16 / int(sizeof(T)))) : u32x4{0, 0, 0, 0};
+  }
+}
+template <typename T, int D>
+__device__ __forceinline__ void put_block(char* tile, const u32x4 (&r)[kPieces<T, D>]) {
+  constexpr int PR = D * int(sizeof(T)) / 16;
+#pragma unroll
+  for (int i = 0; i < kPieces<T, D>; ++i) {
+    const int pc = i * 256 + threadIdx.x;
+    *reinterpret_cast<u32x4*>(tile + Lin<T>::template off<D>(pc / PR, (pc % PR) * (16 / int(sizeof(T))))) = r[i];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the state of a wave: columns [slab, slab + 16 VT) of S^T, all D rows
+// ---------------------------------------------------------------------------
+template <typename T, int D>
+struct State {
+  static constexpr int VT = D / 64, KT = D / 16, JS = kB / Lin<T>::KS;
+  f32x4 s[KT][VT];
+
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+      for (int u = 0; u < VT; ++u) s[t][u] = zero4();
+  }
+  // memory holds [z channel][y channel], or the transpose
+  __device__ __forceinline__ void load(const float* m, bool transposed, int slab) {
+    const int l = lane_id(), q = l & 15, g = l >> 4;
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+      for (int u = 0; u < VT; ++u) {
+        const int v = slab + Lin<T>::template col<VT>(u, q), k = 16 * t + 4 * g;
+        if (!transposed) {
+          s[t][u] = *reinterpret_cast<const f32x4*>(m + v * D + k);
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) s[t][u][r] = m[(k + r) * D + v];
+        }
+      }
+  }
+  __device__ __forceinline__ void store(float* m, int slab) const {
+    const int l = lane_id(), q = l & 15, g = l >> 4;
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+      for (int u = 0; u < VT; ++u)
+        *reinterpret_cast<f32x4*>(m + (slab + Lin<T>::template col<VT>(u, q)) * D + 16 * t + 4 * g) = s[t][u];
+  }
+  __device__ __forceinline__ void decay(float em1) {
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+      for (int u = 0; u < VT; ++u)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) s[t][u][r] = fmaf(em1, s[t][u][r], s[t][u][r]);
+  }
+  // S^T += y^T (w z): the weighted z in two bf16 parts (16 bits of significand), since the
+  // state is held and returned in fp32
+  __device__ __forceinline__ void add(const char* y, const typename Lin<T>::Frag (&z)[JS][VT],
+                                      const float (&w)[JS][Lin<T>::E]) {
+#pragma unroll
+    for (int js = 0; js < JS; ++js) {
+      typename Lin<T>::Frag hi[VT], lo[VT];
+#pragma unroll
+      for (int u = 0; u < VT; ++u) {
+        if constexpr (sizeof(T) == 2) {
+          const u32x4 raw = __builtin_bit_cast(u32x4, z[js][u]);
+          float x[8];
+          IO<bf16>::unpack8(raw, x);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] *= w[js][e];
+          const uint2 a = pack4_bf16(x[0], x[1], x[2], x[3]), b = pack4_bf16(x[4], x[5], x[6], x[7]);
+          const u32x4 h = {a.x, a.y, b.x, b.y};
+          hi[u] = __builtin_bit_cast(bf16x8, h);
+          float y8[8];
+          IO<bf16>::unpack8(h, y8);
+          const uint2 c = pack4_bf16(x[0] - y8[0], x[1] - y8[1], x[2] - y8[2], x[3] - y8[3]);
+          const uint2 d = pack4_bf16(x[4] - y8[4], x[5] - y8[5], x[6] - y8[6], x[7] - y8[7]);
+          lo[u] = __builtin_bit_cast(bf16x8, u32x4{c.x, c.y, d.x, d.y});
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) hi[u][e] = z[js][u][e] * w[js][e];
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < KT; ++t) {
+        const typename Lin<T>::Frag a = Lin<T>::template kc<D>(y, 16 * t, js * Lin<T>::KS);
+#pragma unroll
+        for (int u = 0; u < VT; ++u) {
+          Lin<T>::mul(a, hi[u], s[t][u]);
+          if constexpr (sizeof(T) == 2) Lin<T>::mul(a, lo[u], s[t][u]);
+        }
+      }
+    }
+  }
+};
+
+// Weights of a block's tokens in the state's update: c^(n-1-j), or c^(j+1) backwards
+template <typename T, bool REV>
+__device__ __forceinline__ void state_weights(float l2, int n, float scale, float (&w)[kB / Lin<T>::KS][Lin<T>::E]) {
+  const int g = lane_id() >> 4;
+#pragma unroll
+  for (int js = 0; js < kB / Lin<T>::KS; ++js)
+#pragma unroll
+    for (int e = 0; e < Lin<T>::E; ++e) {
+      const int j = js * Lin<T>::KS + Lin<T>::E * g + e;
+      w[js][e] = j < n ? scale * fast_exp2(float(REV ? j + 1 : n - 1 - j) * l2) : 0.f;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// tables
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(256) void k_lin_table(const LinParams p, const LinBatch b) {
+  for (int i = blockIdx.x; i < b.n; i += gridDim.x) {
+    const int nseg = max(1, int((uint32_t(b.len[i]) + uint32_t(p.seg) - 1) / uint32_t(p.seg)));
+    for (int s = threadIdx.x; s < nseg; s += 256) {
+      LinSeg r;
+      r.t0 = b.t0[i] + s * p.seg;
+      r.len = min(p.seg, b.len[i] - s * p.seg);
+      r.seq = b.seq0 + i;
+      r.idx = s;
+      r.nseg = nseg;
+      p.tab[b.row0[i] + s] = r;
+    }
+    if (threadIdx.x == 0) {
+      p.row0[b.seq0 + i] = b.row0[i];
+      p.row0[b.seq0 + i + 1] = b.row0[i] + nseg;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// a segment's own contribution to the state after it (before it, backwards)
+// ---------------------------------------------------------------------------
+template <typename T, int D, bool REV>
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_lin_local(const LinParams p) {
+  constexpr int TB = kB * D * int(sizeof(T)), VT = D / 64, JS = kB / Lin<T>::KS;
+  __shared__ __attribute__((aligned(1024))) char ys[TB], zs[TB];
+  int c, h;
+  chunk_head_at(p, int(blockIdx.x), c, h);
+  const LinSeg sg = seg_at(p, c);
+  if (REV ? sg.idx == 0 : sg.idx == sg.nseg - 1) return;   // nothing follows it
+  const int yH = p.Hk, yh = h / p.G;
+  const void *y = REV ? p.q : p.k, *z = REV ? p.dO : p.v;
+  const float l2 = decay2(p, h), wscale = REV ? p.scale : 1.f;
+  const int slab = wave_id() * 16 * VT, nb = (sg.len + kB - 1) / kB;
+  State<T, D> S;
+  S.zero();
+  float w[JS][Lin<T>::E], em1 = 0.f;
+  int wn = -1;
+  u32x4 yr[kPieces<T, D>], zr[kPieces<T, D>];
+  auto load = [&](int i) {
+    const int b = REV ? nb - 1 - i : i, n = min(kB, sg.len - b * kB);
+    const int64_t t = sg.t0 + int64_t(b) * kB;
+    load_block<T, D>(y, (t * yH + yh) * D, int64_t(yH) * D, n, yr);
+    load_block<T, D>(z, (t * p.H + h) * D, int64_t(p.H) * D, n, zr);
+  };
+  load(0);
+  for (int i = 0; i < nb; ++i) {
+    const int b = REV ? nb - 1 - i : i, n = min(kB, sg.len - b * kB);
+    if (n != wn) {
+      state_weights<T, REV>(l2, n, wscale, w);
+      em1 = decay_m1(l2, n);
+      wn = n;
+    }
+    chain_barrier();
+    put_block<T, D>(ys, yr);
+    put_block<T, D>(zs, zr);
+    if (i + 1 < nb) load(i + 1);
+    chain_barrier();
+    typename Lin<T>::Frag zf[JS][VT];
+#pragma unroll
+    for (int js = 0; js < JS; ++js)
+#pragma unroll
+      for (int u = 0; u < VT; ++u) zf[js][u] = Lin<T>::template slab<D, VT>(zs, slab, u, js * Lin<T>::KS);
+    S.decay(em1);
+    S.add(ys, zf, w);
+  }
+  S.store((REV ? p.dst : p.st) + (int64_t(c) * p.H + h) * (D * D), slab);
+}
+
+// In place: from each segment's own contribution to the state that it starts from.
+template <int D, bool REV>
+__global__ __launch_bounds__(256) void k_lin_carry(const LinParams p) {
+  constexpr int PER = D * D / 4 / 256;   // workgroups a state
+  const int part = blockIdx.x % PER, h = blockIdx.x / PER % p.H, n = blockIdx.x / PER / p.H;
+  int row0, nseg, len;
+  if (p.dense_T < 0) {
+    row0 = p.row0[n];
+    nseg = p.row0[n + 1] - row0;
+    const LinSeg last = p.tab[row0 + nseg - 1];
+    len = last.len;
+  } else {
+    nseg = p.dense_nseg;
+    row0 = n * nseg;
+    len = p.dense_T - (nseg - 1) * p.seg;
+  }
+  if (nseg == 1) return;
+  const float l2 = decay2(p, h);
+  const int64_t e = 4 * (part * 256 + int(threadIdx.x)), step = int64_t(p.H) * D * D;
+  const float* init = REV ? p.dht : p.h0;
+  f32x4 cur = zero4();
+  if (init) cur = *reinterpret_cast<const f32x4*>(init + (int64_t(n) * p.H + h) * (D * D) + e);
+  float* st = (REV ? p.dst : p.st) + (int64_t(row0) * p.H + h) * (D * D) + e;
+  const float em1 = decay_m1(l2, p.seg), em1_last = decay_m1(l2, len);
+  constexpr int U = 8;                   // segments whose loads are on their way together
+  for (int i0 = 0; i0 < nseg; i0 += U) {
+    f32x4 x[U];
+#pragma unroll
+    for (int a = 0; a < U; ++a)
+      if (i0 + a < nseg - 1) x[a] = *reinterpret_cast<const f32x4*>(st + (REV ? nseg - 1 - i0 - a : i0 + a) * step);
+#pragma unroll
+    for (int a = 0; a < U; ++a)
+      if (i0 + a < nseg) {
+        *reinterpret_cast<f32x4*>(st + (REV ? nseg - 1 - i0 - a : i0 + a) * step) = cur;
+        if (i0 + a < nseg - 1) {
+          const float d = REV && i0 + a == 0 ? em1_last : em1;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) cur[r] = fmaf(d, cur[r], cur[r]) + x[a][r];
+        }
+      }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// outputs
+// ---------------------------------------------------------------------------
+struct LinRole {
+  const void *x, *y, *z;
+  void* out;
+  float* last;            // state after the last segment (before the first, backwards), or NULL
+  const float* first;     // state of the whole sequence's start (end, backwards), or NULL
+  const float* st;        // states of the segments
+  int32_t xk, yk, zk;     // 1: the tensor has Hk heads, 0: H
+  int32_t transposed;     // the state's memory is [y channel][z channel]
+  int32_t out_f32;        // out is the fp32 partial sum per value head
+  float pair, inter, add; // factors of the pairs' product, of S x, of the state's update
+};
+
+template <typename T, int D, bool REV>
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_lin_out(const LinParams p, const LinRole o) {
+  typedef typename Lin<T>::Frag Frag;
+  constexpr int TB = kB * D * int(sizeof(T)), VT = D / 64, KS = Lin<T>::KS, JS = kB / KS, E = Lin<T>::E;
+  __shared__ __attribute__((aligned(1024))) char xs[TB], ys[TB], zs[TB], ps[kB * kB * int(sizeof(T))];
+  __shared__ int bad_s[D], flag_s;
+  int c, h;
+  chunk_head_at(p, int(blockIdx.x), c, h);
+  const LinSeg sg = seg_at(p, c);
+  const int l = lane_id(), q = l & 15, g = l >> 4, w = wave_id();
+  const int slab = w * 16 * VT, nb = (sg.len + kB - 1) / kB;
+  const float l2 = decay2(p, h);
+  const int xH = o.xk ? p.Hk : p.H, yH = o.yk ? p.Hk : p.H, zH = o.zk ? p.Hk : p.H;
+  const int xh = o.xk ? h / p.G : h, yh = o.yk ? h / p.G : h, zh = o.zk ? h / p.G : h;
+  const int64_t sh = int64_t(sg.seq) * p.H + h;
+  u32x4 xr[kPieces<T, D>], yr[kPieces<T, D>], zr[kPieces<T, D>];
+  auto load = [&](int i) {
+    const int b = REV ? nb - 1 - i : i, n = min(kB, sg.len - b * kB);
+    const int64_t t = sg.t0 + int64_t(b) * kB;
+    load_block<T, D>(o.x, (t * xH + xh) * D, int64_t(xH) * D, n, xr);
+    load_block<T, D>(o.y, (t * yH + yh) * D, int64_t(yH) * D, n, yr);
+    load_block<T, D>(o.z, (t * zH + zh) * D, int64_t(zH) * D, n, zr);
+  };
+  if (nb) load(0);
+  State<T, D> S;
+  const bool start = REV ? sg.idx == sg.nseg - 1 : sg.idx == 0;
+  if (!start) S.load(o.st + (int64_t(c) * p.H + h) * (D * D), o.transposed, slab);
+  else if (o.first) S.load(o.first + sh * (D * D), o.transposed, slab);
+  else S.zero();
+  // decay between the wave's 16 tokens i and the block's j
+  float near[4][4];
+#pragma unroll
+  for (int jt = 0; jt < 4; ++jt)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int d = (16 * w + q) - (16 * jt + 4 * g + r), n = REV ? -d : d;
+      near[jt][r] = n >= 0 ? o.pair * fast_exp2(float(n) * l2) : 0.f;
+    }
+  // the pairs of later tokens are never written again
+  for (int i = threadIdx.x; i < kB * kB * int(sizeof(T)) / 16; i += 256) *reinterpret_cast<u32x4*>(ps + 16 * i) = u32x4{0, 0, 0, 0};
+  if (threadIdx.x == 0) flag_s = 0;
+  float wz[JS][E], far[4], em1 = 0.f;
+  int wn = -1;
+  for (int i = 0; i < nb; ++i) {
+    const int b = REV ? nb - 1 - i : i, n = min(kB, sg.len - b * kB);
+    const int64_t t0 = sg.t0 + int64_t(b) * kB;
+    if (n != wn) {
+      state_weights<T, REV>(l2, n, o.add, wz);
+      em1 = decay_m1(l2, n);
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        const int m = REV ? n - 1 - (16 * it + q) : 16 * it + q + 1;
+        far[it] = m >= 0 ? o.inter * fast_exp2(float(m) * l2) : 0.f;
+      }
+      wn = n;
+    }
+    chain_barrier();
+    put_block<T, D>(xs, xr);
+    put_block<T, D>(ys, yr);
+    put_block<T, D>(zs, zr);
+    uint32_t bad = 0;
+#pragma unroll
+    for (int a = 0; a < kPieces<T, D>; ++a) bad |= Lin<T>::bad(zr[a]);
+    if (bad) flag_s = 1;
+    if (i + 1 < nb) load(i + 1);
+    chain_barrier();
+    // pairs: P[i][j] = c^|i-j| (x_i . y_j), the wave's 16 tokens i against the block's j
+    {
+      Frag xf[D / KS];
+#pragma unroll
+      for (int ks = 0; ks < D / KS; ++ks) xf[ks] = Lin<T>::template rk<D>(xs, 16 * w, ks * KS);
+#pragma unroll
+      for (int jt = 0; jt < 4; ++jt) {
+        if (REV ? jt < w : jt > w) continue;
+        f32x4 a = zero4();
+#pragma unroll
+        for (int ks = 0; ks < D / KS; ++ks) Lin<T>::mul(Lin<T>::template rk<D>(ys, 16 * jt, ks * KS), xf[ks], a);
+        // a later token's product counts nothing, whatever it is
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int d = (16 * w + q) - (16 * jt + 4 * g + r);
+          a[r] = (REV ? d <= 0 : d >= 0) ? a[r] * near[jt][r] : 0.f;
+        }
+        Lin<T>::store4(ps + Lin<T>::template off<kB>(16 * w + q, 16 * jt + 4 * g), a[0], a[1], a[2], a[3]);
+      }
+    }
+    chain_barrier();
+    const bool odd = flag_s;
+    if (odd) {
+      // Infinities and NaN in z: a zero pair times one would reach tokens before it, so the
+      // products take zeros in their place, and what comes from that token on is NaN.
+      if (threadIdx.x < D) {
+        int first = kB;
+        for (int a = kB - 1; a >= 0; --a) {
+          char* e = zs + Lin<T>::template off<D>(REV ? kB - 1 - a : a, threadIdx.x);
+          if (Lin<T>::bad1(e)) {
+            first = a;
+            Lin<T>::clear1(e);
+          }
+        }
+        bad_s[threadIdx.x] = first;
+      }
+      chain_barrier();
+      if (threadIdx.x == 0) flag_s = 0;
+    }
+    f32x4 acc[VT][4];
+#pragma unroll
+    for (int u = 0; u < VT; ++u)
+#pragma unroll
+      for (int it = 0; it < 4; ++it) acc[u][it] = zero4();
+#pragma unroll
+    for (int ks = 0; ks < D / KS; ++ks) {
+      Frag a[VT];
+#pragma unroll
+      for (int u = 0; u < VT; ++u) a[u] = Lin<T>::state(S.s[ks * KS / 16][u], S.s[ks * KS / 16 + (KS == 32)][u]);
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        const Frag f = Lin<T>::template rk_state<D>(xs, 16 * it, ks * KS);
+#pragma unroll
+        for (int u = 0; u < VT; ++u) Lin<T>::mul(a[u], f, acc[u][it]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < VT; ++u)
+#pragma unroll
+      for (int it = 0; it < 4; ++it)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[u][it][r] *= far[it];
+    Frag zf[JS][VT];
+#pragma unroll
+    for (int js = 0; js < JS; ++js) {
+#pragma unroll
+      for (int u = 0; u < VT; ++u) zf[js][u] = Lin<T>::template slab<D, VT>(zs, slab, u, js * KS);
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        if (REV ? (js + 1) * KS <= 16 * it : js * KS >= 16 * (it + 1)) continue;
+        const Frag f = Lin<T>::template rk<kB>(ps, 16 * it, js * KS);
+#pragma unroll
+        for (int u = 0; u < VT; ++u) Lin<T>::mul(zf[js][u], f, acc[u][it]);
+      }
+    }
+    if (odd) {
+#pragma unroll
+      for (int u = 0; u < VT; ++u)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int first = bad_s[slab + Lin<T>::template col<VT>(u, 4 * g + r)];
+#pragma unroll
+          for (int it = 0; it < 4; ++it)
+            if ((REV ? kB - 1 - (16 * it + q) : 16 * it + q) >= first) acc[u][it][r] = __builtin_nanf("");
+        }
+    }
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      const int tok = 16 * it + q;
+      if (tok >= n) continue;
+      if (o.out_f32) {
+        float* d = static_cast<float*>(o.out) + ((t0 + tok) * p.H + h) * D + slab;
+#pragma unroll
+        for (int u = 0; u < VT; ++u) *reinterpret_cast<f32x4*>(d + Lin<T>::template col<VT>(u, 4 * g)) = acc[u][it];
+      } else {
+        // outputs per value head, or per key head where each has one value head
+        T* d = static_cast<T*>(o.out) + ((t0 + tok) * p.H + h) * D + slab;
+        if constexpr (VT == 2 && sizeof(T) == 2) {
+          const Frag f = Lin<T>::state(acc[0][it], acc[1][it]);
+          *reinterpret_cast<Frag*>(d + 8 * g) = f;
+        } else {
+#pragma unroll
+          for (int u = 0; u < VT; ++u)
+            Lin<T>::store4(reinterpret_cast<char*>(d + Lin<T>::template col<VT>(u, 4 * g)), acc[u][it][0], acc[u][it][1],
+                           acc[u][it][2], acc[u][it][3]);
+        }
+      }
+    }
+    S.decay(em1);
+    S.add(ys, zf, wz);
+    if (odd) {
+#pragma unroll
+      for (int u = 0; u < VT; ++u)
+        if (bad_s[slab + Lin<T>::template col<VT>(u, q)] < kB) {
+#pragma unroll
+          for (int t = 0; t < D / 16; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) S.s[t][u][r] = __builtin_nanf("");
+        }
+    }
+  }
+  if (o.last && (REV ? sg.idx == 0 : sg.idx == sg.nseg - 1)) S.store(o.last + sh * (D * D), slab);
+}
+
+// Sum of the G value heads' shares of a key head's gradient, in head order
+template <typename T>
+__global__ __launch_bounds__(256) void k_lin_group(const float* __restrict__ src, void* __restrict__ dst, int64_t n8,
+                                                   int Hk, int D, int G) {
+  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= n8) return;
+  const int64_t e = i * 8, row = e / D;
+  const int c = int(e - row * D);
+  float acc[8], x[8];
+  IO<float>::load8(src, row * G * D + c, acc);
+  for (int m = 1; m < G; ++m) {
+    IO<float>::load8(src, (row * G + m) * D + c, x);
+#pragma unroll
+    for (int a = 0; a < 8; ++a) acc[a] += x[a];
+  }
+  IO<T>::store8(dst, e, acc);
+}
+
+// ---------------------------------------------------------------------------
+// single token
+// ---------------------------------------------------------------------------
+// Lane j of a row's eight holds channels 32 m + 4 j .. + 3 (see gdr_step.hip)
+template <typename TIO, int D>
+__device__ __forceinline__ void load_row(const void* base, int64_t off, int j, float (&x)[D / 8]) {
+#pragma unroll
+  for (int m = 0; m < D / 32; ++m) {
+    float y[4];
+    IO<TIO>::load4(base, off + 32 * m + 4 * j, y);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[4 * m + e] = y[e];
+  }
+}
+
+// One row of the state for every eight lanes, 32 rows a workgroup
+template <typename T, int D>
+__global__ __launch_bounds__(256) void k_lin_step(const LinStepParams p) {
+  constexpr int E = D / 8, SPLIT = D / 32;
+  const int64_t id = blockIdx.x;
+  const int part = int(id % SPLIT);
+  const int h = int(id / SPLIT % p.H);
+  int n = int(id / SPLIT / p.H);
+  const int slot = p.slots ? p.slots[n] : n;
+  if (slot < 0 || slot >= p.P) return;
+  const int j = threadIdx.x & 7, row = part * 32 + (threadIdx.x >> 3);
+  float* st = p.state + (int64_t(slot) * p.H + h) * (D * D) + row * D;
+  float S[E], q[E], k[E];
+  load_row<float, D>(st, 0, j, S);
+  load_row<T, D>(p.q, (int64_t(n) * p.Hk + h / p.G) * D, j, q);
+  load_row<T, D>(p.k, (int64_t(n) * p.Hk + h / p.G) * D, j, k);
+  float v = IO<T>::load1(p.v, (int64_t(n) * p.H + h) * D + row);
+  const float a = expf(p.log_decay[h]);
+  // the slot is another row's if an earlier one names it, and takes the later ones that do along
+  bool later = false;
+  if (p.slots) {
+    bool earlier = false;
+    for (int m = threadIdx.x; m < p.N; m += 256)
+      if (p.slots[m] == slot) {
+        earlier |= m < n;
+        later |= m > n;
+      }
+    if (__syncthreads_or(earlier)) return;
+    later = __syncthreads_or(later);
+  }
+  for (;;) {
+    float o = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      S[e] = fmaf(v, k[e], a * S[e]);
+      o = fmaf(S[e], q[e], o);
+    }
+    o = group_sum_dpp<8>(o);
+    if (j == 0) IO<T>::store1(p.o, (int64_t(n) * p.H + h) * D + row, p.scale * o);
+    if (!later) break;
+    do ++n; while (n < p.N && p.slots[n] != slot);
+    if (n >= p.N) break;
+    load_row<T, D>(p.q, (int64_t(n) * p.Hk + h / p.G) * D, j, q);
+    load_row<T, D>(p.k, (int64_t(n) * p.Hk + h / p.G) * D, j, k);
+    v = IO<T>::load1(p.v, (int64_t(n) * p.H + h) * D + row);
+  }
+#pragma unroll
+  for (int m = 0; m < D / 32; ++m) IO<float>::store4(st, 32 * m + 4 * j, S[4 * m], S[4 * m + 1], S[4 * m + 2], S[4 * m + 3]);
+}
+
+// ---------------------------------------------------------------------------
+// launches
+// ---------------------------------------------------------------------------
+int last_error() { return static_cast<int>(hipGetLastError()); }
+
+template <typename T, int D>
+int states(const LinParams& p, bool backward, hipStream_t s) {
+  if (!p.split) return 0;
+  const unsigned grid = unsigned(int64_t(p.NC) * p.H);
+  if (backward) k_lin_local<T, D, true><<<grid, 256, 0, s>>>(p);
+  else k_lin_local<T, D, false><<<grid, 256, 0, s>>>(p);
+  if (const int e = last_error()) return e;
+  const unsigned carry = unsigned(int64_t(p.N) * p.H * (D * D / 1024));
+  if (backward) k_lin_carry<D, true><<<carry, 256, 0, s>>>(p);
+  else k_lin_carry<D, false><<<carry, 256, 0, s>>>(p);
+  return last_error();
+}
+
+template <typename T, int D>
+int fwd(const LinParams& p, hipStream_t s) {
+  const LinRole o = {p.q, p.k, p.v, p.o, p.ht, p.h0, p.st, 1, 1, 0, 0, 0, p.scale, p.scale, 1.f};
+  k_lin_out<T, D, false><<<unsigned(int64_t(p.NC) * p.H), 256, 0, s>>>(p, o);
+  return last_error();
+}
+
+template <typename T, int D>
+int bwd(const LinParams& p, hipStream_t s) {
+  const unsigned grid = unsigned(int64_t(p.NC) * p.H);
+  const bool grouped = p.G > 1;
+  const LinRole q = {p.dO, p.v, p.k, grouped ? p.part : p.dq, nullptr, p.h0, p.st, 0, 0, 1, 1, grouped, p.scale, p.scale, 1.f};
+  const LinRole k = {p.v, p.dO, p.q, grouped ? p.part : p.dk, nullptr, p.dht, p.dst, 0, 0, 1, 1, grouped, p.scale, 1.f, p.scale};
+  const LinRole v = {p.k, p.q, p.dO, p.dv, p.dh0, p.dht, p.dst, 1, 1, 0, 0, 0, p.scale, 1.f, p.scale};
+  const int64_t n8 = int64_t(p.T) * p.Hk * D / 8;
+  const unsigned sum = unsigned((n8 + 255) / 256);
+  k_lin_out<T, D, false><<<grid, 256, 0, s>>>(p, q);
+  if (const int e = last_error()) return e;
+  if (grouped && n8) {
+    k_lin_group<T><<<sum, 256, 0, s>>>(p.part, p.dq, n8, p.Hk, D, p.G);
+    if (const int e = last_error()) return e;
+  }
+  k_lin_out<T, D, true><<<grid, 256, 0, s>>>(p, k);
+  if (const int e = last_error()) return e;
+  if (grouped && n8) {
+    k_lin_group<T><<<sum, 256, 0, s>>>(p.part, p.dk, n8, p.Hk, D, p.G);
+    if (const int e = last_error()) return e;
+  }
+  k_lin_out<T, D, true><<<grid, 256, 0, s>>>(p, v);
+  return last_error();
+}
+
+template <typename T, int D>
+int step(const LinStepParams& p, hipStream_t s) {
+  k_lin_step<T, D><<<unsigned(int64_t(p.N) * p.H * (D / 32)), 256, 0, s>>>(p);
+  return last_error();
+}
+
+#define GDR_LIN_DISPATCH(fn, ...)                                                              \
+  (p.dtype == GDR_BF16 ? (p.D == 128 ? fn<bf16, 128>(__VA_ARGS__) : fn<bf16, 64>(__VA_ARGS__)) \
+                       : (p.D == 128 ? fn<float, 128>(__VA_ARGS__) : fn<float, 64>(__VA_ARGS__)))
+
+}  // namespace
+
+int launch_lin_table(const LinParams& p, const LinBatch& b, void* stream) {
+  (void)hipGetLastError();
+  k_lin_table<<<unsigned(b.n), 256, 0, reinterpret_cast<hipStream_t>(stream)>>>(p, b);
+  return last_error();
+}
+
+int launch_lin_states(const LinParams& p, bool backward, void* stream) {
+  (void)hipGetLastError();
+  if (p.NC == 0) return 0;
+  return GDR_LIN_DISPATCH(states, p, backward, reinterpret_cast<hipStream_t>(stream));
+}
+
+int launch_lin_fwd(const LinParams& p, void* stream) {
+  (void)hipGetLastError();
+  if (p.NC == 0) return 0;
+  return GDR_LIN_DISPATCH(fwd, p, reinterpret_cast<hipStream_t>(stream));
+}
+
+int launch_lin_bwd(const LinParams& p, void* stream) {
+  (void)hipGetLastError();
+  if (p.NC == 0) return 0;
+  return GDR_LIN_DISPATCH(bwd, p, reinterpret_cast<hipStream_t>(stream));
+}
+
+int launch_lin_step(const LinStepParams& p, void* stream) {
+  (void)hipGetLastError();
+  if (p.N == 0) return 0;
+  return GDR_LIN_DISPATCH(step, p, reinterpret_cast<hipStream_t>(stream));
+}
+
+}  // namespace gdr

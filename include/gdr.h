@@ -353,6 +353,116 @@ gdr_status gdr_norm_workspace_bytes(const gdr_norm_shape* shape, size_t* bytes);
 gdr_status gdr_norm_bwd(const gdr_norm_shape* shape, const void* r, const float* w, const void* dy, const void* dres,
                         void* ws, size_t ws_bytes, void* dx, float* dw, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Linear attention with a decay for each head: the delta rule's family without
+ * its correction term, and with a decay that is a constant of the head.  Per
+ * sequence and head:
+ *   S_t = e^lambda S_{t-1} + v_t k_t^T,  o_t = scale S_t q_t,  S_0 = h0 (or 0).
+ * The backward returns the gradients of L = sum_t <dO_t, o_t> + <dht, S_T> with
+ * respect to q, k, v and h0 (the decay is a constant).  q and k are taken as they
+ * are, without the delta rule's normalisation.
+ * B, T, H, N, cu_seqlens_host, dtype, scale, Hk, the tensors' layouts and the
+ * states [N,H,D,D] (row v, column k) as in gdr_shape; D is 64 or 128.  log_decay:
+ * [H] fp32 on the device, meant to be <= 0; -inf keeps nothing of the state.  A
+ * positive one is taken as it stands as long as e^(lambda n) stays in the fp32
+ * range for every n up to the longest sequence.
+ * States, products and sums are fp32; with bf16 tensors the products of pairs of
+ * tokens and the states are rounded to bf16 once where they are multiplied with
+ * bf16 tensors.  An infinity or NaN at a token reaches no token before it (after
+ * it, in the gradients of k and v) and no other sequence; from there on, what the
+ * formulas make infinite or NaN is infinite or NaN, not always the same of the two.
+ * GDR_EUNSUPPORTED from 2^30 tokens B T or 2^16 heads on, and from 2^20 blocks of 64
+ * tokens times heads on (counting B T / 64 + N blocks). */
+typedef struct {
+  int32_t B, T, H, D;               /* dense: [B,T,H,D]; varlen: B == 1, T == total tokens */
+  int32_t N;                        /* sequences, as in gdr_shape */
+  const int64_t* cu_seqlens_host;   /* as in gdr_shape (read during the call only) */
+  int32_t dtype;                    /* gdr_dtype of q, k, v, o, dO, dq, dk, dv */
+  float scale;                      /* readout scale, finite */
+  int32_t Hk;                       /* heads of q and k, as in gdr_shape; 0 means H */
+} gdr_lin_shape;
+
+typedef struct {                    /* device pointers; q, k, v may be NULL when B * T == 0 */
+  const void *q, *k;                /* [B,T,Hk,D] dtype */
+  const void *v;                    /* [B,T,H,D] dtype */
+  const float *log_decay;           /* [H] */
+  const float *h0;                  /* [N,H,D,D] or NULL (zero initial state) */
+} gdr_lin_inputs;
+
+typedef struct {                    /* device pointers, all overwritten; dq, dk, dv may be NULL when B * T == 0 */
+  void *dq, *dk, *dv;               /* as q, k, v */
+  float *dh0;                       /* [N,H,D,D] or NULL (not returned) */
+} gdr_lin_grads;
+
+/* Workspace of gdr_lin_fwd alone (backward 0), or of a gdr_lin_fwd that a
+ * gdr_lin_bwd follows (backward 1; with Hk < H it includes dq or dk per value head
+ * in fp32). */
+gdr_status gdr_lin_workspace_bytes(const gdr_lin_shape* shape, int32_t backward, size_t* bytes);
+
+/* Forward: o (required unless there are no tokens) and optionally the final states
+ * ht [N,H,D,D] fp32 (a sequence without tokens returns its h0).  `ws` needs
+ * gdr_lin_workspace_bytes(), 256-byte aligned, with any content; afterwards it
+ * holds the states that gdr_lin_bwd on the same shape and inputs starts from.
+ * Calls that overlap in time need a workspace each.  Outputs must not overlap
+ * inputs.  Errors as gdr_fwd_recompute. */
+gdr_status gdr_lin_fwd(const gdr_lin_shape* shape, const gdr_lin_inputs* in, void* ws, size_t ws_bytes, void* o,
+                       float* ht, void* stream);
+
+/* Backward, after gdr_lin_fwd on the same shape, inputs and workspace (which it
+ * leaves fit for another gdr_lin_bwd).  dO as o, required unless there are no
+ * tokens; dht [N,H,D,D] fp32 or NULL (zero).  Outputs must not overlap inputs. */
+gdr_status gdr_lin_bwd(const gdr_lin_shape* shape, const gdr_lin_inputs* in, const void* dO, const float* dht,
+                       void* ws, size_t ws_bytes, const gdr_lin_grads* grads, void* stream);
+
+/* One token for each of N rows on a pool of states [P,H,D,D] fp32, updated in
+ * place: shape dense with T == 1, in->h0 NULL; state, P, slots, padding rows and
+ * rows that share a slot as in gdr_step.  o: [N,1,H,D] dtype. */
+gdr_status gdr_lin_step(const gdr_lin_shape* shape, const gdr_lin_inputs* in, float* state, int32_t P,
+                        const int32_t* slots, void* o, void* stream);
+
+/* ------------------------------------------------------------------------
+ * 8-bit projections: the product of e4m3 matrices with a scale for each 128
+ * elements of the contraction, and the quantisation that makes such matrices
+ * (gdr_norm_quant with group 128 makes them too).
+ *
+ * gdr_quant: y = x, or x^T with `transpose`, as bytes and scales.  y has R rows and
+ * C columns ([rows,cols], or [cols,rows] transposed); a scale belongs to `block`
+ * rows (1 or 128) and 128 columns of y, fewer at its end:
+ *   scale = max(max|y| / 448, 2^-126),  q = e4m3(y / scale)
+ * as in gdr_norm_quant, NaN and infinities included.  x: [rows,cols] dtype; q: [R,C]
+ * bytes; scales: [ceil(R / block),ceil(C / 128)] fp32.  q and scales must not
+ * overlap x.  GDR_EUNSUPPORTED from 2^31 rows or columns or 2^24 tiles of 128 x 128 on. */
+typedef struct {
+  int64_t rows, cols;               /* of x */
+  int32_t dtype;                    /* gdr_dtype of x */
+  int32_t block;                    /* rows of y per scale: 1 or 128 */
+  int32_t transpose;                /* 0 or 1 */
+} gdr_quant_shape;
+
+gdr_status gdr_quant(const gdr_quant_shape* shape, const void* x, void* q, float* scales, void* stream);
+
+/* c[m][n] = sum over groups g of 128 elements k of the contraction (the last may be
+ * shorter) of a_scales[m][g] b_scales[n / block][g] sum_{k in g} a[m][k] b[n][k].
+ * a: [M,K] e4m3 bytes with a_scales [M,G], G = ceil(K / 128); b: [N,K] bytes with
+ * b_scales [ceil(N / block),G], block 1 or 128; c: [M,N] dtype.  Products within a
+ * group are exact, sums fp32, c is rounded once.  A linear layer y = x w^T takes a = x
+ * and b = w (block 128); its backward takes the same product with a = dy and
+ * b = w^T, and with a = dy^T and b = x^T (block 1), each quantised along the
+ * contraction.  K >= 1; M and N may be zero.  ws: gdr_gemm_workspace_bytes() (zero
+ * for most shapes; then ws may be NULL), 256-byte aligned, any content; calls that
+ * overlap in time need one each.  c must not overlap the inputs.  Sums run in an
+ * order that depends on the shape alone.  GDR_EUNSUPPORTED above 2^30 rows or columns
+ * of a matrix, from 2^19 tiles of 128 x 128 of c on and from N = 2^27 on. */
+typedef struct {
+  int32_t M, N, K;
+  int32_t dtype;                    /* gdr_dtype of c */
+  int32_t block;                    /* rows of b per scale: 1 or 128 */
+} gdr_gemm_shape;
+
+gdr_status gdr_gemm_workspace_bytes(const gdr_gemm_shape* shape, size_t* bytes);
+gdr_status gdr_gemm(const gdr_gemm_shape* shape, const void* a, const float* a_scales, const void* b,
+                    const float* b_scales, void* ws, size_t ws_bytes, void* c, void* stream);
+
 /* Thread-local text for the last non-OK status returned to this thread. */
 const char* gdr_last_error(void);
 
