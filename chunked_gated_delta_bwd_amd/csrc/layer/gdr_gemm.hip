@@ -100,11 +100,14 @@ __device__ __forceinline__ void put(void* c, int64_t at, int n, const float (&x)
 // ---------------------------------------------------------------------------
 // tiles
 // ---------------------------------------------------------------------------
-// LDS rows of 128 bytes; piece p (16 bytes) of row r at piece p ^ (r mod 8)
+// LDS rows of 128 bytes; piece p (16 bytes) of row r at piece p ^ (r / 2 mod 8): the 16
+// lanes that a 16-byte read serves together lie in rows of which no two of one parity
+// (one half of the banks) share r / 2 mod 8
+__device__ __forceinline__ int place(int r, int p) { return r * 128 + ((p ^ ((r >> 1) & 7)) << 4); }
 __device__ __forceinline__ i32x8 frag(const char* t, int r, int kk) {
   const int p = 4 * kk + 2 * (lane_id() >> 5);
-  const u32x4 lo = *reinterpret_cast<const u32x4*>(t + r * 128 + ((p ^ (r & 7)) << 4));
-  const u32x4 hi = *reinterpret_cast<const u32x4*>(t + r * 128 + (((p + 1) ^ (r & 7)) << 4));
+  const u32x4 lo = *reinterpret_cast<const u32x4*>(t + place(r, p));
+  const u32x4 hi = *reinterpret_cast<const u32x4*>(t + place(r, p + 1));
   return __builtin_bit_cast(i32x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
@@ -142,33 +145,40 @@ __global__ __launch_bounds__(64 * WM * WN) void k_gemm(const GemmParams p) {
   const uint8_t *ga = p.a + int64_t(m0) * p.K, *gb = p.b + int64_t(n0) * p.K;
   typedef typename Off<DMA>::T off_t;
   off_t pa[LA], pb[LB];
-  const int piece = (l & 7) ^ (l >> 3);
+  // load i of the wave fills rows 8 i .. + 7 of its part; lane l its piece l mod 8 of row l / 8
+  static_assert(LA % 2 == 0 && LB % 2 == 0, "rows of load i: i mod 2 decides their places");
+  const int piece = (l & 7) ^ (l >> 4);   // for even i; ^ 4 for odd i
 #pragma unroll
   for (int i = 0; i < LA; ++i) pa[i] = off_t(min((w * LA + i) * 8 + (l >> 3), p.M - 1 - m0)) * off_t(p.K);
 #pragma unroll
   for (int i = 0; i < LB; ++i) pb[i] = off_t(min((w * LB + i) * 8 + (l >> 3), p.N - 1 - n0)) * off_t(p.K);
   u32x4 ra[DMA ? 1 : LA], rb[DMA ? 1 : LB];
   auto load = [&](int g, int buf) {
-    const int k = g * kGroup + 16 * piece, n = p.K - k;   // n < 16: past the row's end, zeros
+    const int k[2] = {g * kGroup + 16 * piece, g * kGroup + 16 * (piece ^ 4)};
     if constexpr (DMA) {
       if ((g + 1) * kGroup <= p.K) {
 #pragma unroll
-        for (int i = 0; i < LA; ++i) dma16(ga + pa[i] + k, as[buf] + (w * LA + i) * 1024);
+        for (int i = 0; i < LA; ++i) dma16(ga + pa[i] + k[i & 1], as[buf] + (w * LA + i) * 1024);
 #pragma unroll
-        for (int i = 0; i < LB; ++i) dma16(gb + pb[i] + k, bs[buf] + (w * LB + i) * 1024);
-      } else {
+        for (int i = 0; i < LB; ++i) dma16(gb + pb[i] + k[i & 1], bs[buf] + (w * LB + i) * 1024);
+      } else {   // whole pieces, or zeros past the row's end
+        const u32x4 none = {0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < LA; ++i)
-          *reinterpret_cast<u32x4*>(as[buf] + (w * LA + i) * 1024 + 16 * l) = bytes16(ga + pa[i] + k, n);
+        for (int i = 0; i < LA; ++i) {
+          if (k[i & 1] < p.K) dma16(ga + pa[i] + k[i & 1], as[buf] + (w * LA + i) * 1024);
+          else *reinterpret_cast<u32x4*>(as[buf] + (w * LA + i) * 1024 + 16 * l) = none;
+        }
 #pragma unroll
-        for (int i = 0; i < LB; ++i)
-          *reinterpret_cast<u32x4*>(bs[buf] + (w * LB + i) * 1024 + 16 * l) = bytes16(gb + pb[i] + k, n);
+        for (int i = 0; i < LB; ++i) {
+          if (k[i & 1] < p.K) dma16(gb + pb[i] + k[i & 1], bs[buf] + (w * LB + i) * 1024);
+          else *reinterpret_cast<u32x4*>(bs[buf] + (w * LB + i) * 1024 + 16 * l) = none;
+        }
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < LA; ++i) ra[i] = bytes16(ga + pa[i] + k, n);
+      for (int i = 0; i < LA; ++i) ra[i] = bytes16(ga + pa[i] + k[i & 1], p.K - k[i & 1]);
 #pragma unroll
-      for (int i = 0; i < LB; ++i) rb[i] = bytes16(gb + pb[i] + k, n);
+      for (int i = 0; i < LB; ++i) rb[i] = bytes16(gb + pb[i] + k[i & 1], p.K - k[i & 1]);
     }
   };
   auto put_tiles = [&](int buf) {
@@ -231,25 +241,36 @@ __global__ __launch_bounds__(64 * WM * WN) void k_gemm(const GemmParams p) {
       sa[i] = ss[buf][wm + 32 * i + li];
       if constexpr (!ROWS) sa[i] *= ss[buf][BM + wn];   // the wave's rows of b lie in one block of 128
     }
+    // The sums of one tile are scaled while the next one's are formed
+    typename Bytes<EXACT>::T fb[2];
+    f32x16 x[2];
+    auto scale_in = [&](int t) {
+      const int j = t / MT, i = t % MT;
 #pragma unroll
-    for (int j = 0; j < QT; ++j) {
-      typename Bytes<EXACT>::T fb[2];
-#pragma unroll
-      for (int kk = 0; kk < 2; ++kk) fb[kk] = operand<EXACT>(frag(bs[buf], wn + 32 * j + br, kk));
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        f32x16 x;
-#pragma unroll
-        for (int r = 0; r < 16; ++r) x[r] = 0.f;
-        x = mul32(fb[0], fa[i][0], x);
-        x = mul32(fb[1], fa[i][1], x);
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const float s = ROWS ? sa[i] * ss[buf][BM + wn + 32 * j + 16 * half + r] : sa[i];
-          acc[j][i][r] = fmaf(x[r], s, acc[j][i][r]);
-        }
+      for (int r = 0; r < 16; ++r) {
+        const float s = ROWS ? sa[i] * ss[buf][BM + wn + 32 * j + 16 * half + r] : sa[i];
+        acc[j][i][r] = fmaf(x[t & 1][r], s, acc[j][i][r]);
       }
+      // the compiler would otherwise put all of these behind the loop's last branch and keep
+      // every tile's sums until then
+      asm volatile("" : "+v"(acc[j][i]));
+    };
+#pragma unroll
+    for (int t = 0; t < QT * MT; ++t) {
+      const int j = t / MT, i = t % MT;
+      if (i == 0) {
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) fb[kk] = operand<EXACT>(frag(bs[buf], wn + 32 * j + br, kk));
+      }
+#pragma unroll
+      for (int r = 0; r < 16; ++r) x[t & 1][r] = 0.f;
+      x[t & 1] = mul32(fb[0], fa[i][0], x[t & 1]);
+      x[t & 1] = mul32(fb[1], fa[i][1], x[t & 1]);
+      __builtin_amdgcn_sched_barrier(0);   // the next tile's instructions go first, then the scaling in their shadow
+      if (t) scale_in(t - 1);
+      __builtin_amdgcn_sched_barrier(0);
     }
+    scale_in(QT * MT - 1);
     if (more) {
       put_scales(buf ^ 1);
       put_tiles(buf ^ 1);
