@@ -17,10 +17,9 @@ namespace gdr {
 namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t __attribute__((ext_vector_type(4), aligned(1))) u32x4u;
 
-// Sum over 64 of the contraction (32x32) or 128 (16x16): a lane's 32 bytes of its row.
+// Sum over a group, 16 x 16: lane l's 32 bytes (piece l / 16 of a group) of row l mod 16.
 // EXACT: the e4m3 instructions align the products that they add together to the largest
 // of them and drop what lies 2^-13 below it (found by adding 2^-s to 1: from s = 14 on a
 // neighbour's 2^-s is gone, whichever e4m3 instruction is used).  On quantised normal
@@ -48,16 +47,8 @@ __device__ __forceinline__ typename Bytes<EXACT>::T operand(i32x8 u) {
     return u;
   }
 }
-__device__ __forceinline__ f32x16 mul32(i32x8 a, i32x8 b, f32x16 c) {
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
-}
 __device__ __forceinline__ f32x4 mul16(i32x8 a, i32x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
-}
-__device__ __forceinline__ f32x16 mul32(const Bytes<true>::T& a, const Bytes<true>::T& b, f32x16 c) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.v[i], b.v[i], c, 0, 0, 0);
-  return c;
 }
 __device__ __forceinline__ f32x4 mul16(const Bytes<true>::T& a, const Bytes<true>::T& b, f32x4 c) {
 #pragma unroll
@@ -100,14 +91,19 @@ __device__ __forceinline__ void put(void* c, int64_t at, int n, const float (&x)
 // ---------------------------------------------------------------------------
 // tiles
 // ---------------------------------------------------------------------------
-// LDS rows of 128 bytes; piece p (16 bytes) of row r at piece p ^ (r / 2 mod 8): the 16
-// lanes that a 16-byte read serves together lie in rows of which no two of one parity
-// (one half of the banks) share r / 2 mod 8
-__device__ __forceinline__ int place(int r, int p) { return r * 128 + ((p ^ ((r >> 1) & 7)) << 4); }
-__device__ __forceinline__ i32x8 frag(const char* t, int r, int kk) {
-  const int p = 4 * kk + 2 * (lane_id() >> 5);
-  const u32x4 lo = *reinterpret_cast<const u32x4*>(t + place(r, p));
-  const u32x4 hi = *reinterpret_cast<const u32x4*>(t + place(r, p + 1));
+// LDS rows of 128 bytes, a group each; piece p (16 bytes) of a row at piece p ^ f.  A
+// 16-byte read serves lanes 0-3, 12-15, 20-23 and 24-27 together (and three sets like it),
+// which are 4 runs of 4 rows, two of them 2 pieces further on; banks are 256 bytes, two
+// rows.  No two of a set meet where f is bit 1 of the row and, above it, minus the run's
+// number.  Row m of a's 16 is row m of the tile (run m / 4); row m of b's 16 is row
+// 16 (m / 4) + 4 t + m % 4 of 64 for the tile's t-th 16 (run: the row's 16), so that the
+// sums of four of them are 16 neighbours of c in a lane.
+__device__ __forceinline__ int turn_a(int r) { return ((r >> 1) & 1) | ((-(r >> 2) & 3) << 1); }
+__device__ __forceinline__ int turn_b(int r) { return ((r >> 1) & 1) | ((-(r >> 4) & 3) << 1); }
+__device__ __forceinline__ i32x8 frag(const char* row, int f) {
+  const int p = 2 * (lane_id() >> 4);
+  const u32x4 lo = *reinterpret_cast<const u32x4*>(row + ((p ^ f) << 4));
+  const u32x4 hi = *reinterpret_cast<const u32x4*>(row + (((p + 1) ^ f) << 4));
   return __builtin_bit_cast(i32x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
@@ -121,6 +117,13 @@ __device__ __forceinline__ void tile_at(int id, int tm, int tn, int& m, int& n) 
   n = r / rows;
 }
 
+// 16 bytes a lane from p + lane_off + wave_off to lds + 16 lane.  The buffer's size is no
+// check here: callers stay within the matrix.
+__device__ __forceinline__ void copy16(const uint8_t* p, uint32_t lane_off, int wave_off, char* lds) {
+  const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, 0x7fffffff, 0x00027000);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)((lds_char_t*)lds), 16, lane_off, wave_off, 0, 0);
+}
+
 template <bool SHORT> struct Off { typedef uint32_t T; };
 template <> struct Off<false> { typedef int64_t T; };
 
@@ -128,165 +131,167 @@ template <> struct Off<false> { typedef int64_t T; };
 // ROWS: b has a scale for each row.  DMA: rows start on 16 bytes.
 template <typename T, int BM, int BN, int WM, int WN, bool EXACT, bool ROWS, bool DMA>
 __global__ __launch_bounds__(64 * WM * WN) void k_gemm(const GemmParams p) {
-  constexpr int NT = 64 * WM * WN, MT = BM / WM / 32, QT = BN / WN / 32;
+  constexpr int NT = 64 * WM * WN, MT = BM / WM / 16, QT = BN / WN / 16;
   constexpr int LA = BM / 8 / (WM * WN), LB = BN / 8 / (WM * WN);   // 1 KB loads a wave
-  static_assert(BM + BN <= NT || BM + BN == 2 * NT, "scales per thread");
-  constexpr int SC = (BM + BN + NT - 1) / NT;
+  static_assert(QT % 4 == 0 && (LA + LB) % 4 == 0 && BM + BN == NT, "");
   __shared__ __attribute__((aligned(1024))) char as[2][BM * 128], bs[2][BN * 128];
-  __shared__ float ss[2][BM + BN];
+  __shared__ __attribute__((aligned(16))) float ss[2][BM + BN];
   int tm, tn;
   tile_at(int(blockIdx.x), (p.M + BM - 1) / BM, (p.N + BN - 1) / BN, tm, tn);
   const int m0 = tm * BM, n0 = tn * BN;
   const int per = (p.G + p.plan.splits - 1) / p.plan.splits, g0 = int(blockIdx.y) * per, g1 = min(p.G, g0 + per);
-  const int l = lane_id(), w = wave_id(), half = l >> 5;
+  const int l = lane_id(), w = __builtin_amdgcn_readfirstlane(wave_id()), h = l >> 4, li = l & 15;
   const int wm = (w % WM) * (BM / WM), wn = (w / WM) * (BN / WN);
-  // Rows past the matrix repeat its last one: what they give is not stored.  Offsets from
-  // the tile's first row: at most 256 rows of 2^30 bytes.
+  // Load i of a wave fills rows 8 (w L + i) + l / 8, lane l the place l mod 8.  Rows past the
+  // matrix repeat its last one: what they give is not stored.  Offsets from the tile's first
+  // row: at most 256 rows of 2^22 bytes, or 128 of 2^24.
   const uint8_t *ga = p.a + int64_t(m0) * p.K, *gb = p.b + int64_t(n0) * p.K;
   typedef typename Off<DMA>::T off_t;
-  off_t pa[LA], pb[LB];
-  // load i of the wave fills rows 8 i .. + 7 of its part; lane l its piece l mod 8 of row l / 8
-  static_assert(LA % 2 == 0 && LB % 2 == 0, "rows of load i: i mod 2 decides their places");
-  const int piece = (l & 7) ^ (l >> 4);   // for even i; ^ 4 for odd i
+  off_t at[LA + LB];
+  auto row_of = [&](int u) { return (u < LA ? w * LA + u : w * LB + u - LA) * 8 + (l >> 3); };
+  auto piece_of = [&](int u) { return (l & 7) ^ (u < LA ? turn_a(row_of(u)) : turn_b(row_of(u))); };
 #pragma unroll
-  for (int i = 0; i < LA; ++i) pa[i] = off_t(min((w * LA + i) * 8 + (l >> 3), p.M - 1 - m0)) * off_t(p.K);
+  for (int u = 0; u < LA + LB; ++u)
+    at[u] = off_t(min(row_of(u), u < LA ? p.M - 1 - m0 : p.N - 1 - n0)) * off_t(p.K) + off_t(16 * piece_of(u));
+  auto spot = [&](int u, int buf) { return u < LA ? as[buf] + (w * LA + u) * 1024 : bs[buf] + (w * LB + u - LA) * 1024; };
+  u32x4 raw[DMA ? 1 : LA + LB];
+  // load u of a whole group g
+  auto load = [&](int u, int g, int buf) {
+    if constexpr (DMA)
+      copy16(u < LA ? ga : gb, at[u], g * kGroup, spot(u, buf));
+    else
+      raw[u] = bytes16((u < LA ? ga : gb) + int64_t(g) * kGroup + at[u], 16);
+  };
+  // all of a last group that is shorter: zeros past the row's end
+  auto load_tail = [&](int g, int buf) {
 #pragma unroll
-  for (int i = 0; i < LB; ++i) pb[i] = off_t(min((w * LB + i) * 8 + (l >> 3), p.N - 1 - n0)) * off_t(p.K);
-  u32x4 ra[DMA ? 1 : LA], rb[DMA ? 1 : LB];
-  auto load = [&](int g, int buf) {
-    const int k[2] = {g * kGroup + 16 * piece, g * kGroup + 16 * (piece ^ 4)};
-    if constexpr (DMA) {
-      if ((g + 1) * kGroup <= p.K) {
-#pragma unroll
-        for (int i = 0; i < LA; ++i) dma16(ga + pa[i] + k[i & 1], as[buf] + (w * LA + i) * 1024);
-#pragma unroll
-        for (int i = 0; i < LB; ++i) dma16(gb + pb[i] + k[i & 1], bs[buf] + (w * LB + i) * 1024);
-      } else {   // whole pieces, or zeros past the row's end
-        const u32x4 none = {0, 0, 0, 0};
-#pragma unroll
-        for (int i = 0; i < LA; ++i) {
-          if (k[i & 1] < p.K) dma16(ga + pa[i] + k[i & 1], as[buf] + (w * LA + i) * 1024);
-          else *reinterpret_cast<u32x4*>(as[buf] + (w * LA + i) * 1024 + 16 * l) = none;
-        }
-#pragma unroll
-        for (int i = 0; i < LB; ++i) {
-          if (k[i & 1] < p.K) dma16(gb + pb[i] + k[i & 1], bs[buf] + (w * LB + i) * 1024);
-          else *reinterpret_cast<u32x4*>(bs[buf] + (w * LB + i) * 1024 + 16 * l) = none;
-        }
+    for (int u = 0; u < LA + LB; ++u) {
+      const uint8_t* src = (u < LA ? ga : gb) + int64_t(g) * kGroup + at[u];
+      const int n = p.K - g * kGroup - 16 * piece_of(u);
+      if constexpr (DMA) {
+        u32x4 v = {0, 0, 0, 0};
+        if (n > 0) v = *reinterpret_cast<const u32x4*>(src);   // a whole piece
+        *reinterpret_cast<u32x4*>(spot(u, buf) + 16 * l) = v;
+      } else {
+        raw[u] = bytes16(src, n);
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < LA; ++i) ra[i] = bytes16(ga + pa[i] + k[i & 1], p.K - k[i & 1]);
-#pragma unroll
-      for (int i = 0; i < LB; ++i) rb[i] = bytes16(gb + pb[i] + k[i & 1], p.K - k[i & 1]);
     }
   };
   auto put_tiles = [&](int buf) {
     if constexpr (!DMA) {
 #pragma unroll
-      for (int i = 0; i < LA; ++i) *reinterpret_cast<u32x4*>(as[buf] + (w * LA + i) * 1024 + 16 * l) = ra[i];
-#pragma unroll
-      for (int i = 0; i < LB; ++i) *reinterpret_cast<u32x4*>(bs[buf] + (w * LB + i) * 1024 + 16 * l) = rb[i];
+      for (int u = 0; u < LA + LB; ++u) *reinterpret_cast<u32x4*>(spot(u, buf) + 16 * l) = raw[u];
     }
   };
-  const float* psc[SC];
-#pragma unroll
-  for (int i = 0; i < SC; ++i) {
-    const int t = i * NT + threadIdx.x;
-    psc[i] = t < BM ? p.sa + int64_t(min(m0 + t, p.M - 1)) * p.G
-                    : p.sb + int64_t(min(n0 + t - BM, p.N - 1) / (ROWS ? 1 : kGroup)) * p.G;
-  }
-  float rs[SC];
-  auto load_scales = [&](int g) {
-#pragma unroll
-    for (int i = 0; i < SC; ++i)
-      if (i * NT + int(threadIdx.x) < BM + BN) rs[i] = psc[i][g];
-  };
-  auto put_scales = [&](int buf) {
-#pragma unroll
-    for (int i = 0; i < SC; ++i)
-      if (i * NT + int(threadIdx.x) < BM + BN) ss[buf][i * NT + threadIdx.x] = rs[i];
-  };
-  f32x16 acc[QT][MT];
+  // a thread's row of scales: of a, then of b
+  const int t = threadIdx.x;
+  const float* psc = t < BM ? p.sa + int64_t(min(m0 + t, p.M - 1)) * p.G
+                            : p.sb + int64_t(min(n0 + t - BM, p.N - 1) / (ROWS ? 1 : kGroup)) * p.G;
+  float rs;
+  f32x4 acc[QT][MT];
 #pragma unroll
   for (int j = 0; j < QT; ++j)
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[j][i][r] = 0.f;
-  // Row i of the instruction is row 16 (i / 4 % 2) + 4 (i / 8) + i % 4 of the 32: a lane's
-  // 16 sums then belong to 16 neighbours
-  const int li = l & 31, br = 16 * ((li >> 2) & 1) + 4 * (li >> 3) + (li & 3);
-  if (g0 < g1) {
-    load_scales(g0);
-    load(g0, 0);
-    put_scales(0);
-    put_tiles(0);
-  }
-  for (int g = g0; g < g1; ++g) {
-    const int buf = (g - g0) & 1;
+    for (int i = 0; i < MT; ++i) acc[j][i] = zero4();
+  typedef typename Bytes<EXACT>::T Op;
+  Op fa[MT], fb[2];
+  float sa[MT];
+  auto read_a = [&](int buf, int i) { return operand<EXACT>(frag(as[buf] + (wm + 16 * i + li) * 128, turn_a(li))); };
+  auto read_b = [&](int buf, int j) {
+    const int r = 16 * (li >> 2) + (li & 3);
+    return operand<EXACT>(frag(bs[buf] + (wn + 64 * (j / 4) + 4 * (j % 4) + r) * 128, turn_b(r)));
+  };
+  // the wave's rows of b lie in one block of 128
+  auto read_scale = [&](int buf, int i) { return ss[buf][wm + 16 * i + li] * (ROWS ? 1.f : ss[buf][BM + wn]); };
+  auto publish = [&]() {
     wait_vm<0>();
     chain_barrier();
-    const bool more = g + 1 < g1;
-    if (more) {
-      load_scales(g + 1);
-      load(g + 1, buf ^ 1);
-    }
-    typename Bytes<EXACT>::T fa[MT][2];
-    float sa[MT];
+  };
+  // A last group that is shorter comes first, so that the loop loads whole groups alone.
+  const int n = g1 - g0;
+  const bool tail = g1 == p.G && p.K % kGroup != 0;
+  auto group = [&](int i) { return tail ? (i == 0 ? g1 - 1 : g0 + i - 1) : g0 + i; };
+  rs = psc[group(0)];
+  if (tail) {
+    load_tail(g1 - 1, 0);
+  } else {
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
+    for (int u = 0; u < LA + LB; ++u) load(u, g0, 0);
+  }
+  ss[0][t] = rs;
+  put_tiles(0);
+  publish();
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk) fa[i][kk] = operand<EXACT>(frag(as[buf], wm + 32 * i + li, kk));
-      sa[i] = ss[buf][wm + 32 * i + li];
-      if constexpr (!ROWS) sa[i] *= ss[buf][BM + wn];   // the wave's rows of b lie in one block of 128
-    }
-    // The sums of one tile are scaled while the next one's are formed
-    typename Bytes<EXACT>::T fb[2];
-    f32x16 x[2];
-    auto scale_in = [&](int t) {
-      const int j = t / MT, i = t % MT;
+  for (int i = 0; i < MT; ++i) {
+    fa[i] = read_a(0, i);
+    sa[i] = read_scale(0, i);
+  }
+  fb[0] = read_b(0, 0);
+  // The it-th group is in buffer it mod 2 while the next one is loaded into the other, a few
+  // loads a tile of 16 rows of b: all at once would hold up every wave until the memory
+  // pipeline has taken them.  The barrier that shows the next group stands before the last
+  // tile, whose operands are in registers by then, and the next group's first operands are
+  // read under it (past the end, what the buffer held before).
+  constexpr int PER = (LA + LB) / 4;   // loads a tile
+  for (int it = 0; it < n; ++it) {
+    const int buf = it & 1, gn = group(min(it + 1, n - 1));
+    const bool more = it + 1 < n;
+    float sn[MT];
+    f32x4 x[2][MT], sb[2];
+    rs = psc[gn];
+    auto scale_in = [&](int j) {
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const float s = ROWS ? sa[i] * ss[buf][BM + wn + 32 * j + 16 * half + r] : sa[i];
-        acc[j][i][r] = fmaf(x[t & 1][r], s, acc[j][i][r]);
+      for (int i = 0; i < MT; ++i) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[j][i][r] = fmaf(x[j & 1][i][r], ROWS ? sa[i] * sb[j & 1][r] : sa[i], acc[j][i][r]);
+        // the compiler would otherwise put these behind the loop's end and keep all sums until then
+        asm volatile("" : "+v"(acc[j][i]));
       }
-      // the compiler would otherwise put all of these behind the loop's last branch and keep
-      // every tile's sums until then
-      asm volatile("" : "+v"(acc[j][i]));
     };
 #pragma unroll
-    for (int t = 0; t < QT * MT; ++t) {
-      const int j = t / MT, i = t % MT;
-      if (i == 0) {
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) fb[kk] = operand<EXACT>(frag(bs[buf], wn + 32 * j + br, kk));
+    for (int j = 0; j < QT; ++j) {
+      if (ROWS) sb[j & 1] = *reinterpret_cast<const f32x4*>(&ss[buf][BM + wn + 64 * (j / 4) + 16 * h + 4 * (j % 4)]);
+      if (j < QT - 1) {
+        fb[(j + 1) & 1] = read_b(buf, j + 1);
+      } else {
+        ss[buf ^ 1][t] = rs;
+        put_tiles(buf ^ 1);
+        publish();
+        fb[0] = read_b(buf ^ 1, 0);
       }
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int r = 0; r < 16; ++r) x[t & 1][r] = 0.f;
-      x[t & 1] = mul32(fb[0], fa[i][0], x[t & 1]);
-      x[t & 1] = mul32(fb[1], fa[i][1], x[t & 1]);
-      __builtin_amdgcn_sched_barrier(0);   // the next tile's instructions go first, then the scaling in their shadow
-      if (t) scale_in(t - 1);
+      for (int i = 0; i < MT; ++i) {
+        x[j & 1][i] = mul16(fb[j & 1], fa[i], zero4());
+        if (j == QT - 1) {
+          fa[i] = read_a(buf ^ 1, i);
+          sn[i] = read_scale(buf ^ 1, i);
+        }
+      }
+      if (j < 4 && j < QT - 1 && more) {
+#pragma unroll
+        for (int u = 0; u < (QT == 4 && j == 2 ? 2 * PER : PER); ++u) load(j * PER + u, gn, buf ^ 1);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      if (j) scale_in(j - 1);
       __builtin_amdgcn_sched_barrier(0);
     }
-    scale_in(QT * MT - 1);
-    if (more) {
-      put_scales(buf ^ 1);
-      put_tiles(buf ^ 1);
-    }
+    scale_in(QT - 1);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) sa[i] = sn[i];
   }
+  wait_vm<0>();
   void* c = p.plan.splits > 1 ? static_cast<void*>(p.part + int64_t(blockIdx.y) * p.M * p.N) : p.c;
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
-    const int m = m0 + wm + 32 * i + li;
+    const int m = m0 + wm + 16 * i + li;
     if (m >= p.M) continue;
 #pragma unroll
-    for (int j = 0; j < QT; ++j) {
-      const int n = n0 + wn + 32 * j + 16 * half;
+    for (int j = 0; j < QT; j += 4) {
+      const int n = n0 + wn + 16 * j + 16 * h;
       float x[16];
 #pragma unroll
-      for (int r = 0; r < 16; ++r) x[r] = acc[j][i][r];
+      for (int r = 0; r < 16; ++r) x[r] = acc[j + r / 4][i][r % 4];
       put<T, 16>(c, int64_t(m) * p.N + n, p.N - n, x);
     }
   }
