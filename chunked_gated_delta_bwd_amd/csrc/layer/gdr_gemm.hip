@@ -130,7 +130,7 @@ template <> struct Off<false> { typedef int64_t T; };
 // T: what the sums are stored as (fp32 for the partial sums of a split contraction).
 // ROWS: b has a scale for each row.  DMA: rows start on 16 bytes.
 template <typename T, int BM, int BN, int WM, int WN, bool EXACT, bool ROWS, bool DMA>
-__global__ __launch_bounds__(64 * WM * WN) void k_gemm(const GemmParams p) {
+__global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm(const GemmParams p) {
   constexpr int NT = 64 * WM * WN, MT = BM / WM / 16, QT = BN / WN / 16;
   constexpr int LA = BM / 8 / (WM * WN), LB = BN / 8 / (WM * WN);   // 1 KB loads a wave
   static_assert(QT % 4 == 0 && (LA + LB) % 4 == 0 && BM + BN == NT, "");
@@ -194,12 +194,12 @@ __global__ __launch_bounds__(64 * WM * WN) void k_gemm(const GemmParams p) {
 #pragma unroll
     for (int i = 0; i < MT; ++i) acc[j][i] = zero4();
   typedef typename Bytes<EXACT>::T Op;
-  Op fa[MT], fb[2];
+  i32x8 fa[MT], fb[2];   // as they lie in LDS; EXACT turns them into bf16 when they are used
   float sa[MT];
-  auto read_a = [&](int buf, int i) { return operand<EXACT>(frag(as[buf] + (wm + 16 * i + li) * 128, turn_a(li))); };
+  auto read_a = [&](int buf, int i) { return frag(as[buf] + (wm + 16 * i + li) * 128, turn_a(li)); };
   auto read_b = [&](int buf, int j) {
     const int r = 16 * (li >> 2) + (li & 3);
-    return operand<EXACT>(frag(bs[buf] + (wn + 64 * (j / 4) + 4 * (j % 4) + r) * 128, turn_b(r)));
+    return frag(bs[buf] + (wn + 64 * (j / 4) + 4 * (j % 4) + r) * 128, turn_b(r));
   };
   // the wave's rows of b lie in one block of 128
   auto read_scale = [&](int buf, int i) { return ss[buf][wm + 16 * i + li] * (ROWS ? 1.f : ss[buf][BM + wn]); };
@@ -238,6 +238,9 @@ __global__ __launch_bounds__(64 * WM * WN) void k_gemm(const GemmParams p) {
     const bool more = it + 1 < n;
     float sn[MT];
     f32x4 x[2][MT], sb[2];
+    Op oa[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) oa[i] = operand<EXACT>(fa[i]);
     rs = psc[gn];
     auto scale_in = [&](int j) {
 #pragma unroll
@@ -260,9 +263,18 @@ __global__ __launch_bounds__(64 * WM * WN) void k_gemm(const GemmParams p) {
         fb[0] = read_b(buf ^ 1, 0);
       }
       __builtin_amdgcn_sched_barrier(0);
+      const Op ob = operand<EXACT>(fb[j & 1]);
+      if constexpr (EXACT) {   // chains of four, side by side
+#pragma unroll
+        for (int i = 0; i < MT; ++i) x[j & 1][i] = zero4();
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int i = 0; i < MT; ++i) x[j & 1][i] = mma(ob.v[e], oa[i].v[e], x[j & 1][i]);
+      }
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        x[j & 1][i] = mul16(fb[j & 1], fa[i], zero4());
+        if constexpr (!EXACT) x[j & 1][i] = mul16(ob, oa[i], zero4());
         if (j == QT - 1) {
           fa[i] = read_a(buf ^ 1, i);
           sn[i] = read_scale(buf ^ 1, i);
