@@ -56,13 +56,23 @@ __device__ __forceinline__ f32x4 mul16(const Bytes<true>::T& a, const Bytes<true
   return c;
 }
 
-// n of the 16 bytes at p, the rest zero
-__device__ __forceinline__ u32x4 bytes16(const uint8_t* p, int n) {
-  if (n >= 16) return *reinterpret_cast<const u32x4u*>(p);
+// n of the 16 bytes at p, the rest zero; the matrix ends at `end`.  Only at its end are
+// they taken one by one: elsewhere what follows a row is the next one, and is masked.
+__device__ __forceinline__ u32x4 bytes16(const uint8_t* p, int n, const uint8_t* end) {
   u32x4 v = {0, 0, 0, 0};
+  if (n <= 0) return v;
+  if (p + 16 <= end) {
+    v = *reinterpret_cast<const u32x4u*>(p);
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
-    if (i < n) v[i / 4] |= uint32_t(p[i]) << (8 * (i % 4));
+    for (int i = 0; i < 4; ++i) {
+      const int k = n - 4 * i;
+      v[i] = k >= 4 ? v[i] : k <= 0 ? 0u : v[i] & ((1u << (8 * k)) - 1u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < n) v[i / 4] |= uint32_t(p[i]) << (8 * (i % 4));
+  }
   return v;
 }
 
@@ -160,7 +170,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm(const GemmParams p) {
     if constexpr (DMA)
       copy16(u < LA ? ga : gb, at[u], g * kGroup, spot(u, buf));
     else
-      raw[u] = bytes16((u < LA ? ga : gb) + int64_t(g) * kGroup + at[u], 16);
+      raw[u] = *reinterpret_cast<const u32x4u*>((u < LA ? ga : gb) + int64_t(g) * kGroup + at[u]);
   };
   // all of a last group that is shorter: zeros past the row's end
   auto load_tail = [&](int g, int buf) {
@@ -173,7 +183,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm(const GemmParams p) {
         if (n > 0) v = *reinterpret_cast<const u32x4*>(src);   // a whole piece
         *reinterpret_cast<u32x4*>(spot(u, buf) + 16 * l) = v;
       } else {
-        raw[u] = bytes16(src, n);
+        raw[u] = bytes16(src, n, u < LA ? p.a + int64_t(p.M) * p.K : p.b + int64_t(p.N) * p.K);
       }
     }
   };
@@ -232,7 +242,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm(const GemmParams p) {
   // pipeline has taken them.  The barrier that shows the next group stands before the last
   // tile, whose operands are in registers by then, and the next group's first operands are
   // read under it (past the end, what the buffer held before).
-  constexpr int PER = (LA + LB) / 4;   // loads a tile
+  constexpr int PER = (LA + LB) / (QT == 4 ? 2 : 4);   // loads a tile
   for (int it = 0; it < n; ++it) {
     const int buf = it & 1, gn = group(min(it + 1, n - 1));
     const bool more = it + 1 < n;
@@ -280,9 +290,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm(const GemmParams p) {
           sn[i] = read_scale(buf ^ 1, i);
         }
       }
-      if (j < 4 && j < QT - 1 && more) {
+      if (j * PER < LA + LB && more) {
 #pragma unroll
-        for (int u = 0; u < (QT == 4 && j == 2 ? 2 * PER : PER); ++u) load(j * PER + u, gn, buf ^ 1);
+        for (int u = 0; u < PER; ++u) load(j * PER + u, gn, buf ^ 1);
       }
       __builtin_amdgcn_sched_barrier(0);
       if (j) scale_in(j - 1);
@@ -312,20 +322,24 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm(const GemmParams p) {
 // The sum of the runs of a split contraction, in their order
 template <typename T>
 __global__ __launch_bounds__(256) void k_gemm_sum(const GemmParams p) {
-  const int64_t e = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4, all = int64_t(p.M) * p.N;
+  const int64_t e = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 8, all = int64_t(p.M) * p.N;
   if (e >= all) return;
-  const int n = int(min(int64_t(4), all - e));
-  float x[4] = {0.f, 0.f, 0.f, 0.f};
+  const int n = int(min(int64_t(8), all - e));
+  float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   for (int s = 0; s < p.plan.splits; ++s) {
     const float* q = p.part + s * all + e;
+    if (n == 8) {
+      const u32x4 a = *reinterpret_cast<const Wide<float>::T*>(q), b = *reinterpret_cast<const Wide<float>::T*>(q + 4);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < n) x[i] += q[i];
+      for (int i = 0; i < 4; ++i) {
+        x[i] += __uint_as_float(a[i]);
+        x[4 + i] += __uint_as_float(b[i]);
+      }
+    } else {
+      for (int i = 0; i < n; ++i) x[i] += q[i];
+    }
   }
-  T* d = static_cast<T*>(p.c) + e;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (i < n) d[i] = T(x[i]);
+  put<T, 8>(p.c, e, n, x);
 }
 
 // ---------------------------------------------------------------------------
@@ -353,11 +367,16 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_gemm_few(const GemmParams p)
   }
 #pragma unroll
   for (int r = 0; r < (ROWS ? 4 : 1); ++r) psb[r] = p.sb + int64_t(ROWS ? min(n0 + 4 * h + r, p.N - 1) : n0 / kGroup) * p.G;
-  auto bytes32 = [&](const uint8_t* s, int g) {
+  auto bytes32 = [&](const uint8_t* s, int g, const uint8_t* end) {
     const int k = g * kGroup, n = p.K - k - 32 * h;
     u32x4 lo, hi;
-    lo = bytes16(s + k, n);
-    hi = bytes16(s + k + 16, n - 16);
+    if ((g + 1) * kGroup <= p.K) {
+      lo = *reinterpret_cast<const u32x4u*>(s + k);
+      hi = *reinterpret_cast<const u32x4u*>(s + k + 16);
+    } else {
+      lo = bytes16(s + k, n, end);
+      hi = bytes16(s + k + 16, n - 16, end);
+    }
     return __builtin_bit_cast(i32x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
   };
   f32x4 acc[MT];
@@ -370,10 +389,10 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_gemm_few(const GemmParams p)
     for (int u = 0; u < U; ++u) {
       const int g = g0 + u * kFewWaves;
       if (g >= p.G) continue;
-      fb[u] = bytes32(pb, g);
+      fb[u] = bytes32(pb, g, p.b + int64_t(p.N) * p.K);
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        fa[u][i] = bytes32(pa[i], g);
+        fa[u][i] = bytes32(pa[i], g, p.a + int64_t(p.M) * p.K);
         sa[u][i] = psa[i][g];
       }
 #pragma unroll
@@ -442,7 +461,7 @@ int launch_type(const GemmParams& p, hipStream_t s) {
   if (p.plan.kind == 0) return rows ? few<T, true>(p, s) : few<T, false>(p, s);
   if (p.plan.splits == 1) return rows ? tiles<T, exact, true>(p, s) : tiles<T, exact, false>(p, s);
   if (const int e = rows ? tiles<float, exact, true>(p, s) : tiles<float, exact, false>(p, s)) return e;
-  k_gemm_sum<T><<<unsigned((int64_t(p.M) * p.N + 1023) / 1024), 256, 0, s>>>(p);
+  k_gemm_sum<T><<<unsigned((int64_t(p.M) * p.N + 2047) / 2048), 256, 0, s>>>(p);
   return static_cast<int>(hipGetLastError());
 }
 
