@@ -22,9 +22,17 @@ struct QuantParams {
 int launch_quant(const QuantParams& p, void* stream);
 
 // How a product is cut into workgroups.
+enum GemmKind {
+  kGemmFew = 0,     // every row of a, 16 of b
+  kGemmSmall = 1,   // tiles of 64 x 128 (rows of a, rows of b)
+  kGemmMedium = 2,  // of 128 x 128
+  kGemmLarge = 3,   // of 256 x 256
+};
+constexpr int kFewRows = 32;
 struct GemmPlan {
-  int32_t kind;               // 0: few rows of a; 1: tiles of 128 x 128; 2: tiles of 256 x 256
-  int32_t splits;             // runs of the contraction, each a workgroup's; their sums are added afterwards
+  int32_t kind;
+  int32_t splits;   // runs of the contraction, each a workgroup's; their sums are added afterwards
+  int32_t copy;     // rows start on 16 bytes: they go to LDS without passing through registers
 };
 
 struct GemmParams {

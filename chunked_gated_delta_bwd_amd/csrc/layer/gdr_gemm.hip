@@ -138,14 +138,16 @@ template <bool SHORT> struct Off { typedef uint32_t T; };
 template <> struct Off<false> { typedef int64_t T; };
 
 // T: what the sums are stored as (fp32 for the partial sums of a split contraction).
-// ROWS: b has a scale for each row.  DMA: rows start on 16 bytes.
-template <typename T, int BM, int BN, int WM, int WN, bool EXACT, bool ROWS, bool DMA>
+// NB: groups in LDS.  ROWS: b has a scale for each row.  DMA: rows start on 16 bytes.
+template <typename T, int BM, int BN, int WM, int WN, int NB, bool EXACT, bool ROWS, bool DMA>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm(const GemmParams p) {
   constexpr int NT = 64 * WM * WN, MT = BM / WM / 16, QT = BN / WN / 16;
   constexpr int LA = BM / 8 / (WM * WN), LB = BN / 8 / (WM * WN);   // 1 KB loads a wave
-  static_assert(QT % 4 == 0 && (LA + LB) % 4 == 0 && BM + BN == NT, "");
-  __shared__ __attribute__((aligned(1024))) char as[2][BM * 128], bs[2][BN * 128];
-  __shared__ __attribute__((aligned(16))) float ss[2][BM + BN];
+  static_assert(QT % 4 == 0 && BM + BN <= NT && (DMA || NB == 2), "");
+  constexpr int LOADS = LA + LB + 1;                                // of a wave and group, its scales included
+  constexpr int PER = (LA + LB + QT - 3) / (QT == 4 ? 2 : QT - 2);   // tiles' loads with each tile of 16 rows of b
+  __shared__ __attribute__((aligned(1024))) char as[NB][BM * 128], bs[NB][BN * 128];
+  __shared__ __attribute__((aligned(16))) float ss[NB][NT];
   int tm, tn;
   tile_at(int(blockIdx.x), (p.M + BM - 1) / BM, (p.N + BN - 1) / BN, tm, tn);
   const int m0 = tm * BM, n0 = tn * BN;
@@ -196,8 +198,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm(const GemmParams p) {
   // a thread's row of scales: of a, then of b
   const int t = threadIdx.x;
   const float* psc = t < BM ? p.sa + int64_t(min(m0 + t, p.M - 1)) * p.G
-                            : p.sb + int64_t(min(n0 + t - BM, p.N - 1) / (ROWS ? 1 : kGroup)) * p.G;
-  float rs;
+                            : p.sb + int64_t(min(n0 + min(t - BM, BN - 1), p.N - 1) / (ROWS ? 1 : kGroup)) * p.G;
+  auto load_scale = [&](int g, int buf) { dma4(psc + g, reinterpret_cast<char*>(&ss[buf][64 * w])); };
   f32x4 acc[QT][MT];
 #pragma unroll
   for (int j = 0; j < QT; ++j)
@@ -213,23 +215,32 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm(const GemmParams p) {
   };
   // the wave's rows of b lie in one block of 128
   auto read_scale = [&](int buf, int i) { return ss[buf][wm + 16 * i + li] * (ROWS ? 1.f : ss[buf][BM + wn]); };
+  // the group after the one in use has come; the loads of later ones may be on their way
   auto publish = [&]() {
-    wait_vm<0>();
+    wait_vm<(NB - 2) * LOADS>();
     chain_barrier();
   };
   // A last group that is shorter comes first, so that the loop loads whole groups alone.
   const int n = g1 - g0;
   const bool tail = g1 == p.G && p.K % kGroup != 0;
   auto group = [&](int i) { return tail ? (i == 0 ? g1 - 1 : g0 + i - 1) : g0 + i; };
-  rs = psc[group(0)];
+  load_scale(group(0), 0);
   if (tail) {
     load_tail(g1 - 1, 0);
   } else {
 #pragma unroll
     for (int u = 0; u < LA + LB; ++u) load(u, g0, 0);
   }
-  ss[0][t] = rs;
   put_tiles(0);
+#pragma unroll
+  for (int i = 1; i < NB - 1; ++i) {
+    load_scale(group(min(i, n - 1)), i);
+    if (n > 1 || !tail) {
+#pragma unroll
+      for (int u = 0; u < LA + LB; ++u) load(u, group(min(i, n - 1)), i);
+    }
+  }
+  if (n == 1) wait_vm<0>();   // there may be fewer loads than publish counts
   publish();
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
@@ -237,21 +248,22 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm(const GemmParams p) {
     sa[i] = read_scale(0, i);
   }
   fb[0] = read_b(0, 0);
-  // The it-th group is in buffer it mod 2 while the next one is loaded into the other, a few
-  // loads a tile of 16 rows of b: all at once would hold up every wave until the memory
-  // pipeline has taken them.  The barrier that shows the next group stands before the last
-  // tile, whose operands are in registers by then, and the next group's first operands are
-  // read under it (past the end, what the buffer held before).
-  constexpr int PER = (LA + LB) / (QT == 4 ? 2 : 4);   // loads a tile
+  // The it-th group is in buffer it mod NB while the one NB - 1 further on is loaded into the
+  // buffer that the last one has left, a few loads a tile of 16 rows of b: all at once would
+  // hold up every wave until the memory pipeline has taken them.  The barrier that shows the
+  // next group stands before the last tile, whose operands are in registers by then, and the
+  // next group's first operands are read under it.  Past the end the last group is loaded
+  // again, so that the loads on their way are always as many as publish counts.
+  int buf = 0, spare = NB - 1;
   for (int it = 0; it < n; ++it) {
-    const int buf = it & 1, gn = group(min(it + 1, n - 1));
-    const bool more = it + 1 < n;
+    const int next = buf + 1 == NB ? 0 : buf + 1, gn = group(min(it + NB - 1, n - 1));
+    const bool more = n > 1 || !tail;   // but for a contraction of less than one group
     float sn[MT];
     f32x4 x[2][MT], sb[2];
     Op oa[MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i) oa[i] = operand<EXACT>(fa[i]);
-    rs = psc[gn];
+    load_scale(gn, spare);
     auto scale_in = [&](int j) {
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
@@ -267,10 +279,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm(const GemmParams p) {
       if (j < QT - 1) {
         fb[(j + 1) & 1] = read_b(buf, j + 1);
       } else {
-        ss[buf ^ 1][t] = rs;
-        put_tiles(buf ^ 1);
+        put_tiles(next);
         publish();
-        fb[0] = read_b(buf ^ 1, 0);
+        fb[0] = read_b(next, 0);
       }
       __builtin_amdgcn_sched_barrier(0);
       const Op ob = operand<EXACT>(fb[j & 1]);
@@ -286,13 +297,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm(const GemmParams p) {
       for (int i = 0; i < MT; ++i) {
         if constexpr (!EXACT) x[j & 1][i] = mul16(ob, oa[i], zero4());
         if (j == QT - 1) {
-          fa[i] = read_a(buf ^ 1, i);
-          sn[i] = read_scale(buf ^ 1, i);
+          fa[i] = read_a(next, i);
+          sn[i] = read_scale(next, i);
         }
       }
       if (j * PER < LA + LB && more) {
 #pragma unroll
-        for (int u = 0; u < PER; ++u) load(j * PER + u, gn, buf ^ 1);
+        for (int u = j * PER; u < min((j + 1) * PER, LA + LB); ++u) load(u, gn, spare);
       }
       __builtin_amdgcn_sched_barrier(0);
       if (j) scale_in(j - 1);
@@ -301,8 +312,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm(const GemmParams p) {
     scale_in(QT - 1);
 #pragma unroll
     for (int i = 0; i < MT; ++i) sa[i] = sn[i];
+    spare = buf;
+    buf = next;
   }
-  wait_vm<0>();
+  wait_vm<0>();   // no load may reach LDS that is another workgroup's by then
   void* c = p.plan.splits > 1 ? static_cast<void*>(p.part + int64_t(blockIdx.y) * p.M * p.N) : p.c;
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
@@ -346,8 +359,8 @@ __global__ __launch_bounds__(256) void k_gemm_sum(const GemmParams p) {
 // few rows of a
 // ---------------------------------------------------------------------------
 // A workgroup of 8 waves takes 16 rows of b and all of a's, its waves every eighth group
-// of the contraction each (32 bytes of a lane's row straight from memory: every byte of b
-// is used once), and adds their sums in LDS.  Bound by the bytes of b.
+// of the contraction each (two pieces of a lane's row straight from memory: every byte of b
+// is used once; both operands take the group's bytes in the same order, whatever it is), and adds their sums in LDS.  Bound by the bytes of b.
 constexpr int kFewWaves = 8;
 
 template <typename T, int MT, bool ROWS>
@@ -356,26 +369,26 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_gemm_few(const GemmParams p)
   __shared__ __attribute__((aligned(16))) float sum[kFewWaves][16 * MT][20];   // [row of a][row of b], padded
   const int l = lane_id(), w = wave_id(), q = l & 15, h = l >> 4;
   const int n0 = int(blockIdx.x) * 16;
-  const uint8_t* pb = p.b + int64_t(min(n0 + q, p.N - 1)) * p.K + 32 * h;
+  const uint8_t* pb = p.b + int64_t(min(n0 + q, p.N - 1)) * p.K + 16 * h;
   const uint8_t* pa[MT];
   const float *psa[MT], *psb[ROWS ? 4 : 1];
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     const int64_t m = min(16 * i + q, p.M - 1);
-    pa[i] = p.a + m * p.K + 32 * h;
+    pa[i] = p.a + m * p.K + 16 * h;
     psa[i] = p.sa + m * p.G;
   }
 #pragma unroll
   for (int r = 0; r < (ROWS ? 4 : 1); ++r) psb[r] = p.sb + int64_t(ROWS ? min(n0 + 4 * h + r, p.N - 1) : n0 / kGroup) * p.G;
   auto bytes32 = [&](const uint8_t* s, int g, const uint8_t* end) {
-    const int k = g * kGroup, n = p.K - k - 32 * h;
+    const int k = g * kGroup, n = p.K - k - 16 * h;
     u32x4 lo, hi;
     if ((g + 1) * kGroup <= p.K) {
       lo = *reinterpret_cast<const u32x4u*>(s + k);
-      hi = *reinterpret_cast<const u32x4u*>(s + k + 16);
+      hi = *reinterpret_cast<const u32x4u*>(s + k + 64);
     } else {
       lo = bytes16(s + k, n, end);
-      hi = bytes16(s + k + 16, n - 16, end);
+      hi = bytes16(s + k + 64, n - 64, end);
     }
     return __builtin_bit_cast(i32x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
   };
@@ -435,30 +448,31 @@ template <typename T, bool ROWS>
 int few(const GemmParams& p, hipStream_t s) {
   const unsigned grid = unsigned((p.N + 15) / 16);
   if (p.M <= 16) k_gemm_few<T, 1, ROWS><<<grid, 64 * kFewWaves, 0, s>>>(p);
-  else if (p.M <= 32) k_gemm_few<T, 2, ROWS><<<grid, 64 * kFewWaves, 0, s>>>(p);
-  else k_gemm_few<T, 4, ROWS><<<grid, 64 * kFewWaves, 0, s>>>(p);
+  else k_gemm_few<T, 2, ROWS><<<grid, 64 * kFewWaves, 0, s>>>(p);
+  return static_cast<int>(hipGetLastError());
+}
+
+template <typename T, int BM, int BN, int WM, int WN, int NB, bool EXACT, bool ROWS, bool DMA>
+int tile(const GemmParams& p, hipStream_t s) {
+  const dim3 grid(unsigned(((p.M + BM - 1) / BM) * ((p.N + BN - 1) / BN)), unsigned(p.plan.splits));
+  k_gemm<T, BM, BN, WM, WN, NB, EXACT, ROWS, DMA><<<grid, 64 * WM * WN, 0, s>>>(p);
   return static_cast<int>(hipGetLastError());
 }
 
 template <typename T, bool EXACT, bool ROWS>
 int tiles(const GemmParams& p, hipStream_t s) {
-  const bool dma = p.K % 16 == 0 && p.K <= (1 << 24);   // 128 rows within 32 bits
-  if (p.plan.kind == 2) {
-    const dim3 grid(unsigned(((p.M + 255) / 256) * ((p.N + 255) / 256)), unsigned(p.plan.splits));
-    if constexpr (sizeof(T) == 2) k_gemm<T, 256, 256, 4, 2, false, ROWS, true><<<grid, 512, 0, s>>>(p);
-  } else {
-    const dim3 grid(unsigned(((p.M + 127) / 128) * ((p.N + 127) / 128)), unsigned(p.plan.splits));
-    if (dma) k_gemm<T, 128, 128, 2, 2, EXACT, ROWS, true><<<grid, 256, 0, s>>>(p);
-    else k_gemm<T, 128, 128, 2, 2, EXACT, ROWS, false><<<grid, 256, 0, s>>>(p);
-  }
-  return static_cast<int>(hipGetLastError());
+  if (p.plan.kind == kGemmSmall)
+    return p.plan.copy ? tile<T, 64, 128, 2, 2, 3, EXACT, ROWS, true>(p, s) : tile<T, 64, 128, 2, 2, 2, EXACT, ROWS, false>(p, s);
+  if constexpr (sizeof(T) == 2)   // bf16 results, a contraction that is not split
+    if (p.plan.kind == kGemmLarge) return tile<T, 256, 256, 4, 2, 2, EXACT, ROWS, true>(p, s);
+  return p.plan.copy ? tile<T, 128, 128, 2, 2, 2, EXACT, ROWS, true>(p, s) : tile<T, 128, 128, 2, 2, 2, EXACT, ROWS, false>(p, s);
 }
 
 template <typename T>
 int launch_type(const GemmParams& p, hipStream_t s) {
   constexpr bool exact = sizeof(T) == 4;
   const bool rows = p.block == 1;
-  if (p.plan.kind == 0) return rows ? few<T, true>(p, s) : few<T, false>(p, s);
+  if (p.plan.kind == kGemmFew) return rows ? few<T, true>(p, s) : few<T, false>(p, s);
   if (p.plan.splits == 1) return rows ? tiles<T, exact, true>(p, s) : tiles<T, exact, false>(p, s);
   if (const int e = rows ? tiles<float, exact, true>(p, s) : tiles<float, exact, false>(p, s)) return e;
   k_gemm_sum<T><<<unsigned((int64_t(p.M) * p.N + 2047) / 2048), 256, 0, s>>>(p);

@@ -155,7 +155,7 @@ def test_quant_nonfinite_and_tiny(block, transpose):
 
 def test_streams_graphs_and_two_calls_at_once():
     gen = torch.Generator().manual_seed(6)
-    M, N, K = 200, 300, 1100
+    M, N, K = 200, 300, 2100
     x, w = R.rand(gen, M, K).float().cuda(), R.rand(gen, N, K).float().cuda()
     px, pw = B.QuantProblem(M, K, B.GDR_F32), B.QuantProblem(N, K, B.GDR_F32, block=128)
     prob = B.GemmProblem(M, N, K, B.GDR_BF16)
