@@ -18,8 +18,6 @@
 namespace gdr {
 namespace {
 
-constexpr int kB = kLinBlock;
-
 // ---------------------------------------------------------------------------
 // fragments of a type: 16 bytes of each lane, KS elements of the contraction a step
 // ---------------------------------------------------------------------------
@@ -60,26 +58,34 @@ template <> struct Lin<bf16> {
   static __device__ __forceinline__ void store4(char* p, float a, float b, float c, float d) {
     *reinterpret_cast<uint2*>(p) = pack4_bf16(a, b, c, d);
   }
+  static constexpr int B = 64;       // tokens per block
   // nonzero where one of the eight has all exponent bits set
-  static __device__ __forceinline__ uint32_t bad(const u32x4& u) {
+  static __device__ __forceinline__ uint32_t bad(Frag f) {
+    const u32x4 u = __builtin_bit_cast(u32x4, f);
     uint32_t b = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) b |= (u[i] & 0x7f807f80u) + 0x00800080u;
     return b & 0x80008000u;
   }
-  static __device__ __forceinline__ bool bad1(const char* p) {
-    return (*reinterpret_cast<const uint16_t*>(p) & 0x7f80u) == 0x7f80u;
+  static __device__ __forceinline__ float get(Frag f, int e) {
+    const u32x4 u = __builtin_bit_cast(u32x4, f);
+    return __uint_as_float(e & 1 ? u[e / 2] & 0xffff0000u : u[e / 2] << 16);
   }
-  static __device__ __forceinline__ void clear1(char* p) { *reinterpret_cast<uint16_t*>(p) = 0; }
+  static __device__ __forceinline__ Frag without(Frag f, uint32_t drop) {   // bit e of drop: element e becomes 0
+    u32x4 u = __builtin_bit_cast(u32x4, f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] &= (drop >> (2 * i) & 1 ? 0xffff0000u : ~0u) & (drop >> (2 * i + 1) & 1 ? 0x0000ffffu : ~0u);
+    return __builtin_bit_cast(Frag, u);
+  }
 };
 
 template <> struct Lin<float> {
   typedef f32x4 Frag;
   static constexpr int KS = 16;
   static constexpr int E = 4;
-  // Piece c / 4 (16 bytes) of row r at piece (c / 4) ^ (r % 16)
+  // Piece c / 4 (16 bytes) of row r at piece (c / 4) ^ (r % 16), r % 8 where a row has 8
   template <int W> static __device__ __forceinline__ int off(int r, int c) {
-    return r * (4 * W) + (((c >> 2) ^ (r & 15)) << 4) + ((c & 3) << 2);
+    return r * (4 * W) + (((c >> 2) ^ (r & (W >= 64 ? 15 : 7))) << 4) + ((c & 3) << 2);
   }
   template <int W> static __device__ __forceinline__ Frag rk(const char* t, int r0, int k0) {
     const int l = lane_id();
@@ -107,16 +113,19 @@ template <> struct Lin<float> {
   static __device__ __forceinline__ void store4(char* p, float a, float b, float c, float d) {
     *reinterpret_cast<f32x4*>(p) = f32x4{a, b, c, d};
   }
-  static __device__ __forceinline__ uint32_t bad(const u32x4& u) {
+  static constexpr int B = 32;
+  static __device__ __forceinline__ uint32_t bad(Frag f) {
     uint32_t b = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) b |= (u[i] & 0x7f800000u) + 0x00800000u;
+    for (int i = 0; i < 4; ++i) b |= (__float_as_uint(f[i]) & 0x7f800000u) + 0x00800000u;
     return b & 0x80000000u;
   }
-  static __device__ __forceinline__ bool bad1(const char* p) {
-    return (*reinterpret_cast<const uint32_t*>(p) & 0x7f800000u) == 0x7f800000u;
+  static __device__ __forceinline__ float get(Frag f, int e) { return f[e]; }
+  static __device__ __forceinline__ Frag without(Frag f, uint32_t drop) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = drop >> i & 1 ? 0.f : f[i];
+    return f;
   }
-  static __device__ __forceinline__ void clear1(char* p) { *reinterpret_cast<uint32_t*>(p) = 0; }
 };
 
 // ---------------------------------------------------------------------------
@@ -143,8 +152,8 @@ __device__ __forceinline__ float decay2(const LinParams& p, int h) {
 // not add up over the blocks of a long sequence
 __device__ __forceinline__ float decay_m1(float l2, int n) { return expm1f(float(n) * l2 * 0.6931471805599453f); }
 
-// 16-byte pieces of a block of 64 rows for each of 256 threads
-template <typename T, int D> constexpr int kPieces = kB * D * int(sizeof(T)) / 16 / 256;
+// 16-byte pieces of a block for each of 256 threads
+template <typename T, int D> constexpr int kPieces = Lin<T>::B * D * int(sizeof(T)) / 16 / 256;
 
 template <typename T, int D>
 __device__ __forceinline__ void load_block(const void* base, int64_t row0, int64_t stride, int n,
@@ -170,9 +179,9 @@ __device__ __forceinline__ void put_block(char* tile, const u32x4 (&r)[kPieces<T
 // ---------------------------------------------------------------------------
 // the state of a wave: columns [slab, slab + 16 VT) of S^T, all D rows
 // ---------------------------------------------------------------------------
-template <typename T, int D>
+template <typename T, int D, int VT>
 struct State {
-  static constexpr int VT = D / 64, KT = D / 16, JS = kB / Lin<T>::KS;
+  static constexpr int KT = D / 16, JS = Lin<T>::B / Lin<T>::KS;
   f32x4 s[KT][VT];
 
   __device__ __forceinline__ void zero() {
@@ -256,10 +265,10 @@ struct State {
 
 // Weights of a block's tokens in the state's update: c^(n-1-j), or c^(j+1) backwards
 template <typename T, bool REV>
-__device__ __forceinline__ void state_weights(float l2, int n, float scale, float (&w)[kB / Lin<T>::KS][Lin<T>::E]) {
+__device__ __forceinline__ void state_weights(float l2, int n, float scale, float (&w)[Lin<T>::B / Lin<T>::KS][Lin<T>::E]) {
   const int g = lane_id() >> 4;
 #pragma unroll
-  for (int js = 0; js < kB / Lin<T>::KS; ++js)
+  for (int js = 0; js < Lin<T>::B / Lin<T>::KS; ++js)
 #pragma unroll
     for (int e = 0; e < Lin<T>::E; ++e) {
       const int j = js * Lin<T>::KS + Lin<T>::E * g + e;
@@ -294,7 +303,7 @@ __global__ __launch_bounds__(256) void k_lin_table(const LinParams p, const LinB
 // ---------------------------------------------------------------------------
 template <typename T, int D, bool REV>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_lin_local(const LinParams p) {
-  constexpr int TB = kB * D * int(sizeof(T)), VT = D / 64, JS = kB / Lin<T>::KS;
+  constexpr int kB = Lin<T>::B, TB = kB * D * int(sizeof(T)), VT = D / 64, JS = kB / Lin<T>::KS;
   __shared__ __attribute__((aligned(1024))) char ys[TB], zs[TB];
   int c, h;
   chunk_head_at(p, int(blockIdx.x), c, h);
@@ -304,7 +313,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_lin_local(const
   const void *y = REV ? p.q : p.k, *z = REV ? p.dO : p.v;
   const float l2 = decay2(p, h), wscale = REV ? p.scale : 1.f;
   const int slab = wave_id() * 16 * VT, nb = (sg.len + kB - 1) / kB;
-  State<T, D> S;
+  State<T, D, VT> S;
   S.zero();
   float w[JS][Lin<T>::E], em1 = 0.f;
   int wn = -1;
@@ -385,135 +394,181 @@ __global__ __launch_bounds__(256) void k_lin_carry(const LinParams p) {
 // ---------------------------------------------------------------------------
 // outputs
 // ---------------------------------------------------------------------------
+// What one group of waves computes: out from the tiles x, y, z of a block.
 struct LinRole {
-  const void *x, *y, *z;
   void* out;
   float* last;            // state after the last segment (before the first, backwards), or NULL
   const float* first;     // state of the whole sequence's start (end, backwards), or NULL
   const float* st;        // states of the segments
-  int32_t xk, yk, zk;     // 1: the tensor has Hk heads, 0: H
+  int32_t x, y, z;        // its tensors among those of the call
   int32_t transposed;     // the state's memory is [y channel][z channel]
-  int32_t out_f32;        // out is the fp32 partial sum per value head
   float pair, inter, add; // factors of the pairs' product, of S x, of the state's update
 };
+struct LinCall {
+  const void* t[4];       // tensors
+  int32_t shared[4];      // 1: with Hk heads, 0: with H
+  LinRole r[2];
+};
 
-template <typename T, int D, bool REV>
-__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_lin_out(const LinParams p, const LinRole o) {
+// TILES tensors are copied to LDS block by block, one block ahead; ROLES groups of
+// D / 16 / VT waves work on them.  OUT32: out is fp32 (a value head's share of the
+// gradient of a grouped q or k).
+template <typename T, int D, bool REV, int TILES, int ROLES, int VT, bool OUT32>
+__global__ __launch_bounds__(ROLES * (D / 16 / VT) * 64, ROLES * (D / 16 / VT) / 4) void k_lin_out(const LinParams p, const LinCall o) {
   typedef typename Lin<T>::Frag Frag;
-  constexpr int TB = kB * D * int(sizeof(T)), VT = D / 64, KS = Lin<T>::KS, JS = kB / KS, E = Lin<T>::E;
-  __shared__ __attribute__((aligned(1024))) char xs[TB], ys[TB], zs[TB], ps[kB * kB * int(sizeof(T))];
-  __shared__ int bad_s[D], flag_s;
+  constexpr int kB = Lin<T>::B, KS = Lin<T>::KS, JS = kB / KS, E = Lin<T>::E, TI = kB / 16;
+  constexpr int RW = D / 16 / VT, NW = ROLES * RW;                     // waves of a role, of the workgroup
+  constexpr int ROW = D * int(sizeof(T)), TB = kB * ROW, PR = ROW / 16;   // bytes of a row and a tile, pieces of a row
+  constexpr int LPT = TB / 1024 / NW, RPL = 1024 / ROW;                // a wave's 1 KB loads of a tile, rows of a load
+  constexpr int NPAIR = TI * TI / RW > 0 ? TI * TI / RW : 1;           // tiles of pairs of a wave
+  constexpr int STORES = TI * (VT == 2 && sizeof(T) == 2 && !OUT32 ? 1 : VT);   // of a wave and block
+  static_assert(LPT >= 1 && TB / 1024 % NW == 0 && (NW * RPL) % 16 == 0, "a load's rows turn alike");
+  __shared__ __attribute__((aligned(1024))) char tiles[2][TILES][TB];
+  __shared__ __attribute__((aligned(1024))) char pairs[ROLES][kB * kB * int(sizeof(T))];
   int c, h;
   chunk_head_at(p, int(blockIdx.x), c, h);
   const LinSeg sg = seg_at(p, c);
-  const int l = lane_id(), q = l & 15, g = l >> 4, w = wave_id();
+  const int l = lane_id(), q = l & 15, g = l >> 4, wave = __builtin_amdgcn_readfirstlane(wave_id());
+  const int role = ROLES == 1 ? 0 : wave / RW, w = wave % RW;
+  const LinRole& ro = o.r[role];
   const int slab = w * 16 * VT, nb = (sg.len + kB - 1) / kB;
   const float l2 = decay2(p, h);
-  const int xH = o.xk ? p.Hk : p.H, yH = o.yk ? p.Hk : p.H, zH = o.zk ? p.Hk : p.H;
-  const int xh = o.xk ? h / p.G : h, yh = o.yk ? h / p.G : h, zh = o.zk ? h / p.G : h;
   const int64_t sh = int64_t(sg.seq) * p.H + h;
-  u32x4 xr[kPieces<T, D>], yr[kPieces<T, D>], zr[kPieces<T, D>];
+  // A lane's row and place in a load, and the piece that belongs there
+  const int lrow = wave * RPL + l / PR, piece = Lin<T>::template off<D>(lrow & 15, 0) % ROW / 16 ^ (l % PR);
   auto load = [&](int i) {
     const int b = REV ? nb - 1 - i : i, n = min(kB, sg.len - b * kB);
-    const int64_t t = sg.t0 + int64_t(b) * kB;
-    load_block<T, D>(o.x, (t * xH + xh) * D, int64_t(xH) * D, n, xr);
-    load_block<T, D>(o.y, (t * yH + yh) * D, int64_t(yH) * D, n, yr);
-    load_block<T, D>(o.z, (t * zH + zh) * D, int64_t(zH) * D, n, zr);
+    const int64_t t0 = sg.t0 + int64_t(b) * kB;
+#pragma unroll
+    for (int m = 0; m < TILES; ++m) {
+      const int heads = o.shared[m] ? p.Hk : p.H, head = o.shared[m] ? h / p.G : h;
+      const char* src = static_cast<const char*>(o.t[m]) + (t0 * heads + head) * ROW;
+#pragma unroll
+      for (int a = 0; a < LPT; ++a) {
+        // rows past the end repeat the last one; they are cleared when they have come
+        const int row = min(a * NW * RPL + lrow, n - 1);
+        dma16(src + int64_t(row) * heads * ROW + 16 * piece, tiles[i & 1][m] + (a * NW + wave) * 1024);
+      }
+    }
   };
   if (nb) load(0);
-  State<T, D> S;
+  State<T, D, VT> S;
   const bool start = REV ? sg.idx == sg.nseg - 1 : sg.idx == 0;
-  if (!start) S.load(o.st + (int64_t(c) * p.H + h) * (D * D), o.transposed, slab);
-  else if (o.first) S.load(o.first + sh * (D * D), o.transposed, slab);
+  if (!start) S.load(ro.st + (int64_t(c) * p.H + h) * (D * D), ro.transposed, slab);
+  else if (ro.first) S.load(ro.first + sh * (D * D), ro.transposed, slab);
   else S.zero();
-  // decay between the wave's 16 tokens i and the block's j
-  float near[4][4];
+  // The wave's tiles of pairs: tokens i of tile w % TI, tokens j of w / TI and every RW / TI-th
+  // on, and the decay between them
+  const int it0 = w % TI, jt0 = w / TI;
+  constexpr int JSTEP = RW / TI > 0 ? RW / TI : 1;
+  float near[NPAIR][4];
 #pragma unroll
-  for (int jt = 0; jt < 4; ++jt)
+  for (int a = 0; a < NPAIR; ++a)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int d = (16 * w + q) - (16 * jt + 4 * g + r), n = REV ? -d : d;
-      near[jt][r] = n >= 0 ? o.pair * fast_exp2(float(n) * l2) : 0.f;
+      const int d = (16 * it0 + q) - (16 * (jt0 + a * JSTEP) + 4 * g + r), n = REV ? -d : d;
+      near[a][r] = n >= 0 ? ro.pair * fast_exp2(float(n) * l2) : 0.f;
     }
   // the pairs of later tokens are never written again
-  for (int i = threadIdx.x; i < kB * kB * int(sizeof(T)) / 16; i += 256) *reinterpret_cast<u32x4*>(ps + 16 * i) = u32x4{0, 0, 0, 0};
-  if (threadIdx.x == 0) flag_s = 0;
-  float wz[JS][E], far[4], em1 = 0.f;
+  char* const ps = pairs[role];
+  for (int i = w * 64 + l; i < kB * kB * int(sizeof(T)) / 16; i += RW * 64) *reinterpret_cast<u32x4*>(ps + 16 * i) = u32x4{0, 0, 0, 0};
+  float wz[JS][E], far[TI], em1 = 0.f;
   int wn = -1;
   for (int i = 0; i < nb; ++i) {
     const int b = REV ? nb - 1 - i : i, n = min(kB, sg.len - b * kB);
     const int64_t t0 = sg.t0 + int64_t(b) * kB;
+    // The block has come.  Behind its loads a wave has issued the stores of the block before
+    // alone, STORES of them unless that block was not whole.
+    if (wn == kB) wait_vm<STORES>();
+    else wait_vm<0>();
+    chain_barrier();
     if (n != wn) {
-      state_weights<T, REV>(l2, n, o.add, wz);
+      state_weights<T, REV>(l2, n, ro.add, wz);
       em1 = decay_m1(l2, n);
 #pragma unroll
-      for (int it = 0; it < 4; ++it) {
+      for (int it = 0; it < TI; ++it) {
         const int m = REV ? n - 1 - (16 * it + q) : 16 * it + q + 1;
-        far[it] = m >= 0 ? o.inter * fast_exp2(float(m) * l2) : 0.f;
+        far[it] = m >= 0 ? ro.inter * fast_exp2(float(m) * l2) : 0.f;
       }
       wn = n;
     }
-    chain_barrier();
-    put_block<T, D>(xs, xr);
-    put_block<T, D>(ys, yr);
-    put_block<T, D>(zs, zr);
-    uint32_t bad = 0;
-#pragma unroll
-    for (int a = 0; a < kPieces<T, D>; ++a) bad |= Lin<T>::bad(zr[a]);
-    if (bad) flag_s = 1;
     if (i + 1 < nb) load(i + 1);
-    chain_barrier();
-    // pairs: P[i][j] = c^|i-j| (x_i . y_j), the wave's 16 tokens i against the block's j
-    {
+    if (n < kB) {
+      for (int m = 0; m < TILES; ++m)
+        for (int a = threadIdx.x; a < (kB - n) * PR; a += NW * 64)
+          *reinterpret_cast<u32x4*>(tiles[i & 1][m] + n * ROW + 16 * a) = u32x4{0, 0, 0, 0};
+      chain_barrier();
+    }
+    const char *const xs = tiles[i & 1][ro.x], *const ys = tiles[i & 1][ro.y], *const zs = tiles[i & 1][ro.z];
+    // pairs: P[i][j] = c^|i-j| (x_i . y_j)
+    if (jt0 < TI) {
       Frag xf[D / KS];
 #pragma unroll
-      for (int ks = 0; ks < D / KS; ++ks) xf[ks] = Lin<T>::template rk<D>(xs, 16 * w, ks * KS);
+      for (int ks = 0; ks < D / KS; ++ks) xf[ks] = Lin<T>::template rk<D>(xs, 16 * it0, ks * KS);
 #pragma unroll
-      for (int jt = 0; jt < 4; ++jt) {
-        if (REV ? jt < w : jt > w) continue;
+      for (int s = 0; s < NPAIR; ++s) {
+        const int jt = jt0 + s * JSTEP;
+        if (REV ? jt < it0 : jt > it0) continue;
         f32x4 a = zero4();
 #pragma unroll
         for (int ks = 0; ks < D / KS; ++ks) Lin<T>::mul(Lin<T>::template rk<D>(ys, 16 * jt, ks * KS), xf[ks], a);
         // a later token's product counts nothing, whatever it is
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int d = (16 * w + q) - (16 * jt + 4 * g + r);
-          a[r] = (REV ? d <= 0 : d >= 0) ? a[r] * near[jt][r] : 0.f;
+          const int d = (16 * it0 + q) - (16 * jt + 4 * g + r);
+          a[r] = (REV ? d <= 0 : d >= 0) ? a[r] * near[s][r] : 0.f;
         }
-        Lin<T>::store4(ps + Lin<T>::template off<kB>(16 * w + q, 16 * jt + 4 * g), a[0], a[1], a[2], a[3]);
+        Lin<T>::store4(ps + Lin<T>::template off<kB>(16 * it0 + q, 16 * jt + 4 * g), a[0], a[1], a[2], a[3]);
+      }
+    }
+    Frag zf[JS][VT];
+    uint32_t bad = 0;
+#pragma unroll
+    for (int js = 0; js < JS; ++js)
+#pragma unroll
+      for (int u = 0; u < VT; ++u) {
+        zf[js][u] = Lin<T>::template slab<D, VT>(zs, slab, u, js * KS);
+        bad |= Lin<T>::bad(zf[js][u]);
+      }
+    // Infinities and NaN in z: a zero pair times one would reach tokens before it, so the
+    // products take zeros in their place, and what comes from that token on is NaN: first[u],
+    // in the order of the walk, for column u of the lane's.
+    int first[VT];
+    const bool odd = __any(bad != 0);
+    if (odd) {
+#pragma unroll
+      for (int u = 0; u < VT; ++u) {
+        first[u] = kB;
+#pragma unroll
+        for (int js = 0; js < JS; ++js) {
+          uint32_t drop = 0;
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const int j = js * KS + E * g + e;
+            if (!(fabsf(Lin<T>::get(zf[js][u], e)) <= 3.4028235e38f)) {
+              drop |= 1u << e;
+              first[u] = min(first[u], REV ? kB - 1 - j : j);
+            }
+          }
+          zf[js][u] = Lin<T>::without(zf[js][u], drop);
+        }
+        first[u] = min(first[u], __shfl_xor(first[u], 16, 64));
+        first[u] = min(first[u], __shfl_xor(first[u], 32, 64));
       }
     }
     chain_barrier();
-    const bool odd = flag_s;
-    if (odd) {
-      // Infinities and NaN in z: a zero pair times one would reach tokens before it, so the
-      // products take zeros in their place, and what comes from that token on is NaN.
-      if (threadIdx.x < D) {
-        int first = kB;
-        for (int a = kB - 1; a >= 0; --a) {
-          char* e = zs + Lin<T>::template off<D>(REV ? kB - 1 - a : a, threadIdx.x);
-          if (Lin<T>::bad1(e)) {
-            first = a;
-            Lin<T>::clear1(e);
-          }
-        }
-        bad_s[threadIdx.x] = first;
-      }
-      chain_barrier();
-      if (threadIdx.x == 0) flag_s = 0;
-    }
-    f32x4 acc[VT][4];
+    f32x4 acc[VT][TI];
 #pragma unroll
     for (int u = 0; u < VT; ++u)
 #pragma unroll
-      for (int it = 0; it < 4; ++it) acc[u][it] = zero4();
+      for (int it = 0; it < TI; ++it) acc[u][it] = zero4();
 #pragma unroll
     for (int ks = 0; ks < D / KS; ++ks) {
       Frag a[VT];
 #pragma unroll
       for (int u = 0; u < VT; ++u) a[u] = Lin<T>::state(S.s[ks * KS / 16][u], S.s[ks * KS / 16 + (KS == 32)][u]);
 #pragma unroll
-      for (int it = 0; it < 4; ++it) {
+      for (int it = 0; it < TI; ++it) {
         const Frag f = Lin<T>::template rk_state<D>(xs, 16 * it, ks * KS);
 #pragma unroll
         for (int u = 0; u < VT; ++u) Lin<T>::mul(a[u], f, acc[u][it]);
@@ -522,61 +577,55 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_lin_out(const L
 #pragma unroll
     for (int u = 0; u < VT; ++u)
 #pragma unroll
-      for (int it = 0; it < 4; ++it)
+      for (int it = 0; it < TI; ++it)
 #pragma unroll
         for (int r = 0; r < 4; ++r) acc[u][it][r] *= far[it];
-    Frag zf[JS][VT];
 #pragma unroll
-    for (int js = 0; js < JS; ++js) {
+    for (int js = 0; js < JS; ++js)
 #pragma unroll
-      for (int u = 0; u < VT; ++u) zf[js][u] = Lin<T>::template slab<D, VT>(zs, slab, u, js * KS);
-#pragma unroll
-      for (int it = 0; it < 4; ++it) {
+      for (int it = 0; it < TI; ++it) {
         if (REV ? (js + 1) * KS <= 16 * it : js * KS >= 16 * (it + 1)) continue;
         const Frag f = Lin<T>::template rk<kB>(ps, 16 * it, js * KS);
 #pragma unroll
         for (int u = 0; u < VT; ++u) Lin<T>::mul(zf[js][u], f, acc[u][it]);
       }
-    }
     if (odd) {
 #pragma unroll
       for (int u = 0; u < VT; ++u)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int first = bad_s[slab + Lin<T>::template col<VT>(u, 4 * g + r)];
+          const int from = __shfl(first[u], 4 * g + r, 64);
 #pragma unroll
-          for (int it = 0; it < 4; ++it)
-            if ((REV ? kB - 1 - (16 * it + q) : 16 * it + q) >= first) acc[u][it][r] = __builtin_nanf("");
+          for (int it = 0; it < TI; ++it)
+            if ((REV ? kB - 1 - (16 * it + q) : 16 * it + q) >= from) acc[u][it][r] = __builtin_nanf("");
         }
     }
+    auto store = [&](int it) {
+      const int64_t at = ((t0 + 16 * it + q) * p.H + h) * D + slab;
+      if constexpr (OUT32 || sizeof(T) == 4) {
 #pragma unroll
-    for (int it = 0; it < 4; ++it) {
-      const int tok = 16 * it + q;
-      if (tok >= n) continue;
-      if (o.out_f32) {
-        float* d = static_cast<float*>(o.out) + ((t0 + tok) * p.H + h) * D + slab;
-#pragma unroll
-        for (int u = 0; u < VT; ++u) *reinterpret_cast<f32x4*>(d + Lin<T>::template col<VT>(u, 4 * g)) = acc[u][it];
+        for (int u = 0; u < VT; ++u)
+          *reinterpret_cast<f32x4*>(static_cast<float*>(ro.out) + at + Lin<T>::template col<VT>(u, 4 * g)) = acc[u][it];
+      } else if constexpr (VT == 2) {
+        *reinterpret_cast<Frag*>(static_cast<T*>(ro.out) + at + 8 * g) = Lin<T>::state(acc[0][it], acc[1][it]);
       } else {
-        // outputs per value head, or per key head where each has one value head
-        T* d = static_cast<T*>(o.out) + ((t0 + tok) * p.H + h) * D + slab;
-        if constexpr (VT == 2 && sizeof(T) == 2) {
-          const Frag f = Lin<T>::state(acc[0][it], acc[1][it]);
-          *reinterpret_cast<Frag*>(d + 8 * g) = f;
-        } else {
-#pragma unroll
-          for (int u = 0; u < VT; ++u)
-            Lin<T>::store4(reinterpret_cast<char*>(d + Lin<T>::template col<VT>(u, 4 * g)), acc[u][it][0], acc[u][it][1],
-                           acc[u][it][2], acc[u][it][3]);
-        }
+        Lin<T>::store4(reinterpret_cast<char*>(static_cast<T*>(ro.out) + at + 4 * g), acc[0][it][0], acc[0][it][1], acc[0][it][2], acc[0][it][3]);
       }
+    };
+    if (n == kB) {
+#pragma unroll
+      for (int it = 0; it < TI; ++it) store(it);
+    } else {
+#pragma unroll
+      for (int it = 0; it < TI; ++it)
+        if (16 * it + q < n) store(it);
     }
     S.decay(em1);
     S.add(ys, zf, wz);
     if (odd) {
 #pragma unroll
       for (int u = 0; u < VT; ++u)
-        if (bad_s[slab + Lin<T>::template col<VT>(u, q)] < kB) {
+        if (first[u] < kB) {
 #pragma unroll
           for (int t = 0; t < D / 16; ++t)
 #pragma unroll
@@ -584,7 +633,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_lin_out(const L
         }
     }
   }
-  if (o.last && (REV ? sg.idx == 0 : sg.idx == sg.nseg - 1)) S.store(o.last + sh * (D * D), slab);
+  if (ro.last && (REV ? sg.idx == 0 : sg.idx == sg.nseg - 1)) S.store(ro.last + sh * (D * D), slab);
 }
 
 // Sum of the G value heads' shares of a key head's gradient, in head order
@@ -688,36 +737,42 @@ int states(const LinParams& p, bool backward, hipStream_t s) {
   return last_error();
 }
 
-template <typename T, int D>
-int fwd(const LinParams& p, hipStream_t s) {
-  const LinRole o = {p.q, p.k, p.v, p.o, p.ht, p.h0, p.st, 1, 1, 0, 0, 0, p.scale, p.scale, 1.f};
-  k_lin_out<T, D, false><<<unsigned(int64_t(p.NC) * p.H), 256, 0, s>>>(p, o);
+template <typename T, int D, bool REV, int TILES, int ROLES, int VT, bool OUT32>
+int out(const LinParams& p, const LinCall& o, hipStream_t s) {
+  k_lin_out<T, D, REV, TILES, ROLES, VT, OUT32><<<unsigned(int64_t(p.NC) * p.H), ROLES * (D / 16 / VT) * 64, 0, s>>>(p, o);
   return last_error();
 }
 
 template <typename T, int D>
+int fwd(const LinParams& p, hipStream_t s) {
+  constexpr int VT = 1;
+  const LinCall o = {{p.q, p.k, p.v}, {1, 1, 0}, {{p.o, p.ht, p.h0, p.st, 0, 1, 2, 0, p.scale, p.scale, 1.f}}};
+  return out<T, D, false, 3, 1, VT, false>(p, o, s);
+}
+
+template <typename T, int D>
 int bwd(const LinParams& p, hipStream_t s) {
-  const unsigned grid = unsigned(int64_t(p.NC) * p.H);
+  constexpr int VT = D / 64;
   const bool grouped = p.G > 1;
-  const LinRole q = {p.dO, p.v, p.k, grouped ? p.part : p.dq, nullptr, p.h0, p.st, 0, 0, 1, 1, grouped, p.scale, p.scale, 1.f};
-  const LinRole k = {p.v, p.dO, p.q, grouped ? p.part : p.dk, nullptr, p.dht, p.dst, 0, 0, 1, 1, grouped, p.scale, 1.f, p.scale};
-  const LinRole v = {p.k, p.q, p.dO, p.dv, p.dh0, p.dht, p.dst, 1, 1, 0, 0, 0, p.scale, 1.f, p.scale};
   const int64_t n8 = int64_t(p.T) * p.Hk * D / 8;
-  const unsigned sum = unsigned((n8 + 255) / 256);
-  k_lin_out<T, D, false><<<grid, 256, 0, s>>>(p, q);
-  if (const int e = last_error()) return e;
-  if (grouped && n8) {
-    k_lin_group<T><<<sum, 256, 0, s>>>(p.part, p.dq, n8, p.Hk, D, p.G);
-    if (const int e = last_error()) return e;
-  }
-  k_lin_out<T, D, true><<<grid, 256, 0, s>>>(p, k);
-  if (const int e = last_error()) return e;
-  if (grouped && n8) {
-    k_lin_group<T><<<sum, 256, 0, s>>>(p.part, p.dk, n8, p.Hk, D, p.G);
-    if (const int e = last_error()) return e;
-  }
-  k_lin_out<T, D, true><<<grid, 256, 0, s>>>(p, v);
-  return last_error();
+  auto sum = [&](void* dst) {
+    if (n8) k_lin_group<T><<<unsigned((n8 + 255) / 256), 256, 0, s>>>(p.part, dst, n8, p.Hk, D, p.G);
+    return last_error();
+  };
+  const LinRole q = {grouped ? p.part : p.dq, nullptr, p.h0, p.st, 0, 1, 2, 1, p.scale, p.scale, 1.f};
+  const LinCall oq = {{p.dO, p.v, p.k}, {0, 0, 1}, {q}};
+  if (const int e = grouped ? out<T, D, false, 3, 1, 1, true>(p, oq, s) : out<T, D, false, 3, 1, 1, false>(p, oq, s)) return e;
+  if (grouped)
+    if (const int e = sum(p.dq)) return e;
+  const LinRole k = {grouped ? p.part : p.dk, nullptr, p.dht, p.dst, 2, 3, 0, 1, p.scale, 1.f, p.scale};
+  const LinRole v = {p.dv, p.dh0, p.dht, p.dst, 1, 0, 3, 0, p.scale, 1.f, p.scale};
+  if (!grouped) return out<T, D, true, 4, 2, VT, false>(p, {{p.q, p.k, p.v, p.dO}, {1, 1, 0, 0}, {v, k}}, s);
+  LinRole k3 = k, v3 = v;
+  k3.x = 0, k3.y = 1, k3.z = 2;
+  v3.x = 0, v3.y = 1, v3.z = 2;
+  if (const int e = out<T, D, true, 3, 1, 1, true>(p, {{p.v, p.dO, p.q}, {0, 0, 1}, {k3}}, s)) return e;
+  if (const int e = sum(p.dk)) return e;
+  return out<T, D, true, 3, 1, 1, false>(p, {{p.k, p.q, p.dO}, {1, 1, 0}, {v3}}, s);
 }
 
 template <typename T, int D>
