@@ -18,6 +18,8 @@
 namespace gdr {
 namespace {
 
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
 // ---------------------------------------------------------------------------
 // fragments of a type: 16 bytes of each lane, KS elements of the contraction a step
 // ---------------------------------------------------------------------------
@@ -56,16 +58,16 @@ template <> struct Lin<bf16> {
     return __builtin_bit_cast(Frag, u32x4{lo.x, lo.y, hi.x, hi.y});
   }
   static __device__ __forceinline__ void store4(char* p, float a, float b, float c, float d) {
-    *reinterpret_cast<uint2*>(p) = pack4_bf16(a, b, c, d);
+    // as a vector: a struct's copy would lose the name of its array (see k_lin_out)
+    const uint2 v = pack4_bf16(a, b, c, d);
+    *reinterpret_cast<u32x2*>(p) = u32x2{v.x, v.y};
   }
   static constexpr int B = 64;       // tokens per block
-  // nonzero where one of the eight has all exponent bits set
-  static __device__ __forceinline__ uint32_t bad(Frag f) {
-    const u32x4 u = __builtin_bit_cast(u32x4, f);
-    uint32_t b = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) b |= (u[i] & 0x7f807f80u) + 0x00800080u;
-    return b & 0x80008000u;
+  // whether a lane of the wave holds an infinity or a NaN: times zero, they alone are not zero
+  static __device__ __forceinline__ bool any_bad(const Frag (&f)[2]) {
+    const Frag none = {};
+    const f32x4 x = mma(f[1], none, mma(f[0], none, zero4()));
+    return __any(!(x[0] + x[1] + (x[2] + x[3]) == 0.f));
   }
   static __device__ __forceinline__ float get(Frag f, int e) {
     const u32x4 u = __builtin_bit_cast(u32x4, f);
@@ -114,11 +116,12 @@ template <> struct Lin<float> {
     *reinterpret_cast<f32x4*>(p) = f32x4{a, b, c, d};
   }
   static constexpr int B = 32;
-  static __device__ __forceinline__ uint32_t bad(Frag f) {
+  static __device__ __forceinline__ bool any_bad(const Frag (&f)[2]) {
     uint32_t b = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) b |= (__float_as_uint(f[i]) & 0x7f800000u) + 0x00800000u;
-    return b & 0x80000000u;
+    for (int i = 0; i < 4; ++i)
+      b |= ((__float_as_uint(f[0][i]) & 0x7f800000u) + 0x00800000u) | ((__float_as_uint(f[1][i]) & 0x7f800000u) + 0x00800000u);
+    return __any(b >> 31);
   }
   static __device__ __forceinline__ float get(Frag f, int e) { return f[e]; }
   static __device__ __forceinline__ Frag without(Frag f, uint32_t drop) {
@@ -140,6 +143,17 @@ __device__ __forceinline__ LinSeg seg_at(const LinParams& p, int s) {
   r.t0 = r.seq * p.dense_T + r.idx * p.seg;
   r.len = min(p.seg, p.dense_T - r.idx * p.seg);
   return r;
+}
+
+// Segment and head of a workgroup: the heads of a segment one after the other, since their
+// rows lie side by side.  Value heads that share q and k go to one XCD (see chunk_head_at).
+__device__ __forceinline__ void place_of(const LinParams& p, int id, int& c, int& h) {
+  if (p.G > 1) {
+    chunk_head_at(p, id, c, h);
+  } else {
+    c = id / p.H;
+    h = id % p.H;
+  }
 }
 
 // lambda in base-2 units.  A log decay of -inf counts as -1e30: c^0 is 1 and any other
@@ -222,42 +236,46 @@ struct State {
 #pragma unroll
         for (int r = 0; r < 4; ++r) s[t][u][r] = fmaf(em1, s[t][u][r], s[t][u][r]);
   }
-  // S^T += y^T (w z): the weighted z in two bf16 parts (16 bits of significand), since the
-  // state is held and returned in fp32
-  __device__ __forceinline__ void add(const char* y, const typename Lin<T>::Frag (&z)[JS][VT],
-                                      const float (&w)[JS][Lin<T>::E]) {
+  // S^T += y^T (w z).  The weighted z of bf16 tensors is rounded to bf16 (part 0).  What that
+  // leaves is two bf16 parts more (24 bits of significand together) for states that are
+  // returned or that another segment starts from, in fp32.  A state that only meets x within
+  // the segment is rounded to bf16 there itself.
+  typedef typename Lin<T>::Frag Frag;
+  static __device__ __forceinline__ Frag weighted(Frag z, const float (&w)[Lin<T>::E], int part) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) z[e] *= w[e];
+      return z;
+    } else {
+      float x[8];
+      IO<bf16>::unpack8(__builtin_bit_cast(u32x4, z), x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[e] *= w[e];
+        if (part > 0) x[e] = lo_part(x[e]);
+        if (part > 1) x[e] = lo_part(x[e]);
+      }
+      return Lin<T>::state(f32x4{x[0], x[1], x[2], x[3]}, f32x4{x[4], x[5], x[6], x[7]});
+    }
+  }
+  // parts FROM .. TO - 1
+  template <int FROM, int TO>
+  __device__ __forceinline__ void add(const char* y, const Frag (&z)[JS][VT], const float (&w)[JS][Lin<T>::E]) {
+    constexpr int N = sizeof(T) == 4 ? 1 : TO - FROM;
 #pragma unroll
     for (int js = 0; js < JS; ++js) {
-      typename Lin<T>::Frag hi[VT], lo[VT];
+      Frag x[N][VT];
 #pragma unroll
-      for (int u = 0; u < VT; ++u) {
-        if constexpr (sizeof(T) == 2) {
-          const u32x4 raw = __builtin_bit_cast(u32x4, z[js][u]);
-          float x[8];
-          IO<bf16>::unpack8(raw, x);
+      for (int a = 0; a < N; ++a)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] *= w[js][e];
-          const uint2 a = pack4_bf16(x[0], x[1], x[2], x[3]), b = pack4_bf16(x[4], x[5], x[6], x[7]);
-          const u32x4 h = {a.x, a.y, b.x, b.y};
-          hi[u] = __builtin_bit_cast(bf16x8, h);
-          float y8[8];
-          IO<bf16>::unpack8(h, y8);
-          const uint2 c = pack4_bf16(x[0] - y8[0], x[1] - y8[1], x[2] - y8[2], x[3] - y8[3]);
-          const uint2 d = pack4_bf16(x[4] - y8[4], x[5] - y8[5], x[6] - y8[6], x[7] - y8[7]);
-          lo[u] = __builtin_bit_cast(bf16x8, u32x4{c.x, c.y, d.x, d.y});
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) hi[u][e] = z[js][u][e] * w[js][e];
-        }
-      }
+        for (int u = 0; u < VT; ++u) x[a][u] = weighted(z[js][u], w[js], FROM + a);
 #pragma unroll
       for (int t = 0; t < KT; ++t) {
-        const typename Lin<T>::Frag a = Lin<T>::template kc<D>(y, 16 * t, js * Lin<T>::KS);
+        const Frag f = Lin<T>::template kc<D>(y, 16 * t, js * Lin<T>::KS);
 #pragma unroll
-        for (int u = 0; u < VT; ++u) {
-          Lin<T>::mul(a, hi[u], s[t][u]);
-          if constexpr (sizeof(T) == 2) Lin<T>::mul(a, lo[u], s[t][u]);
-        }
+        for (int a = 0; a < N; ++a)
+#pragma unroll
+          for (int u = 0; u < VT; ++u) Lin<T>::mul(f, x[a][u], s[t][u]);
       }
     }
   }
@@ -306,9 +324,9 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_lin_local(const
   constexpr int kB = Lin<T>::B, TB = kB * D * int(sizeof(T)), VT = D / 64, JS = kB / Lin<T>::KS;
   __shared__ __attribute__((aligned(1024))) char ys[TB], zs[TB];
   int c, h;
-  chunk_head_at(p, int(blockIdx.x), c, h);
+  place_of(p, int(blockIdx.x), c, h);
   const LinSeg sg = seg_at(p, c);
-  if (REV ? sg.idx == 0 : sg.idx == sg.nseg - 1) return;   // nothing follows it
+  if (REV ? sg.idx == 0 : sg.idx == sg.nseg - 1) return;   // nothing starts from it
   const int yH = p.Hk, yh = h / p.G;
   const void *y = REV ? p.q : p.k, *z = REV ? p.dO : p.v;
   const float l2 = decay2(p, h), wscale = REV ? p.scale : 1.f;
@@ -343,7 +361,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_lin_local(const
 #pragma unroll
       for (int u = 0; u < VT; ++u) zf[js][u] = Lin<T>::template slab<D, VT>(zs, slab, u, js * Lin<T>::KS);
     S.decay(em1);
-    S.add(ys, zf, w);
+    S.template add<0, 3>(ys, zf, w);
   }
   S.store((REV ? p.dst : p.st) + (int64_t(c) * p.H + h) * (D * D), slab);
 }
@@ -353,12 +371,11 @@ template <int D, bool REV>
 __global__ __launch_bounds__(256) void k_lin_carry(const LinParams p) {
   constexpr int PER = D * D / 4 / 256;   // workgroups a state
   const int part = blockIdx.x % PER, h = blockIdx.x / PER % p.H, n = blockIdx.x / PER / p.H;
-  int row0, nseg, len;
+  int row0, nseg, len;                   // of the last segment
   if (p.dense_T < 0) {
     row0 = p.row0[n];
     nseg = p.row0[n + 1] - row0;
-    const LinSeg last = p.tab[row0 + nseg - 1];
-    len = last.len;
+    len = p.tab[row0 + nseg - 1].len;
   } else {
     nseg = p.dense_nseg;
     row0 = n * nseg;
@@ -394,112 +411,162 @@ __global__ __launch_bounds__(256) void k_lin_carry(const LinParams p) {
 // ---------------------------------------------------------------------------
 // outputs
 // ---------------------------------------------------------------------------
-// What one group of waves computes: out from the tiles x, y, z of a block.
+// out from the tensors x, y, z
 struct LinRole {
+  const void *x, *y, *z;
   void* out;
   float* last;            // state after the last segment (before the first, backwards), or NULL
   const float* first;     // state of the whole sequence's start (end, backwards), or NULL
   const float* st;        // states of the segments
-  int32_t x, y, z;        // its tensors among those of the call
+  int32_t xk, yk, zk;     // 1: the tensor has Hk heads, 0: H
   int32_t transposed;     // the state's memory is [y channel][z channel]
   float pair, inter, add; // factors of the pairs' product, of S x, of the state's update
-};
-struct LinCall {
-  const void* t[4];       // tensors
-  int32_t shared[4];      // 1: with Hk heads, 0: with H
-  LinRole r[2];
+  int32_t flip;           // last segment first: what the kernel before has read last is still near
 };
 
-// TILES tensors are copied to LDS block by block, one block ahead; ROLES groups of
-// D / 16 / VT waves work on them.  OUT32: out is fp32 (a value head's share of the
-// gradient of a grouped q or k).
-template <typename T, int D, bool REV, int TILES, int ROLES, int VT, bool OUT32>
-__global__ __launch_bounds__(ROLES * (D / 16 / VT) * 64, ROLES * (D / 16 / VT) / 4) void k_lin_out(const LinParams p, const LinCall o) {
+// A wave holds 16 columns of S^T (channels of z) in registers.  The tiles of x, y and z are
+// copied to LDS one block ahead.  OUT32: out is fp32 (a value head's share of the gradient of
+// a grouped q or k).
+template <typename T, int D, bool REV, bool OUT32>
+__global__ __launch_bounds__(D * 4, 2) void k_lin_out(const LinParams p, const LinRole o) {
   typedef typename Lin<T>::Frag Frag;
   constexpr int kB = Lin<T>::B, KS = Lin<T>::KS, JS = kB / KS, E = Lin<T>::E, TI = kB / 16;
-  constexpr int RW = D / 16 / VT, NW = ROLES * RW;                     // waves of a role, of the workgroup
+  constexpr int NW = D / 16;                                               // waves
   constexpr int ROW = D * int(sizeof(T)), TB = kB * ROW, PR = ROW / 16;   // bytes of a row and a tile, pieces of a row
-  constexpr int LPT = TB / 1024 / NW, RPL = 1024 / ROW;                // a wave's 1 KB loads of a tile, rows of a load
-  constexpr int NPAIR = TI * TI / RW > 0 ? TI * TI / RW : 1;           // tiles of pairs of a wave
-  constexpr int STORES = TI * (VT == 2 && sizeof(T) == 2 && !OUT32 ? 1 : VT);   // of a wave and block
-  static_assert(LPT >= 1 && TB / 1024 % NW == 0 && (NW * RPL) % 16 == 0, "a load's rows turn alike");
-  __shared__ __attribute__((aligned(1024))) char tiles[2][TILES][TB];
-  __shared__ __attribute__((aligned(1024))) char pairs[ROLES][kB * kB * int(sizeof(T))];
+  constexpr int LPT = TB / 1024 / NW, RPL = 1024 / ROW;                    // a wave's 1 KB loads of a tile, rows of a load
+  constexpr int NPAIR = TI * TI / NW > 0 ? TI * TI / NW : 1, JSTEP = NW / TI;   // a wave's tiles of pairs
+  constexpr int STORES = TI;                                               // of a wave and block
+  constexpr int PB = kB * kB * int(sizeof(T));
+  static_assert(LPT >= 1 && TB / 1024 % NW == 0 && (NW * RPL) % 16 == 0, "the rows of a wave's loads turn alike");
+  // Arrays of their own, each named where it is used: of one array with two halves the
+  // compiler takes it that a read may meet the loads on their way, and waits for them.
+  __shared__ __attribute__((aligned(1024))) char tiles0[3][TB], tiles1[3][TB], pairs0[PB], pairs1[PB];
   int c, h;
-  chunk_head_at(p, int(blockIdx.x), c, h);
+  place_of(p, int(o.flip ? gridDim.x - 1 - blockIdx.x : blockIdx.x), c, h);
   const LinSeg sg = seg_at(p, c);
-  const int l = lane_id(), q = l & 15, g = l >> 4, wave = __builtin_amdgcn_readfirstlane(wave_id());
-  const int role = ROLES == 1 ? 0 : wave / RW, w = wave % RW;
-  const LinRole& ro = o.r[role];
-  const int slab = w * 16 * VT, nb = (sg.len + kB - 1) / kB;
+  const int l = lane_id(), q = l & 15, g = l >> 4, w = __builtin_amdgcn_readfirstlane(wave_id());
+  const int slab = w * 16, nb = (sg.len + kB - 1) / kB;
   const float l2 = decay2(p, h);
   const int64_t sh = int64_t(sg.seq) * p.H + h;
+  auto tokens = [&](int i) {   // of the walk's i-th block: first and number
+    const int b = REV ? nb - 1 - i : i;
+    return make_int2(b * kB, min(kB, sg.len - b * kB));
+  };
   // A lane's row and place in a load, and the piece that belongs there
-  const int lrow = wave * RPL + l / PR, piece = Lin<T>::template off<D>(lrow & 15, 0) % ROW / 16 ^ (l % PR);
-  auto load = [&](int i) {
-    const int b = REV ? nb - 1 - i : i, n = min(kB, sg.len - b * kB);
-    const int64_t t0 = sg.t0 + int64_t(b) * kB;
+  const int lrow = w * RPL + l / PR, piece = (Lin<T>::template off<D>(lrow & 15, 0) % ROW / 16) ^ (l % PR);
+  auto load = [&](int i, auto& tiles) {
+    const int2 tn = tokens(i);
+    const int64_t t0 = sg.t0 + tn.x;
 #pragma unroll
-    for (int m = 0; m < TILES; ++m) {
-      const int heads = o.shared[m] ? p.Hk : p.H, head = o.shared[m] ? h / p.G : h;
-      const char* src = static_cast<const char*>(o.t[m]) + (t0 * heads + head) * ROW;
+    for (int m = 0; m < 3; ++m) {
+      const bool shared = m == 0 ? o.xk : m == 1 ? o.yk : o.zk;
+      const int heads = shared ? p.Hk : p.H, head = shared ? h / p.G : h;
+      const char* src = static_cast<const char*>(m == 0 ? o.x : m == 1 ? o.y : o.z) + (t0 * heads + head) * ROW;
 #pragma unroll
       for (int a = 0; a < LPT; ++a) {
         // rows past the end repeat the last one; they are cleared when they have come
-        const int row = min(a * NW * RPL + lrow, n - 1);
-        dma16(src + int64_t(row) * heads * ROW + 16 * piece, tiles[i & 1][m] + (a * NW + wave) * 1024);
+        const int row = min(a * NW * RPL + lrow, tn.y - 1);
+        dma16(src + int64_t(row) * heads * ROW + 16 * piece, tiles[m] + (a * NW + w) * 1024);
       }
     }
   };
-  if (nb) load(0);
-  State<T, D, VT> S;
-  const bool start = REV ? sg.idx == sg.nseg - 1 : sg.idx == 0;
-  if (!start) S.load(ro.st + (int64_t(c) * p.H + h) * (D * D), ro.transposed, slab);
-  else if (ro.first) S.load(ro.first + sh * (D * D), ro.transposed, slab);
+  if (nb) load(0, tiles0);
+  State<T, D, 1> S;
+  const bool start = REV ? sg.idx == sg.nseg - 1 : sg.idx == 0, end = REV ? sg.idx == 0 : sg.idx == sg.nseg - 1;
+  const bool exact = end && o.last;
+  if (!start) S.load(o.st + (int64_t(c) * p.H + h) * (D * D), o.transposed, slab);
+  else if (o.first) S.load(o.first + sh * (D * D), o.transposed, slab);
   else S.zero();
-  // The wave's tiles of pairs: tokens i of tile w % TI, tokens j of w / TI and every RW / TI-th
+  // The wave's tiles of pairs: tokens i of tile w % TI, tokens j of w / TI and every JSTEP-th
   // on, and the decay between them
   const int it0 = w % TI, jt0 = w / TI;
-  constexpr int JSTEP = RW / TI > 0 ? RW / TI : 1;
   float near[NPAIR][4];
 #pragma unroll
   for (int a = 0; a < NPAIR; ++a)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int d = (16 * it0 + q) - (16 * (jt0 + a * JSTEP) + 4 * g + r), n = REV ? -d : d;
-      near[a][r] = n >= 0 ? ro.pair * fast_exp2(float(n) * l2) : 0.f;
+      near[a][r] = n >= 0 ? o.pair * fast_exp2(float(n) * l2) : 0.f;
     }
   // the pairs of later tokens are never written again
-  char* const ps = pairs[role];
-  for (int i = w * 64 + l; i < kB * kB * int(sizeof(T)) / 16; i += RW * 64) *reinterpret_cast<u32x4*>(ps + 16 * i) = u32x4{0, 0, 0, 0};
+  for (int i = threadIdx.x; i < PB / 16; i += NW * 64) {
+    *reinterpret_cast<u32x4*>(pairs0 + 16 * i) = u32x4{0, 0, 0, 0};
+    *reinterpret_cast<u32x4*>(pairs1 + 16 * i) = u32x4{0, 0, 0, 0};
+  }
   float wz[JS][E], far[TI], em1 = 0.f;
   int wn = -1;
-  for (int i = 0; i < nb; ++i) {
-    const int b = REV ? nb - 1 - i : i, n = min(kB, sg.len - b * kB);
-    const int64_t t0 = sg.t0 + int64_t(b) * kB;
-    // The block has come.  Behind its loads a wave has issued the stores of the block before
-    // alone, STORES of them unless that block was not whole.
-    if (wn == kB) wait_vm<STORES>();
-    else wait_vm<0>();
+  // here and not at the state's first use, where the compiler would wait for every load that
+  // is on its way, in each turn of the loop
+  wait_vm<0>();
+  // A block's sums, its z and where its infinities and NaN begin, until its pairs are there
+  f32x4 acc[TI];
+  Frag zf[JS];
+  bool odd = false;
+  int bad_from = kB;
+#pragma unroll
+  for (int it = 0; it < TI; ++it) acc[it] = zero4();
+#pragma unroll
+  for (int js = 0; js < JS; ++js) zf[js] = Frag{};
+  // The pairs' part of the walk's i-th block, and its output; block -1 has none
+  auto finish = [&](int i, auto& ps) {
+#pragma unroll
+    for (int js = 0; js < JS; ++js)
+#pragma unroll
+      for (int it = 0; it < TI; ++it) {
+        if (REV ? (js + 1) * KS <= 16 * it : js * KS >= 16 * (it + 1)) continue;
+        Lin<T>::mul(zf[js], Lin<T>::template rk<kB>(ps, 16 * it, js * KS), acc[it]);
+      }
+    if (odd) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int from = __shfl(bad_from, 4 * g + r, 64);
+#pragma unroll
+        for (int it = 0; it < TI; ++it)
+          if ((REV ? kB - 1 - (16 * it + q) : 16 * it + q) >= from) acc[it][r] = __builtin_nanf("");
+      }
+    }
+    // The buffer ends behind the block's last token, and is empty for block -1: what lies
+    // further on is dropped, so that every turn has the same number of stores.
+    constexpr int OB = OUT32 ? 4 : int(sizeof(T));
+    const int2 tn = tokens(max(i, 0));
+    const uint32_t pitch = uint32_t(p.H) * D * OB;
+    const __amdgpu_buffer_rsrc_t dst = __builtin_amdgcn_make_buffer_rsrc(
+        static_cast<char*>(o.out) + ((int64_t(sg.t0) + tn.x) * p.H + h) * (D * OB), 0, i < 0 ? 0 : int(uint32_t(tn.y - 1) * pitch + D * OB), 0x00027000);
+#pragma unroll
+    for (int it = 0; it < TI; ++it) {
+      const uint32_t at = uint32_t(16 * it + q) * pitch + slab * OB;
+      if constexpr (OB == 4) {
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[it]), dst, at + 16 * g, 0, 0);
+      } else {
+        const uint2 v = pack4_bf16(acc[it][0], acc[it][1], acc[it][2], acc[it][3]);
+        __builtin_amdgcn_raw_buffer_store_b64(u32x2{v.x, v.y}, dst, at + 8 * g, 0, 0);
+      }
+    }
+  };
+  auto turn = [&](int i, auto& tiles, auto& next, auto& ps, auto& ps_before) {
+    // The block has come (behind its loads a wave has issued the stores of a block alone), and
+    // so have the pairs of the block before.
+    wait_vm<STORES>();
     chain_barrier();
+    if (i + 1 < nb) load(i + 1, next);
+    finish(i - 1, ps_before);
+    const int n = tokens(i).y;
     if (n != wn) {
-      state_weights<T, REV>(l2, n, ro.add, wz);
+      state_weights<T, REV>(l2, n, o.add, wz);
       em1 = decay_m1(l2, n);
 #pragma unroll
       for (int it = 0; it < TI; ++it) {
         const int m = REV ? n - 1 - (16 * it + q) : 16 * it + q + 1;
-        far[it] = m >= 0 ? ro.inter * fast_exp2(float(m) * l2) : 0.f;
+        far[it] = m >= 0 ? o.inter * fast_exp2(float(m) * l2) : 0.f;
       }
       wn = n;
     }
-    if (i + 1 < nb) load(i + 1);
     if (n < kB) {
-      for (int m = 0; m < TILES; ++m)
-        for (int a = threadIdx.x; a < (kB - n) * PR; a += NW * 64)
-          *reinterpret_cast<u32x4*>(tiles[i & 1][m] + n * ROW + 16 * a) = u32x4{0, 0, 0, 0};
+      for (int m = 0; m < 3; ++m)
+        for (int a = threadIdx.x; a < (kB - n) * PR; a += NW * 64) *reinterpret_cast<u32x4*>(tiles[m] + n * ROW + 16 * a) = u32x4{0, 0, 0, 0};
       chain_barrier();
     }
-    const char *const xs = tiles[i & 1][ro.x], *const ys = tiles[i & 1][ro.y], *const zs = tiles[i & 1][ro.z];
+    const char *const xs = tiles[0], *const ys = tiles[1], *const zs = tiles[2];
     // pairs: P[i][j] = c^|i-j| (x_i . y_j)
     if (jt0 < TI) {
       Frag xf[D / KS];
@@ -521,119 +588,65 @@ __global__ __launch_bounds__(ROLES * (D / 16 / VT) * 64, ROLES * (D / 16 / VT) /
         Lin<T>::store4(ps + Lin<T>::template off<kB>(16 * it0 + q, 16 * jt + 4 * g), a[0], a[1], a[2], a[3]);
       }
     }
-    Frag zf[JS][VT];
-    uint32_t bad = 0;
 #pragma unroll
-    for (int js = 0; js < JS; ++js)
-#pragma unroll
-      for (int u = 0; u < VT; ++u) {
-        zf[js][u] = Lin<T>::template slab<D, VT>(zs, slab, u, js * KS);
-        bad |= Lin<T>::bad(zf[js][u]);
-      }
+    for (int js = 0; js < JS; ++js) zf[js] = Lin<T>::template slab<D, 1>(zs, slab, 0, js * KS);
     // Infinities and NaN in z: a zero pair times one would reach tokens before it, so the
-    // products take zeros in their place, and what comes from that token on is NaN: first[u],
-    // in the order of the walk, for column u of the lane's.
-    int first[VT];
-    const bool odd = __any(bad != 0);
+    // products take zeros in their place, and what comes from that token on is NaN: bad_from, in
+    // the order of the walk, for the lane's column.
+    odd = Lin<T>::any_bad(zf);
     if (odd) {
+      bad_from = kB;
 #pragma unroll
-      for (int u = 0; u < VT; ++u) {
-        first[u] = kB;
+      for (int js = 0; js < JS; ++js) {
+        uint32_t drop = 0;
 #pragma unroll
-        for (int js = 0; js < JS; ++js) {
-          uint32_t drop = 0;
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const int j = js * KS + E * g + e;
-            if (!(fabsf(Lin<T>::get(zf[js][u], e)) <= 3.4028235e38f)) {
-              drop |= 1u << e;
-              first[u] = min(first[u], REV ? kB - 1 - j : j);
-            }
+        for (int e = 0; e < E; ++e) {
+          const int j = js * KS + E * g + e;
+          if (!(fabsf(Lin<T>::get(zf[js], e)) <= 3.4028235e38f)) {
+            drop |= 1u << e;
+            bad_from = min(bad_from, REV ? kB - 1 - j : j);
           }
-          zf[js][u] = Lin<T>::without(zf[js][u], drop);
         }
-        first[u] = min(first[u], __shfl_xor(first[u], 16, 64));
-        first[u] = min(first[u], __shfl_xor(first[u], 32, 64));
+        zf[js] = Lin<T>::without(zf[js], drop);
       }
+      bad_from = min(bad_from, __shfl_xor(bad_from, 16, 64));
+      bad_from = min(bad_from, __shfl_xor(bad_from, 32, 64));
     }
-    chain_barrier();
-    f32x4 acc[VT][TI];
 #pragma unroll
-    for (int u = 0; u < VT; ++u)
-#pragma unroll
-      for (int it = 0; it < TI; ++it) acc[u][it] = zero4();
+    for (int it = 0; it < TI; ++it) acc[it] = zero4();
 #pragma unroll
     for (int ks = 0; ks < D / KS; ++ks) {
-      Frag a[VT];
+      const Frag a = Lin<T>::state(S.s[ks * KS / 16][0], S.s[ks * KS / 16 + (KS == 32)][0]);
 #pragma unroll
-      for (int u = 0; u < VT; ++u) a[u] = Lin<T>::state(S.s[ks * KS / 16][u], S.s[ks * KS / 16 + (KS == 32)][u]);
-#pragma unroll
-      for (int it = 0; it < TI; ++it) {
-        const Frag f = Lin<T>::template rk_state<D>(xs, 16 * it, ks * KS);
-#pragma unroll
-        for (int u = 0; u < VT; ++u) Lin<T>::mul(a[u], f, acc[u][it]);
-      }
+      for (int it = 0; it < TI; ++it) Lin<T>::mul(a, Lin<T>::template rk_state<D>(xs, 16 * it, ks * KS), acc[it]);
     }
 #pragma unroll
-    for (int u = 0; u < VT; ++u)
+    for (int it = 0; it < TI; ++it)
 #pragma unroll
-      for (int it = 0; it < TI; ++it)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[u][it][r] *= far[it];
-#pragma unroll
-    for (int js = 0; js < JS; ++js)
-#pragma unroll
-      for (int it = 0; it < TI; ++it) {
-        if (REV ? (js + 1) * KS <= 16 * it : js * KS >= 16 * (it + 1)) continue;
-        const Frag f = Lin<T>::template rk<kB>(ps, 16 * it, js * KS);
-#pragma unroll
-        for (int u = 0; u < VT; ++u) Lin<T>::mul(zf[js][u], f, acc[u][it]);
-      }
-    if (odd) {
-#pragma unroll
-      for (int u = 0; u < VT; ++u)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int from = __shfl(first[u], 4 * g + r, 64);
-#pragma unroll
-          for (int it = 0; it < TI; ++it)
-            if ((REV ? kB - 1 - (16 * it + q) : 16 * it + q) >= from) acc[u][it][r] = __builtin_nanf("");
-        }
-    }
-    auto store = [&](int it) {
-      const int64_t at = ((t0 + 16 * it + q) * p.H + h) * D + slab;
-      if constexpr (OUT32 || sizeof(T) == 4) {
-#pragma unroll
-        for (int u = 0; u < VT; ++u)
-          *reinterpret_cast<f32x4*>(static_cast<float*>(ro.out) + at + Lin<T>::template col<VT>(u, 4 * g)) = acc[u][it];
-      } else if constexpr (VT == 2) {
-        *reinterpret_cast<Frag*>(static_cast<T*>(ro.out) + at + 8 * g) = Lin<T>::state(acc[0][it], acc[1][it]);
-      } else {
-        Lin<T>::store4(reinterpret_cast<char*>(static_cast<T*>(ro.out) + at + 4 * g), acc[0][it][0], acc[0][it][1], acc[0][it][2], acc[0][it][3]);
-      }
-    };
-    if (n == kB) {
-#pragma unroll
-      for (int it = 0; it < TI; ++it) store(it);
-    } else {
-#pragma unroll
-      for (int it = 0; it < TI; ++it)
-        if (16 * it + q < n) store(it);
-    }
+      for (int r = 0; r < 4; ++r) acc[it][r] *= far[it];
     S.decay(em1);
-    S.add(ys, zf, wz);
-    if (odd) {
+    Frag zv[JS][1];
 #pragma unroll
-      for (int u = 0; u < VT; ++u)
-        if (first[u] < kB) {
+    for (int js = 0; js < JS; ++js) zv[js][0] = zf[js];
+    S.template add<0, 1>(ys, zv, wz);
+    if (sizeof(T) == 2 && exact) S.template add<1, 3>(ys, zv, wz);
+    if (odd && bad_from < kB) {
 #pragma unroll
-          for (int t = 0; t < D / 16; ++t)
+      for (int t = 0; t < D / 16; ++t)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) S.s[t][u][r] = __builtin_nanf("");
-        }
+        for (int r = 0; r < 4; ++r) S.s[t][0][r] = __builtin_nanf("");
     }
+  };
+  for (int i = 0; i < nb; i += 2) {
+    turn(i, tiles0, tiles1, pairs0, pairs1);
+    if (i + 1 < nb) turn(i + 1, tiles1, tiles0, pairs1, pairs0);
   }
-  if (ro.last && (REV ? sg.idx == 0 : sg.idx == sg.nseg - 1)) S.store(ro.last + sh * (D * D), slab);
+  if (nb) {
+    chain_barrier();
+    if (nb & 1) finish(nb - 1, pairs0);
+    else finish(nb - 1, pairs1);
+  }
+  if (exact) S.store(o.last + sh * (D * D), slab);
 }
 
 // Sum of the G value heads' shares of a key head's gradient, in head order
@@ -737,42 +750,39 @@ int states(const LinParams& p, bool backward, hipStream_t s) {
   return last_error();
 }
 
-template <typename T, int D, bool REV, int TILES, int ROLES, int VT, bool OUT32>
-int out(const LinParams& p, const LinCall& o, hipStream_t s) {
-  k_lin_out<T, D, REV, TILES, ROLES, VT, OUT32><<<unsigned(int64_t(p.NC) * p.H), ROLES * (D / 16 / VT) * 64, 0, s>>>(p, o);
+template <typename T, int D, bool REV, bool OUT32>
+int out(const LinParams& p, const LinRole& o, hipStream_t s) {
+  k_lin_out<T, D, REV, OUT32><<<unsigned(int64_t(p.NC) * p.H), D * 4, 0, s>>>(p, o);
   return last_error();
 }
 
 template <typename T, int D>
 int fwd(const LinParams& p, hipStream_t s) {
-  constexpr int VT = 1;
-  const LinCall o = {{p.q, p.k, p.v}, {1, 1, 0}, {{p.o, p.ht, p.h0, p.st, 0, 1, 2, 0, p.scale, p.scale, 1.f}}};
-  return out<T, D, false, 3, 1, VT, false>(p, o, s);
+  return out<T, D, false, false>(p, {p.q, p.k, p.v, p.o, p.ht, p.h0, p.st, 1, 1, 0, 0, p.scale, p.scale, 1.f, 1}, s);
 }
 
 template <typename T, int D>
 int bwd(const LinParams& p, hipStream_t s) {
-  constexpr int VT = D / 64;
   const bool grouped = p.G > 1;
   const int64_t n8 = int64_t(p.T) * p.Hk * D / 8;
   auto sum = [&](void* dst) {
     if (n8) k_lin_group<T><<<unsigned((n8 + 255) / 256), 256, 0, s>>>(p.part, dst, n8, p.Hk, D, p.G);
     return last_error();
   };
-  const LinRole q = {grouped ? p.part : p.dq, nullptr, p.h0, p.st, 0, 1, 2, 1, p.scale, p.scale, 1.f};
-  const LinCall oq = {{p.dO, p.v, p.k}, {0, 0, 1}, {q}};
-  if (const int e = grouped ? out<T, D, false, 3, 1, 1, true>(p, oq, s) : out<T, D, false, 3, 1, 1, false>(p, oq, s)) return e;
-  if (grouped)
+  LinRole q = {p.dO, p.v, p.k, p.dq, nullptr, p.h0, p.st, 0, 0, 1, 1, p.scale, p.scale, 1.f, 1};
+  LinRole k = {p.v, p.dO, p.q, p.dk, nullptr, p.dht, p.dst, 0, 0, 1, 1, p.scale, 1.f, p.scale, 0};
+  const LinRole v = {p.k, p.q, p.dO, p.dv, p.dh0, p.dht, p.dst, 1, 1, 0, 0, p.scale, 1.f, p.scale, 1};
+  if (grouped) {
+    q.out = k.out = p.part;
+    if (const int e = out<T, D, false, true>(p, q, s)) return e;
     if (const int e = sum(p.dq)) return e;
-  const LinRole k = {grouped ? p.part : p.dk, nullptr, p.dht, p.dst, 2, 3, 0, 1, p.scale, 1.f, p.scale};
-  const LinRole v = {p.dv, p.dh0, p.dht, p.dst, 1, 0, 3, 0, p.scale, 1.f, p.scale};
-  if (!grouped) return out<T, D, true, 4, 2, VT, false>(p, {{p.q, p.k, p.v, p.dO}, {1, 1, 0, 0}, {v, k}}, s);
-  LinRole k3 = k, v3 = v;
-  k3.x = 0, k3.y = 1, k3.z = 2;
-  v3.x = 0, v3.y = 1, v3.z = 2;
-  if (const int e = out<T, D, true, 3, 1, 1, true>(p, {{p.v, p.dO, p.q}, {0, 0, 1}, {k3}}, s)) return e;
-  if (const int e = sum(p.dk)) return e;
-  return out<T, D, true, 3, 1, 1, false>(p, {{p.k, p.q, p.dO}, {1, 1, 0}, {v3}}, s);
+    if (const int e = out<T, D, true, true>(p, k, s)) return e;
+    if (const int e = sum(p.dk)) return e;
+  } else {
+    if (const int e = out<T, D, false, false>(p, q, s)) return e;
+    if (const int e = out<T, D, true, false>(p, k, s)) return e;
+  }
+  return out<T, D, true, false>(p, v, s);
 }
 
 template <typename T, int D>
