@@ -367,9 +367,8 @@ gdr_status gdr_norm_bwd(const gdr_norm_shape* shape, const void* r, const float*
  * positive one is taken as it stands as long as e^(lambda n) stays in the fp32
  * range for every n up to the longest sequence.
  * States, products and sums are fp32.  With bf16 tensors the products of pairs of
- * tokens, the states and what a run of tokens adds to its state are rounded to bf16
- * once where they are multiplied with bf16 tensors; states that are returned, or that
- * a run starts from, are not.  An infinity or NaN at a token reaches no token before it (after
+ * tokens and the states are rounded to bf16 once where they are multiplied with
+ * bf16 tensors; the states themselves, returned or not, are not.  An infinity or NaN at a token reaches no token before it (after
  * it, in the gradients of k and v) and no other sequence; from there on, what the
  * formulas make infinite or NaN is infinite or NaN, not always the same of the two.
  * GDR_EUNSUPPORTED from 2^30 tokens B T or 2^16 heads on, and from 2^20 blocks of 64

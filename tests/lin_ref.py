@@ -3,11 +3,10 @@ CPU, with a bound of what the library's arithmetic may add.
 
 U = 2^-24 is half a step of fp32, HALF (layer_ref) half a step of a type.  Blocks are 64
 tokens from each sequence's start.  With bf16 tensors the library rounds to bf16, by half
-a step (2^-8) each, the pairs' products within a block, the state at a block's start where
-it meets the query, and what has been added to that state since its segment began (segments
-are whole blocks of a sequence, so at most: since the sequence began); what it adds to a
-state that is returned is in three bf16 parts (24 bits, as fp32).  Everything else is fp32:
-a product over D channels or 64 tokens adds one U a term, decays are exponentials of
+a step (2^-8) each, the pairs' products within a block and the state at a block's start
+where it meets the query.  What it adds to a state is in two bf16 parts (2^-16 is left),
+in three (24 bits, as fp32) where the state is returned.  Everything else is fp32: a
+product over D channels or 64 tokens adds one U a term, decays are exponentials of
 n lambda (the product rounds by U n |lambda|, the exponential by a few U), and a state that
 passes nb blocks is decayed and added to nb times.  Each bound is taken of the sum of the
 terms' magnitudes, since terms may cancel."""
@@ -60,7 +59,7 @@ def role(x, y, z, init, lam, out_first, reverse=False):
         S = add_f * (w[:, None] * zd).t() @ yd + pw(torch.tensor(float(L - 1 - at if reverse else at), dtype=torch.float64)) * S0
         A = abs(add_f) * (w[:, None] * zd.abs()).t() @ yd.abs()     # what was added, terms' sizes
         mm = (at - i if reverse else i - at + 1)[rows]
-        err[rows] += h * abs(init_f) * pw(mm)[:, None] * (xd[rows].abs() @ (S.abs() + A).t())
+        err[rows] += h * abs(init_f) * pw(mm)[:, None] * (xd[rows].abs() @ (S.abs() + 2.0 ** -8 * A).t())
     left = i + 1 if reverse else L - 1 - i
     whole = pw(torch.tensor(float(L), dtype=torch.float64))
     end = add_f * (pw(left)[:, None] * zd).t() @ yd + whole * S0
