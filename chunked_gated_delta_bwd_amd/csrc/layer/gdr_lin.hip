@@ -423,14 +423,20 @@ struct LinRole {
   int32_t xk, yk, zk;     // 1: the tensor has Hk heads, 0: H
   int32_t transposed;     // the state's memory is [y channel][z channel]
   float pair, inter, add; // factors of the pairs' product, of S x, of the state's update
+  int32_t wide;           // out is fp32 (a value head's share of the gradient of a grouped q or k)
+};
+// One launch: n roles that walk the same way.  Two workgroups on one XCD, started together,
+// take the two roles of a segment and head: what both read comes from HBM once.
+struct LinRoles {
+  LinRole r[2];
+  int32_t n;
   int32_t flip;           // last segment first: what the kernel before has read last is still near
 };
 
 // A wave holds 16 columns of S^T (channels of z) in registers.  The tiles of x, y and z are
-// copied to LDS one block ahead.  OUT32: out is fp32 (a value head's share of the gradient of
-// a grouped q or k).
-template <typename T, int D, bool REV, bool OUT32>
-__global__ __launch_bounds__(D * 4, 2) void k_lin_out(const LinParams p, const LinRole o) {
+// copied to LDS one block ahead.
+template <typename T, int D, bool REV>
+__global__ __launch_bounds__(D * 4, 2) void k_lin_out(const LinParams p, const LinRoles roles) {
   typedef typename Lin<T>::Frag Frag;
   constexpr int kB = Lin<T>::B, KS = Lin<T>::KS, JS = kB / KS, E = Lin<T>::E, TI = kB / 16;
   constexpr int NW = D / 16;                                               // waves
@@ -443,8 +449,20 @@ __global__ __launch_bounds__(D * 4, 2) void k_lin_out(const LinParams p, const L
   // Arrays of their own, each named where it is used: of one array with two halves the
   // compiler takes it that a read may meet the loads on their way, and waits for them.
   __shared__ __attribute__((aligned(1024))) char tiles0[3][TB], tiles1[3][TB], pairs0[PB], pairs1[PB];
-  int c, h;
-  place_of(p, int(o.flip ? gridDim.x - 1 - blockIdx.x : blockIdx.x), c, h);
+  int c, h, id = blockIdx.x, role = 0;
+  const int places = p.NC * p.H;
+  if (roles.n == 2) {
+    const int whole = places & ~7;       // workgroups 8 apart share an XCD
+    if (id < 2 * whole) {
+      role = id >> 3 & 1;
+      id = (id >> 4) * 8 + (id & 7);
+    } else {
+      role = id >= whole + places;
+      id -= role ? places : whole;
+    }
+  }
+  const LinRole o = roles.r[role];
+  place_of(p, roles.flip ? places - 1 - id : id, c, h);
   const LinSeg sg = seg_at(p, c);
   const int l = lane_id(), q = l & 15, g = l >> 4, w = __builtin_amdgcn_readfirstlane(wave_id());
   const int slab = w * 16, nb = (sg.len + kB - 1) / kB;
@@ -529,19 +547,21 @@ __global__ __launch_bounds__(D * 4, 2) void k_lin_out(const LinParams p, const L
     }
     // The buffer ends behind the block's last token, and is empty for block -1: what lies
     // further on is dropped, so that every turn has the same number of stores.
-    constexpr int OB = OUT32 ? 4 : int(sizeof(T));
+    const int OB = o.wide ? 4 : int(sizeof(T));
     const int2 tn = tokens(max(i, 0));
     const uint32_t pitch = uint32_t(p.H) * D * OB;
     const __amdgpu_buffer_rsrc_t dst = __builtin_amdgcn_make_buffer_rsrc(
         static_cast<char*>(o.out) + ((int64_t(sg.t0) + tn.x) * p.H + h) * (D * OB), 0, i < 0 ? 0 : int(uint32_t(tn.y - 1) * pitch + D * OB), 0x00027000);
+    const uint32_t at = uint32_t(q) * pitch + slab * OB;
+    if (sizeof(T) == 4 || o.wide) {
 #pragma unroll
-    for (int it = 0; it < TI; ++it) {
-      const uint32_t at = uint32_t(16 * it + q) * pitch + slab * OB;
-      if constexpr (OB == 4) {
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[it]), dst, at + 16 * g, 0, 0);
-      } else {
+      for (int it = 0; it < TI; ++it)
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[it]), dst, at + 16 * it * pitch + 16 * g, 0, 0);
+    } else {
+#pragma unroll
+      for (int it = 0; it < TI; ++it) {
         const uint2 v = pack4_bf16(acc[it][0], acc[it][1], acc[it][2], acc[it][3]);
-        __builtin_amdgcn_raw_buffer_store_b64(u32x2{v.x, v.y}, dst, at + 8 * g, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b64(u32x2{v.x, v.y}, dst, at + 16 * it * pitch + 8 * g, 0, 0);
       }
     }
   };
@@ -752,39 +772,34 @@ int states(const LinParams& p, bool backward, hipStream_t s) {
   return last_error();
 }
 
-template <typename T, int D, bool REV, bool OUT32>
-int out(const LinParams& p, const LinRole& o, hipStream_t s) {
-  k_lin_out<T, D, REV, OUT32><<<unsigned(int64_t(p.NC) * p.H), D * 4, 0, s>>>(p, o);
+template <typename T, int D, bool REV>
+int out(const LinParams& p, const LinRoles& r, hipStream_t s) {
+  k_lin_out<T, D, REV><<<unsigned(int64_t(p.NC) * p.H * r.n), D * 4, 0, s>>>(p, r);
   return last_error();
 }
 
 template <typename T, int D>
 int fwd(const LinParams& p, hipStream_t s) {
-  return out<T, D, false, false>(p, {p.q, p.k, p.v, p.o, p.ht, p.h0, p.st, 1, 1, 0, 0, p.scale, p.scale, 1.f, 1}, s);
+  const LinRole o = {p.q, p.k, p.v, p.o, p.ht, p.h0, p.st, 1, 1, 0, 0, p.scale, p.scale, 1.f, 0};
+  return out<T, D, false>(p, {{o, o}, 1, 1}, s);
 }
 
 template <typename T, int D>
 int bwd(const LinParams& p, hipStream_t s) {
-  const bool grouped = p.G > 1;
+  const int grouped = p.G > 1;
   const int64_t n8 = int64_t(p.T) * p.Hk * D / 8;
   auto sum = [&](void* dst) {
-    if (n8) k_lin_group<T><<<unsigned((n8 + 255) / 256), 256, 0, s>>>(p.part, dst, n8, p.Hk, D, p.G);
+    if (grouped && n8) k_lin_group<T><<<unsigned((n8 + 255) / 256), 256, 0, s>>>(p.part, dst, n8, p.Hk, D, p.G);
     return last_error();
   };
-  LinRole q = {p.dO, p.v, p.k, p.dq, nullptr, p.h0, p.st, 0, 0, 1, 1, p.scale, p.scale, 1.f, 1};
-  LinRole k = {p.v, p.dO, p.q, p.dk, nullptr, p.dht, p.dst, 0, 0, 1, 1, p.scale, 1.f, p.scale, 0};
-  const LinRole v = {p.k, p.q, p.dO, p.dv, p.dh0, p.dht, p.dst, 1, 1, 0, 0, p.scale, 1.f, p.scale, 1};
-  if (grouped) {
-    q.out = k.out = p.part;
-    if (const int e = out<T, D, false, true>(p, q, s)) return e;
-    if (const int e = sum(p.dq)) return e;
-    if (const int e = out<T, D, true, true>(p, k, s)) return e;
-    if (const int e = sum(p.dk)) return e;
-  } else {
-    if (const int e = out<T, D, false, false>(p, q, s)) return e;
-    if (const int e = out<T, D, true, false>(p, k, s)) return e;
-  }
-  return out<T, D, true, false>(p, v, s);
+  void* part = p.part;
+  const LinRole q = {p.dO, p.v, p.k, grouped ? part : p.dq, nullptr, p.h0, p.st, 0, 0, 1, 1, p.scale, p.scale, 1.f, grouped};
+  const LinRole k = {p.v, p.dO, p.q, grouped ? part : p.dk, nullptr, p.dht, p.dst, 0, 0, 1, 1, p.scale, 1.f, p.scale, grouped};
+  const LinRole v = {p.k, p.q, p.dO, p.dv, p.dh0, p.dht, p.dst, 1, 1, 0, 0, p.scale, 1.f, p.scale, 0};
+  if (const int e = out<T, D, false>(p, {{q, q}, 1, 1}, s)) return e;
+  if (const int e = sum(p.dq)) return e;
+  if (const int e = out<T, D, true>(p, {{k, v}, 2, 0}, s)) return e;
+  return sum(p.dk);
 }
 
 template <typename T, int D>
