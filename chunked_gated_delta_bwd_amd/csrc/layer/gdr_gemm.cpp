@@ -36,7 +36,7 @@ gdr_status check_gemm_shape(const gdr_gemm_shape* s) {
   if (s->M < 0 || s->N < 0 || s->K < 1) return set_error(GDR_EINVAL, "bad M/N/K");
   if (s->block != 1 && s->block != gdr::kGroup) return set_error(GDR_EUNSUPPORTED, "block %d not in {1, 128}", s->block);
   if (s->M > (1 << 30) || s->N > (1 << 30) || s->K > (1 << 30) ||
-      ceil_div(s->M, 128) * ceil_div(s->N, 128) >= (int64_t(1) << 19) || ceil_div(s->N, 16) * 512 >= gdr::kMaxThreads)
+      ceil_div(s->M, 128) * ceil_div(s->N, 128) >= (int64_t(1) << 19))
     return set_error(GDR_EUNSUPPORTED, "product too large for one launch");
   return GDR_OK;
 }

@@ -43,9 +43,11 @@ gdr_status check_lin_shape(const gdr_lin_shape* s) {
     }
     if (cu[s->N] != s->T) return set_error(GDR_EINVAL, "cu_seqlens[N] = %lld != T = %d", (long long)cu[s->N], s->T);
   }
-  const int64_t tokens = int64_t(s->B) * s->T, blocks = tokens / gdr::kLinBlock + s->N;
-  // a workgroup of 256 threads at least for every state and at most for every block
-  if (tokens >= (int64_t(1) << 30) || s->H > (1 << 16) || blocks * s->H * 16 * 256 >= gdr::kMaxThreads)
+  // at most 16 workgroups of 256 threads for every state or block, and the bytes of a block's
+  // rows within 32 bits
+  constexpr int64_t most = gdr::kMaxThreads / (16 * 256);
+  const int64_t blocks = int64_t(s->B) * s->T / gdr::kLinBlock + s->N;
+  if (s->H > (1 << 16) || blocks >= most || blocks * s->H >= most)
     return set_error(GDR_EUNSUPPORTED, "problem too large for one launch and 32-bit indexing");
   return GDR_OK;
 }

@@ -368,11 +368,11 @@ gdr_status gdr_norm_bwd(const gdr_norm_shape* shape, const void* r, const float*
  * range for every n up to the longest sequence.
  * States, products and sums are fp32.  With bf16 tensors the products of pairs of
  * tokens and the states are rounded to bf16 once where they are multiplied with
- * bf16 tensors; the states themselves, returned or not, are not.  An infinity or NaN at a token reaches no token before it (after
- * it, in the gradients of k and v) and no other sequence; from there on, what the
- * formulas make infinite or NaN is infinite or NaN, not always the same of the two.
- * GDR_EUNSUPPORTED from 2^30 tokens B T or 2^16 heads on, and from 2^20 blocks of 64
- * tokens times heads on (counting B T / 64 + N blocks). */
+ * bf16 tensors; the states themselves, returned or not, are not.  An infinity or NaN
+ * at a token reaches no token before it (after it, in the gradients of k and v) and no
+ * other sequence; from there on, what the formulas make infinite or NaN is infinite or
+ * NaN, not always the same of the two.  GDR_EUNSUPPORTED above 2^16 heads, and from
+ * 2^20 blocks of 64 tokens times heads on (B T / 64 + N blocks). */
 typedef struct {
   int32_t B, T, H, D;               /* dense: [B,T,H,D]; varlen: B == 1, T == total tokens */
   int32_t N;                        /* sequences, as in gdr_shape */
@@ -444,15 +444,18 @@ gdr_status gdr_quant(const gdr_quant_shape* shape, const void* x, void* q, float
 /* c[m][n] = sum over groups g of 128 elements k of the contraction (the last may be
  * shorter) of a_scales[m][g] b_scales[n / block][g] sum_{k in g} a[m][k] b[n][k].
  * a: [M,K] e4m3 bytes with a_scales [M,G], G = ceil(K / 128); b: [N,K] bytes with
- * b_scales [ceil(N / block),G], block 1 or 128; c: [M,N] dtype.  Products within a
- * group are exact, sums fp32, c is rounded once.  A linear layer y = x w^T takes a = x
+ * b_scales [ceil(N / block),G], block 1 or 128; c: [M,N] dtype.  With an fp32 c products
+ * are exact and sums fp32.  With a bf16 c the matrix instructions take the bytes as
+ * they are: within a group they sum the products of up to 8 neighbouring k with the bits
+ * below 2^-13 of the largest of them dropped (2^-10 of the sum of their magnitudes at
+ * most), the rest is fp32 and c is rounded once.  A linear layer y = x w^T takes a = x
  * and b = w (block 128); its backward takes the same product with a = dy and
  * b = w^T, and with a = dy^T and b = x^T (block 1), each quantised along the
  * contraction.  K >= 1; M and N may be zero.  ws: gdr_gemm_workspace_bytes() (zero
  * for most shapes; then ws may be NULL), 256-byte aligned, any content; calls that
  * overlap in time need one each.  c must not overlap the inputs.  Sums run in an
  * order that depends on the shape alone.  GDR_EUNSUPPORTED above 2^30 rows or columns
- * of a matrix, from 2^19 tiles of 128 x 128 of c on and from N = 2^27 on. */
+ * of a matrix and from 2^19 tiles of 128 x 128 of c on. */
 typedef struct {
   int32_t M, N, K;
   int32_t dtype;                    /* gdr_dtype of c */
