@@ -69,14 +69,15 @@ template <> struct Lin<bf16> {
     const f32x4 x = mma(f[1], none, mma(f[0], none, zero4()));
     return __any(!(x[0] + x[1] + (x[2] + x[3]) == 0.f));
   }
-  static __device__ __forceinline__ float get(Frag f, int e) {
-    const u32x4 u = __builtin_bit_cast(u32x4, f);
-    return __uint_as_float(e & 1 ? u[e / 2] & 0xffff0000u : u[e / 2] << 16);
+  // 1 where element e is an infinity or a NaN, 0 elsewhere; the fragment with a 0 in its place.
+  // In integers: sixteen comparisons' masks would spill what the loop around them keeps.
+  static __device__ __forceinline__ uint32_t bad(Frag f, int e) {
+    const uint32_t u = __builtin_bit_cast(u32x4, f)[e / 2] >> (16 * (e & 1));
+    return ((u & 0x7f80u) + 0x80u) >> 15;
   }
-  static __device__ __forceinline__ Frag without(Frag f, uint32_t drop) {   // bit e of drop: element e becomes 0
+  static __device__ __forceinline__ Frag without(Frag f, int e, uint32_t bit) {
     u32x4 u = __builtin_bit_cast(u32x4, f);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] &= (drop >> (2 * i) & 1 ? 0xffff0000u : ~0u) & (drop >> (2 * i + 1) & 1 ? 0x0000ffffu : ~0u);
+    u[e / 2] &= ~((0u - bit) & (0xffffu << (16 * (e & 1))));
     return __builtin_bit_cast(Frag, u);
   }
 };
@@ -123,10 +124,11 @@ template <> struct Lin<float> {
       b |= ((__float_as_uint(f[0][i]) & 0x7f800000u) + 0x00800000u) | ((__float_as_uint(f[1][i]) & 0x7f800000u) + 0x00800000u);
     return __any(b >> 31);
   }
-  static __device__ __forceinline__ float get(Frag f, int e) { return f[e]; }
-  static __device__ __forceinline__ Frag without(Frag f, uint32_t drop) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = drop >> i & 1 ? 0.f : f[i];
+  static __device__ __forceinline__ uint32_t bad(Frag f, int e) {
+    return ((__float_as_uint(f[e]) & 0x7f800000u) + 0x00800000u) >> 31;
+  }
+  static __device__ __forceinline__ Frag without(Frag f, int e, uint32_t bit) {
+    f[e] = __uint_as_float(__float_as_uint(f[e]) & (bit - 1u));
     return f;
   }
 };
@@ -162,9 +164,18 @@ __device__ __forceinline__ float decay2(const LinParams& p, int h) {
   const float l = p.log_decay[h] * kLog2e;
   return l < -1e30f ? -1e30f : l;
 }
-// c^n - 1: a state is decayed by S + (c^n - 1) S, so that a slow decay's rounding does
-// not add up over the blocks of a long sequence
-__device__ __forceinline__ float decay_m1(float l2, int n) { return expm1f(float(n) * l2 * 0.6931471805599453f); }
+// A state's decay by c^n.  Over one half it is S + (c^n - 1) S, so that a slow decay's rounding
+// does not add up over the blocks of a long sequence; below, c^n - 1 would lose c^n's bits.
+struct Decay {
+  float f;
+  uint32_t keep;   // all bits, or none
+  __device__ __forceinline__ float operator()(float s) const { return fmaf(f, s, __uint_as_float(__float_as_uint(s) & keep)); }
+};
+__device__ __forceinline__ Decay decay_of(float l2, int n) {
+  const float x = float(n) * l2;
+  const bool slow = x > -1.f;
+  return {slow ? expm1f(x * 0.6931471805599453f) : exp2f(x), slow ? ~0u : 0u};
+}
 
 // 16-byte pieces of a block for each of 256 threads
 template <typename T, int D> constexpr int kPieces = Lin<T>::B * D * int(sizeof(T)) / 16 / 256;
@@ -228,13 +239,13 @@ struct State {
       for (int u = 0; u < VT; ++u)
         *reinterpret_cast<f32x4*>(m + (slab + Lin<T>::template col<VT>(u, q)) * D + 16 * t + 4 * g) = s[t][u];
   }
-  __device__ __forceinline__ void decay(float em1) {
+  __device__ __forceinline__ void decay(const Decay& d) {
 #pragma unroll
     for (int t = 0; t < KT; ++t)
 #pragma unroll
       for (int u = 0; u < VT; ++u)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) s[t][u][r] = fmaf(em1, s[t][u][r], s[t][u][r]);
+        for (int r = 0; r < 4; ++r) s[t][u][r] = d(s[t][u][r]);
   }
   // S^T += y^T (w z).  The weighted z of bf16 tensors is a sum of bf16 parts: three (24 bits of
   // significand, as fp32) for states that are returned or that another segment starts from,
@@ -335,7 +346,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_lin_local(const
   const int slab = wave_id() * 16 * VT, nb = (sg.len + kB - 1) / kB;
   State<T, D, VT> S;
   S.zero();
-  float w[JS][Lin<T>::E], em1 = 0.f;
+  float w[JS][Lin<T>::E];
+  Decay over = {};   // a block
   int wn = -1;
   u32x4 yr[kPieces<T, D>], zr[kPieces<T, D>];
   auto load = [&](int i) {
@@ -349,7 +361,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_lin_local(const
     const int b = REV ? nb - 1 - i : i, n = min(kB, sg.len - b * kB);
     if (n != wn) {
       state_weights<T, REV>(l2, n, wscale, w);
-      em1 = decay_m1(l2, n);
+      over = decay_of(l2, n);
       wn = n;
     }
     chain_barrier();
@@ -362,7 +374,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_lin_local(const
     for (int js = 0; js < JS; ++js)
 #pragma unroll
       for (int u = 0; u < VT; ++u) zf[js][u] = Lin<T>::template slab<D, VT>(zs, slab, u, js * Lin<T>::KS);
-    S.decay(em1);
+    S.decay(over);
     S.template add<0, 3>(ys, zf, w);
   }
   S.store((REV ? p.dst : p.st) + (int64_t(c) * p.H + h) * (D * D), slab);
@@ -390,7 +402,7 @@ __global__ __launch_bounds__(256) void k_lin_carry(const LinParams p) {
   f32x4 cur = zero4();
   if (init) cur = *reinterpret_cast<const f32x4*>(init + (int64_t(n) * p.H + h) * (D * D) + e);
   float* st = (REV ? p.dst : p.st) + (int64_t(row0) * p.H + h) * (D * D) + e;
-  const float em1 = decay_m1(l2, p.seg), em1_last = decay_m1(l2, len);
+  const Decay whole = decay_of(l2, p.seg), short_one = decay_of(l2, len);
   constexpr int U = 8;                   // segments whose loads are on their way together
   for (int i0 = 0; i0 < nseg; i0 += U) {
     f32x4 x[U];
@@ -402,9 +414,9 @@ __global__ __launch_bounds__(256) void k_lin_carry(const LinParams p) {
       if (i0 + a < nseg) {
         *reinterpret_cast<f32x4*>(st + (REV ? nseg - 1 - i0 - a : i0 + a) * step) = cur;
         if (i0 + a < nseg - 1) {
-          const float d = REV && i0 + a == 0 ? em1_last : em1;
+          const Decay d = REV && i0 + a == 0 ? short_one : whole;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) cur[r] = fmaf(d, cur[r], cur[r]) + x[a][r];
+          for (int r = 0; r < 4; ++r) cur[r] = d(cur[r]) + x[a][r];
         }
       }
   }
@@ -467,31 +479,38 @@ __global__ __launch_bounds__(D * 4, 2) void k_lin_out(const LinParams p, const L
   const int slab = w * 16, nb = (sg.len + kB - 1) / kB;
   const float l2 = decay2(p, h);
   const int64_t sh = int64_t(sg.seq) * p.H + h;
-  auto tokens = [&](int i) {   // of the walk's i-th block: first and number
-    const int b = REV ? nb - 1 - i : i;
-    return make_int2(b * kB, min(kB, sg.len - b * kB));
-  };
+  const int n_last = sg.len - (nb - 1) * kB;
+  auto rows = [&](int i) { return i == (REV ? 0 : nb - 1) ? n_last : kB; };   // of the walk's i-th block
   // A lane's row and place in a load, and the piece that belongs there
   const int lrow = w * RPL + l / PR, piece = (Lin<T>::template off<D>(lrow & 15, 0) % ROW / 16) ^ (l % PR);
-  auto load = [&](int i, auto& tiles, int m) {
-    const int2 tn = tokens(i);
-    const int64_t t0 = sg.t0 + tn.x;
-    {
-      const bool shared = m == 0 ? o.xk : m == 1 ? o.yk : o.zk;
-      const int heads = shared ? p.Hk : p.H, head = shared ? h / p.G : h;
-      const char* src = static_cast<const char*>(m == 0 ? o.x : m == 1 ? o.y : o.z) + (t0 * heads + head) * ROW;
-      // The buffer ends behind the block's last row: no lane reads past it.  What those lanes
-      // leave in LDS is cleared when the block has come.
-      const uint32_t pitch = uint32_t(heads) * ROW;
-      const __amdgpu_buffer_rsrc_t buf = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(src), 0, int(uint32_t(tn.y - 1) * pitch + ROW), 0x00027000);
+  // Where the walk's next block begins, of x, y and z and of the output, and the bytes between rows
+  const int64_t t0 = sg.t0 + (REV ? (nb - 1) * kB : 0);
+  const int OB = o.wide ? 4 : int(sizeof(T));
+  const char* src[3];
+  uint32_t pitch[3];
 #pragma unroll
-      for (int a = 0; a < LPT; ++a)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_void_t*)((lds_char_t*)(tiles[m] + (a * NW + w) * 1024)), 16,
-                                                 (a * NW * RPL + lrow) * pitch + 16 * piece, 0, 0, 0);
-    }
+  for (int m = 0; m < 3; ++m) {
+    const bool shared = m == 0 ? o.xk : m == 1 ? o.yk : o.zk;
+    const int heads = shared ? p.Hk : p.H, head = shared ? h / p.G : h;
+    src[m] = static_cast<const char*>(m == 0 ? o.x : m == 1 ? o.y : o.z) + (t0 * heads + head) * ROW;
+    pitch[m] = uint32_t(heads) * ROW;
+  }
+  const uint32_t out_pitch = uint32_t(p.H) * D * OB;
+  char* out = static_cast<char*>(o.out) + (t0 * p.H + h) * (D * OB);
+  auto load = [&](int i, auto& tiles, int m) {
+    // The buffer ends behind the block's last row: no lane reads past it.  What those lanes
+    // leave in LDS is cleared when the block has come.
+    const __amdgpu_buffer_rsrc_t buf = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(src[m]), 0, int(uint32_t(rows(i) - 1) * pitch[m] + ROW), 0x00027000);
+#pragma unroll
+    for (int a = 0; a < LPT; ++a)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_void_t*)((lds_char_t*)(tiles[m] + (a * NW + w) * 1024)), 16,
+                                               (a * NW * RPL + lrow) * pitch[m] + 16 * piece, 0, 0, 0);
+    src[m] += (REV ? -int64_t(kB) : int64_t(kB)) * pitch[m];
   };
-  if (nb)
+  if (nb) {
+#pragma unroll
     for (int m = 0; m < 3; ++m) load(0, tiles0, m);
+  }
   State<T, D, 1> S;
   const bool start = REV ? sg.idx == sg.nseg - 1 : sg.idx == 0, end = REV ? sg.idx == 0 : sg.idx == sg.nseg - 1;
   const bool exact = end && o.last;
@@ -500,13 +519,13 @@ __global__ __launch_bounds__(D * 4, 2) void k_lin_out(const LinParams p, const L
   else S.zero();
   // The wave's tiles of pairs: tokens i of tile w % TI, tokens j of w / TI and every JSTEP-th
   // on, and the decay between them
-  const int it0 = w % TI, jt0 = w / TI;
+  const int it0 = w % TI, jt0 = w / TI, gap0 = 16 * (it0 - jt0) + q - 4 * g;
   float near[NPAIR][4];
 #pragma unroll
   for (int a = 0; a < NPAIR; ++a)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int d = (16 * it0 + q) - (16 * (jt0 + a * JSTEP) + 4 * g + r), n = REV ? -d : d;
+      const int d = gap0 - (16 * a * JSTEP + r), n = REV ? -d : d;
       near[a][r] = n >= 0 ? o.pair * fast_exp2(float(n) * l2) : 0.f;
     }
   // the pairs of later tokens are never written again
@@ -514,7 +533,8 @@ __global__ __launch_bounds__(D * 4, 2) void k_lin_out(const LinParams p, const L
     *reinterpret_cast<u32x4*>(pairs0 + 16 * i) = u32x4{0, 0, 0, 0};
     *reinterpret_cast<u32x4*>(pairs1 + 16 * i) = u32x4{0, 0, 0, 0};
   }
-  float wz[JS][E], far[TI], em1 = 0.f;
+  float wz[JS][E], far[TI];
+  Decay over = {};   // a block
   int wn = -1;
   // here and not at the state's first use, where the compiler would wait for every load that
   // is on its way, in each turn of the loop
@@ -548,21 +568,18 @@ __global__ __launch_bounds__(D * 4, 2) void k_lin_out(const LinParams p, const L
     }
     // The buffer ends behind the block's last token, and is empty for block -1: what would lie
     // further on is dropped.
-    const int OB = o.wide ? 4 : int(sizeof(T));
-    const int2 tn = tokens(max(i, 0));
-    const uint32_t pitch = uint32_t(p.H) * D * OB;
-    const __amdgpu_buffer_rsrc_t dst = __builtin_amdgcn_make_buffer_rsrc(
-        static_cast<char*>(o.out) + ((int64_t(sg.t0) + tn.x) * p.H + h) * (D * OB), 0, i < 0 ? 0 : int(uint32_t(tn.y - 1) * pitch + D * OB), 0x00027000);
-    const uint32_t at = uint32_t(q) * pitch + slab * OB;
+    const __amdgpu_buffer_rsrc_t dst = __builtin_amdgcn_make_buffer_rsrc(out, 0, i < 0 ? 0 : int(uint32_t(rows(i) - 1) * out_pitch + D * OB), 0x00027000);
+    const uint32_t at = uint32_t(q) * out_pitch + slab * OB;
+    if (i >= 0) out += (REV ? -int64_t(kB) : int64_t(kB)) * out_pitch;
     if (sizeof(T) == 4 || o.wide) {
 #pragma unroll
       for (int it = 0; it < TI; ++it)
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[it]), dst, at + 16 * it * pitch + 16 * g, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[it]), dst, at + 16 * it * out_pitch + 16 * g, 0, 0);
     } else {
 #pragma unroll
       for (int it = 0; it < TI; ++it) {
         const uint2 v = pack4_bf16(acc[it][0], acc[it][1], acc[it][2], acc[it][3]);
-        __builtin_amdgcn_raw_buffer_store_b64(u32x2{v.x, v.y}, dst, at + 16 * it * pitch + 8 * g, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b64(u32x2{v.x, v.y}, dst, at + 16 * it * out_pitch + 8 * g, 0, 0);
       }
     }
   };
@@ -570,6 +587,8 @@ __global__ __launch_bounds__(D * 4, 2) void k_lin_out(const LinParams p, const L
   auto pairs = [&](auto& tiles, auto& ps) {
     const char *const xs = tiles[0], *const ys = tiles[1];
     if (jt0 >= TI) return;
+    int gap = gap0;
+    asm volatile("" : "+v"(gap));   // compared each time: the masks of all turns would spill
     Frag xf[D / KS];
 #pragma unroll
     for (int ks = 0; ks < D / KS; ++ks) xf[ks] = Lin<T>::template rk<D>(xs, 16 * it0, ks * KS);
@@ -583,7 +602,7 @@ __global__ __launch_bounds__(D * 4, 2) void k_lin_out(const LinParams p, const L
       // a later token's product counts nothing, whatever it is
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int d = (16 * it0 + q) - (16 * jt + 4 * g + r);
+        const int d = gap - (16 * s * JSTEP + r);
         a[r] = (REV ? d <= 0 : d >= 0) ? a[r] * near[s][r] : 0.f;
       }
       Lin<T>::store4(ps + Lin<T>::template off<kB>(16 * it0 + q, 16 * jt + 4 * g), a[0], a[1], a[2], a[3]);
@@ -598,10 +617,10 @@ __global__ __launch_bounds__(D * 4, 2) void k_lin_out(const LinParams p, const L
     // The block has come, and so have the pairs of the block before.
     wait_vm<0>();
     chain_barrier();
-    const int n = tokens(i).y;
+    const int n = rows(i);
     if (n != wn) {
       state_weights<T, REV>(l2, n, o.add, wz);
-      em1 = decay_m1(l2, n);
+      over = decay_of(l2, n);
 #pragma unroll
       for (int it = 0; it < TI; ++it) {
         const int m = REV ? n - 1 - (16 * it + q) : 16 * it + q + 1;
@@ -627,18 +646,14 @@ __global__ __launch_bounds__(D * 4, 2) void k_lin_out(const LinParams p, const L
     if (odd) {
       bad_from = kB;
 #pragma unroll
-      for (int js = 0; js < JS; ++js) {
-        uint32_t drop = 0;
+      for (int js = 0; js < JS; ++js)
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           const int j = js * KS + E * g + e;
-          if (!(fabsf(Lin<T>::get(zf[js], e)) <= 3.4028235e38f)) {
-            drop |= 1u << e;
-            bad_from = min(bad_from, REV ? kB - 1 - j : j);
-          }
+          const uint32_t bit = Lin<T>::bad(zf[js], e);
+          zf[js] = Lin<T>::without(zf[js], e, bit);
+          bad_from = min(bad_from, (REV ? kB - 1 - j : j) | int((bit - 1u) & 1024u));
         }
-        zf[js] = Lin<T>::without(zf[js], drop);
-      }
       bad_from = min(bad_from, __shfl_xor(bad_from, 16, 64));
       bad_from = min(bad_from, __shfl_xor(bad_from, 32, 64));
     }
@@ -655,7 +670,7 @@ __global__ __launch_bounds__(D * 4, 2) void k_lin_out(const LinParams p, const L
 #pragma unroll
       for (int r = 0; r < 4; ++r) acc[it][r] *= far[it];
     if (i + 1 < nb) load(i + 1, next, 1);
-    S.decay(em1);
+    S.decay(over);
     Frag zv[JS][1];
 #pragma unroll
     for (int js = 0; js < JS; ++js) zv[js][0] = zf[js];

@@ -107,6 +107,24 @@ def test_decays(lam, dtype):
         R.check(name, out[name], value, err)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("packed", [False, True])
+def test_what_a_strong_decay_leaves_of_a_state(packed, dtype):
+    """Tokens that add nothing: the states alone, decayed to as little as e^-60, to fp32's precision."""
+    H, D, scale = 6, 64, 1.0
+    lam = [-0.3, -0.8, -6.0, -16.0, -30.0, -60.0]
+    lengths = [1, 1, 1] if not packed else [1, 2, 0, 1]
+    t, dO, dht = make(19, lengths, H, H, D, dtype, lam=lam)
+    t["v"], dO = torch.zeros_like(t["v"]), torch.zeros_like(dO)
+    ref = L.lin(t["q"], t["k"], t["v"], t["log_decay"], t["h0"], lengths, scale, dO, dht)
+    d, out = cuda(t), buffers(t)
+    out["ht"], out["dh0"] = nan_like(t["h0"]), nan_like(t["h0"])
+    go(problem(lengths, H, H, D, dtype, scale, packed), d, dO.cuda(), dht.cuda(), out)
+    torch.cuda.synchronize()
+    for name, (value, err) in ref.items():
+        R.check(name, out[name], value, err)
+
+
 def test_gradients_against_autograd_and_differences():
     lengths, H, Hk, D = [70, 0, 33], 4, 2, 64
     t, dO, dht = make(5, lengths, H, Hk, D, "f32")
