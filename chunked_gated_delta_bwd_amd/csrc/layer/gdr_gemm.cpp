@@ -53,12 +53,13 @@ gdr_status check_gemm_shape(const gdr_gemm_shape* s) {
 // A split contraction pays where few workgroups leave most compute units idle: 64 x 4096 x
 // 4096 with 32 workgroups 12.9 in 4 runs, 14.1 in 2, 16.2 as one for every 16 rows of b;
 // 256 x 4096 x 4096 with 128 workgroups 17.3 whole, 21.4 in 2 runs.  Rows that pass through
-// registers take a split further: 1000 x 2050 x 4100, f32, 53.7 whole, 46.5 in 2 runs, where
-// the K of 4096 takes 38.7 whole, 43.7 in 2.
+// registers take a split further: 1000 x 2050 x 4102, f32, 53.8 whole, 51.3 in 2 runs, and
+// 500 x 1030 x 2046 25.8 and 20.6, where the K of 4096 takes 37.9 whole, 42.7 in 2.  Rows on
+// 4 bytes copied to LDS: 1000 x 2050 x 4100, f32, 46.8, through registers 48.2.
 gdr::GemmPlan gemm_plan(const gdr_gemm_shape* s) {
   const int64_t groups = ceil_div(s->K, gdr::kGroup);
   if (s->M <= gdr::kFewRows) return {gdr::kGemmFew, 1, 0};
-  const int32_t copy = s->K % 16 == 0 && s->K <= (1 << 22);   // 256 rows within 32 bits
+  const int32_t copy = s->K % 4 == 0 && s->K <= (1 << 22);   // 256 rows within 32 bits
   if (copy && s->dtype == GDR_BF16 && groups >= 8 && ceil_div(s->M, 256) * ceil_div(s->N, 256) >= 256)
     return {gdr::kGemmLarge, 1, copy};
   if (ceil_div(s->M, 128) * ceil_div(s->N, 128) >= 512) return {gdr::kGemmMedium, 1, copy};

@@ -32,7 +32,7 @@ constexpr int kFewRows = 32;
 struct GemmPlan {
   int32_t kind;
   int32_t splits;   // runs of the contraction, each a workgroup's; their sums are added afterwards
-  int32_t copy;     // rows start on 16 bytes: they go to LDS without passing through registers
+  int32_t copy;     // rows start on 4 bytes: they go to LDS without passing through registers
 };
 
 struct GemmParams {

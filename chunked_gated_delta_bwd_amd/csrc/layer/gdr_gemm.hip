@@ -1,11 +1,19 @@
 // Product of e4m3 matrices with a scale for each 128 of the contraction (gdr_gemm).
 //
 //   c[m][n] = sum_g sa[m][g] sb[n][g] sum_{k in g} a[m][k] b[n][k]
-// The inner sum over a group's 128 elements is matrix instructions alone (32x32x64, two
-// a group), started from zero; what they leave is scaled and added in fp32, so that the
-// scales may be any numbers.  b's rows are the instruction's rows and a's its columns:
-// a lane then holds sums of one row of a, whose scale is one register, and b's scale is
-// the same for all of them where it belongs to a block of 128 rows.
+// The inner sum over a group's 128 elements is matrix instructions alone (one 16x16x128 of
+// e4m3, or four 16x16x32 of bf16 where c is fp32), started from zero; what they leave is
+// scaled and added in fp32, so that the scales may be any numbers.  b's rows are the
+// instruction's rows and a's its columns: a lane then holds sums of one row of a, whose scale
+// is one register, and b's scale is the same for all of them where it belongs to a block of
+// 128 rows.
+//
+// Large products are bound by the matrix instructions at the clock that the card's power
+// allows (32768 x 4096 x 4096: 514 to 550 us = 2,000 to 2,140 TFLOP/s; its instructions
+// alone, fed from registers, 365 to 380), ordinary ones by how far tiles fill 256 compute
+// units and LDS feeds them (1000 x 2050 x 4100, fp32: 44 us; 2048 cubed, bf16: 15.3), small
+// ones by latency (64 x 4096 x 4096: 12.8 us, of which the kernel 9.7; one row, 4096 x 2048:
+// 6.8, of which the kernel 3.8).
 #include <hip/hip_runtime.h>
 
 #include "../gdr_device.h"
@@ -138,7 +146,8 @@ template <bool SHORT> struct Off { typedef uint32_t T; };
 template <> struct Off<false> { typedef int64_t T; };
 
 // T: what the sums are stored as (fp32 for the partial sums of a split contraction).
-// NB: groups in LDS.  ROWS: b has a scale for each row.  DMA: rows start on 16 bytes.
+// NB: groups in LDS.  ROWS: b has a scale for each row.  DMA: rows start on 4 bytes,
+// as loads to LDS ask for.
 template <typename T, int BM, int BN, int WM, int WN, int NB, bool EXACT, bool ROWS, bool DMA>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm(const GemmParams p) {
   constexpr int NT = 64 * WM * WN, MT = BM / WM / 16, QT = BN / WN / 16;
@@ -156,7 +165,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm(const GemmParams p) {
   const int wm = (w % WM) * (BM / WM), wn = (w / WM) * (BN / WN);
   // Load i of a wave fills rows 8 (w L + i) + l / 8, lane l the place l mod 8.  Rows past the
   // matrix repeat its last one: what they give is not stored.  Offsets from the tile's first
-  // row: at most 256 rows of 2^22 bytes, or 128 of 2^24.
+  // row: at most 256 rows of 2^22 bytes.
   const uint8_t *ga = p.a + int64_t(m0) * p.K, *gb = p.b + int64_t(n0) * p.K;
   typedef typename Off<DMA>::T off_t;
   off_t at[LA + LB];
@@ -180,13 +189,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm(const GemmParams p) {
     for (int u = 0; u < LA + LB; ++u) {
       const uint8_t* src = (u < LA ? ga : gb) + int64_t(g) * kGroup + at[u];
       const int n = p.K - g * kGroup - 16 * piece_of(u);
-      if constexpr (DMA) {
-        u32x4 v = {0, 0, 0, 0};
-        if (n > 0) v = *reinterpret_cast<const u32x4*>(src);   // a whole piece
-        *reinterpret_cast<u32x4*>(spot(u, buf) + 16 * l) = v;
-      } else {
-        raw[u] = bytes16(src, n, u < LA ? p.a + int64_t(p.M) * p.K : p.b + int64_t(p.N) * p.K);
-      }
+      const u32x4 v = bytes16(src, n, u < LA ? p.a + int64_t(p.M) * p.K : p.b + int64_t(p.N) * p.K);
+      if constexpr (DMA) *reinterpret_cast<u32x4*>(spot(u, buf) + 16 * l) = v;
+      else raw[u] = v;
     }
   };
   auto put_tiles = [&](int buf) {
@@ -360,7 +365,10 @@ __global__ __launch_bounds__(256) void k_gemm_sum(const GemmParams p) {
 // ---------------------------------------------------------------------------
 // A workgroup of 8 waves takes 16 rows of b and all of a's, its waves every eighth group
 // of the contraction each (two pieces of a lane's row straight from memory: every byte of b
-// is used once; both operands take the group's bytes in the same order, whatever it is), and adds their sums in LDS.  Bound by the bytes of b.
+// is used once; both operands take the group's bytes in the same order, whatever it is), and
+// adds their sums in LDS.  Bound by latency and the bytes of b: 1 x 4096 x 2048 in 3.8 us.
+// At 32 rows of a it is still the shorter one (32 x 4096 x 4096: 10.2 us, tiles of 64 x 128
+// in 4 runs 12.4), at 64 not (16.3 and 12.9).
 constexpr int kFewWaves = 8;
 
 template <typename T, int MT, bool ROWS>

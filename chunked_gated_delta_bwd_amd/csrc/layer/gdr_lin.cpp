@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cstdint>
 #include <cstring>
 
 #include "gdr_check.h"
@@ -52,22 +53,44 @@ gdr_status check_lin_shape(const gdr_lin_shape* s) {
   return GDR_OK;
 }
 
-// Tokens per segment: whole blocks, so many that about kWorkgroups workgroups share the
-// work, but not so few that the states between segments cost more than they bring.
-constexpr int64_t kWorkgroups = 512, kFewestBlocks = 4;
+// Tokens per segment: whole blocks, as many as a model of the time finds best.  In units of a
+// block's turn in one of the four output kernels (2.7 us): segments run one to a compute unit,
+// split ones' own states cost a quarter more, and the states between them 3 and another 3 for
+// each 256.  Segments of one length take whole rounds of the compute units; of a pack's, which
+// are not, half a segment is lost at the end.  Measured, forward and backward together, heads
+// of 128, in us for segments of
+//                          1 block     2     4     8    16    32
+//   T = 512, 4 heads            51      61    87    90 (no split)
+//   T = 2048, 4 heads           64      69    93   145
+//   T = 2048, 16 heads         135      98   102   151
+//   4 x 1000, 8 heads          134      96   100   149
+//   T = 8192, 16 heads                        245   216
+//   T = 32768, 16 heads                                   697   677
+//   4 x 4095, 32 heads                                    675   667
+// and, heads of 64, T = 8192, 8 heads: 85 for 2, 74 for 4, 90 for 8; 12 uneven sequences, 32
+// heads: 1830 for 66, 1681 for 33, 1661 for 22.
 int64_t segment_of(const gdr_lin_shape* s) {
+  constexpr int64_t kUnits = 256;
   int64_t blocks = 0, longest = 0;
-  for (int n = 0; n < s->N; ++n) {
+  const bool pack = s->cu_seqlens_host != nullptr;
+  for (int n = 0; n < (pack ? s->N : 1); ++n) {
     const int64_t b = parts_of(seq_len(s, n), gdr::kLinBlock);
     blocks += b;
     longest = std::max(longest, b);
-    if (!s->cu_seqlens_host) {
-      blocks = b * s->N;
-      break;
+  }
+  if (!pack) blocks *= s->N;
+  int64_t best = longest, least = INT64_MAX;
+  for (int64_t k = 1; k <= std::min<int64_t>(longest, 1024); k += std::max<int64_t>(1, k / 8)) {
+    const int64_t seg = parts_of(longest, k);
+    const int64_t groups = (pack ? blocks / seg + s->N / 2 : s->N * parts_of(longest, seg)) * s->H;
+    const int64_t turns = pack ? std::max(seg, blocks * s->H / kUnits + seg / 2) : parts_of(groups, kUnits) * seg;
+    const int64_t time = k == 1 ? 4 * turns : 5 * turns + 12 + 12 * groups / kUnits;
+    if (time < least) {
+      least = time;
+      best = seg;
     }
   }
-  const int64_t fair = std::max(kFewestBlocks, (blocks * s->H + kWorkgroups - 1) / kWorkgroups);
-  return std::max<int64_t>(1, std::min(fair, longest)) * gdr::kLinBlock;
+  return best * gdr::kLinBlock;
 }
 
 struct LinLayout {
