@@ -34,23 +34,25 @@ template <> struct Lin<bf16> {
   template <int W> static __device__ __forceinline__ Frag rk(const char* t, int r0, int k0) {
     return frag_rk_s<W, 0>(t, r0, k0);
   }
-  // the order of the contraction that state() leaves
-  template <int W> static __device__ __forceinline__ Frag rk_state(const char* t, int r0, int k0) {
-    return frag_rk_split_s<W, 0>(t, r0, k0);
-  }
   template <int W> static __device__ __forceinline__ Frag kc(const char* t, int c0, int k0) {
     return frag_kc_s<W, 0>(t, c0, k0);
   }
-  // Columns of a slab: with two tiles of 16, column m of tile u is 8 (m / 4) + 4 u + m % 4
-  // of the slab's 32, so that the accumulators of both hold eight neighbours per lane.
+  // Of 32 columns in two tiles, column m of tile u is 8 (m / 4) + 4 u + m % 4, so that the
+  // accumulators of both hold eight neighbours per lane, as a row's fragment does.  Both
+  // tiles' addresses differ by 8 bytes (see gdr_lds.h for the exclusive or).
+  template <int W> static __device__ __forceinline__ Frag pair(const char* t, int c0, int u, int k0) {
+    const int l = lane_id(), q = l & 15, r = 8 * (l >> 4) + (q >> 2);
+    auto at = [&](int row) { return t + k0 * (2 * W) + ((prow<W>(row) * (2 * W) + (((q & 3) ^ swz<W, 0>(row)) << 4)) ^ (2 * c0)) + 8 * u; };
+    return tr_pair(at(r), at(r + 4));
+  }
+  // the accumulators' four rows of tile t
+  static __device__ __forceinline__ int row(int t, int g) { return 32 * (t >> 1) + 8 * g + 4 * (t & 1); }
   template <int VT> static __device__ __forceinline__ int col(int u, int m) {
     return VT == 2 ? 8 * (m >> 2) + 4 * u + (m & 3) : m;
   }
   template <int W, int VT> static __device__ __forceinline__ Frag slab(const char* t, int c0, int u, int k0) {
     if constexpr (VT == 1) return kc<W>(t, c0, k0);
-    const int l = lane_id(), q = l & 15, g = l >> 4, r = 8 * g + (q >> 2);
-    const int c = c0 + 8 * (q & 3) + 4 * u;
-    return tr_pair(t + soff<W, 0>(k0 + r, c), t + soff<W, 0>(k0 + r + 4, c));
+    return pair<W>(t, c0, u, k0);
   }
   static __device__ __forceinline__ void mul(Frag a, Frag b, f32x4& c) { c = mma(a, b, c); }
   static __device__ __forceinline__ Frag state(f32x4 a, f32x4 b) {
@@ -94,9 +96,10 @@ template <> struct Lin<float> {
     const int l = lane_id();
     return *reinterpret_cast<const Frag*>(t + off<W>(r0 + (l & 15), k0 + 4 * (l >> 4)));
   }
-  template <int W> static __device__ __forceinline__ Frag rk_state(const char* t, int r0, int k0) {
-    return rk<W>(t, r0, k0);
+  template <int W> static __device__ __forceinline__ Frag pair(const char* t, int c0, int u, int k0) {
+    return kc<W>(t, c0 + 16 * u, k0);
   }
+  static __device__ __forceinline__ int row(int t, int g) { return 16 * t + 4 * g; }
   template <int W> static __device__ __forceinline__ Frag kc(const char* t, int c0, int k0) {
     const int l = lane_id();
     Frag f;
@@ -222,7 +225,7 @@ struct State {
     for (int t = 0; t < KT; ++t)
 #pragma unroll
       for (int u = 0; u < VT; ++u) {
-        const int v = slab + Lin<T>::template col<VT>(u, q), k = 16 * t + 4 * g;
+        const int v = slab + Lin<T>::template col<VT>(u, q), k = Lin<T>::row(t, g);
         if (!transposed) {
           s[t][u] = *reinterpret_cast<const f32x4*>(m + v * D + k);
         } else {
@@ -237,7 +240,7 @@ struct State {
     for (int t = 0; t < KT; ++t)
 #pragma unroll
       for (int u = 0; u < VT; ++u)
-        *reinterpret_cast<f32x4*>(m + (slab + Lin<T>::template col<VT>(u, q)) * D + 16 * t + 4 * g) = s[t][u];
+        *reinterpret_cast<f32x4*>(m + (slab + Lin<T>::template col<VT>(u, q)) * D + Lin<T>::row(t, g)) = s[t][u];
   }
   __device__ __forceinline__ void decay(const Decay& d) {
 #pragma unroll
@@ -284,7 +287,7 @@ struct State {
         for (int u = 0; u < VT; ++u) x[a][u] = weighted(z[js][u], w[js], FROM + a);
 #pragma unroll
       for (int t = 0; t < KT; ++t) {
-        const Frag f = Lin<T>::template kc<D>(y, 16 * t, js * Lin<T>::KS);
+        const Frag f = Lin<T>::template pair<D>(y, 32 * (t >> 1), t & 1, js * Lin<T>::KS);
 #pragma unroll
         for (int a = 0; a < N; ++a)
 #pragma unroll
@@ -663,7 +666,7 @@ __global__ __launch_bounds__(D * 4, 2) void k_lin_out(const LinParams p, const L
     for (int ks = 0; ks < D / KS; ++ks) {
       const Frag a = Lin<T>::state(S.s[ks * KS / 16][0], S.s[ks * KS / 16 + (KS == 32)][0]);
 #pragma unroll
-      for (int it = 0; it < TI; ++it) Lin<T>::mul(a, Lin<T>::template rk_state<D>(xs, 16 * it, ks * KS), acc[it]);
+      for (int it = 0; it < TI; ++it) Lin<T>::mul(a, Lin<T>::template rk<D>(xs, 16 * it, ks * KS), acc[it]);
     }
 #pragma unroll
     for (int it = 0; it < TI; ++it)
