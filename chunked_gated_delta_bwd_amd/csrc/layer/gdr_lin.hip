@@ -9,6 +9,22 @@
 //   dv: (k, q, dO)   dk: (v, dO, q) with the transposed state's gradient, backwards,
 //   R' = c^n R + scale sum_i c^(i+1) dO_i q_i^T,  R being what the block's last token sees,
 // so one kernel, k_lin_out, computes all four.
+//
+// Long sequences are cut into segments: k_lin_local forms what each adds to the state,
+// k_lin_carry runs the states through them, and k_lin_out walks every segment from its
+// state.  The state stays in registers, 16 columns of S^T a wave, so that a block's
+// products read LDS alone; a workgroup walks one head, since a block's work (64 tokens, 4
+// MFLOP a head of 128) is a turn of a few microseconds and heads are many.
+//
+// T = 32768, 16 heads of 128, bf16 (a tensor is 134 MB): k_lin_local 70 to 85 us (two
+// tensors: 55 at the rate of a large copy), k_lin_carry 8, k_lin_out 133 to 155 for one
+// output (four tensors: 110) and 253 to 305 for the gradients of k and v together (220, or
+// 165 with what both read counted once).  Neither HBM nor any unit is full: matrix cores
+// 24 %, VALU 33 %, LDS 29 % of the cycles; what a turn waits for is the chain from LDS
+// through the products to the next, with two waves a SIMD, which the state's registers and
+// the two blocks in LDS (114 KB) allow.  Measured slower: four waves of 32 columns, and two
+// workgroups of half the registers a compute unit.  k_lin_step: 250 rows, 32 heads of 128
+// (1.02 GB of states read and written): 189 us, 5.4 TB/s.
 #include <hip/hip_runtime.h>
 
 #include "../gdr_device.h"
@@ -47,13 +63,6 @@ template <> struct Lin<bf16> {
   }
   // the accumulators' four rows of tile t
   static __device__ __forceinline__ int row(int t, int g) { return 32 * (t >> 1) + 8 * g + 4 * (t & 1); }
-  template <int VT> static __device__ __forceinline__ int col(int u, int m) {
-    return VT == 2 ? 8 * (m >> 2) + 4 * u + (m & 3) : m;
-  }
-  template <int W, int VT> static __device__ __forceinline__ Frag slab(const char* t, int c0, int u, int k0) {
-    if constexpr (VT == 1) return kc<W>(t, c0, k0);
-    return pair<W>(t, c0, u, k0);
-  }
   static __device__ __forceinline__ void mul(Frag a, Frag b, f32x4& c) { c = mma(a, b, c); }
   static __device__ __forceinline__ Frag state(f32x4 a, f32x4 b) {
     const uint2 lo = pack4_bf16(a[0], a[1], a[2], a[3]), hi = pack4_bf16(b[0], b[1], b[2], b[3]);
@@ -106,10 +115,6 @@ template <> struct Lin<float> {
 #pragma unroll
     for (int e = 0; e < 4; ++e) f[e] = *reinterpret_cast<const float*>(t + off<W>(k0 + 4 * (l >> 4) + e, c0 + (l & 15)));
     return f;
-  }
-  template <int VT> static __device__ __forceinline__ int col(int u, int m) { return 16 * u + m; }
-  template <int W, int VT> static __device__ __forceinline__ Frag slab(const char* t, int c0, int u, int k0) {
-    return kc<W>(t, c0 + 16 * u, k0);
   }
   static __device__ __forceinline__ void mul(Frag a, Frag b, f32x4& c) {
 #pragma unroll
@@ -180,75 +185,69 @@ __device__ __forceinline__ Decay decay_of(float l2, int n) {
   return {slow ? expm1f(x * 0.6931471805599453f) : exp2f(x), slow ? ~0u : 0u};
 }
 
-// 16-byte pieces of a block for each of 256 threads
-template <typename T, int D> constexpr int kPieces = Lin<T>::B * D * int(sizeof(T)) / 16 / 256;
-
+// Copies blocks of a tensor to LDS, by the D / 16 waves of a workgroup.  A lane's row and place
+// in a load of 1 KB, and the piece that belongs there, are the same in each of its loads.
 template <typename T, int D>
-__device__ __forceinline__ void load_block(const void* base, int64_t row0, int64_t stride, int n,
-                                           u32x4 (&r)[kPieces<T, D>]) {
-  constexpr int PR = D * int(sizeof(T)) / 16;   // pieces a row
-  const T* b = static_cast<const T*>(base) + row0;
-#pragma unroll
-  for (int i = 0; i < kPieces<T, D>; ++i) {
-    const int pc = i * 256 + threadIdx.x, row = pc / PR, c = pc % PR;
-    r[i] = row < n ? *reinterpret_cast<const u32x4*>(b + row * stride + c * (16 / int(sizeof(T)))) : u32x4{0, 0, 0, 0};
+struct Mover {
+  static constexpr int NW = D / 16, ROW = D * int(sizeof(T)), PR = ROW / 16, RPL = 1024 / ROW;   // pieces a row, rows a load
+  static constexpr int TB = Lin<T>::B * ROW, LPT = TB / 1024 / NW;                                // a wave's loads of a tile
+  static_assert(LPT >= 1 && TB / 1024 % NW == 0 && (NW * RPL) % 16 == 0, "the rows of a wave's loads turn alike");
+  int w, row, piece;
+  __device__ __forceinline__ explicit Mover(int wave) : w(wave) {
+    row = w * RPL + lane_id() / PR;
+    piece = (Lin<T>::template off<D>(row & 15, 0) % ROW / 16) ^ (lane_id() % PR);
   }
-}
-template <typename T, int D>
-__device__ __forceinline__ void put_block(char* tile, const u32x4 (&r)[kPieces<T, D>]) {
-  constexpr int PR = D * int(sizeof(T)) / 16;
+  // n rows from src on.  The buffer ends behind the last: no lane reads past it.  What those
+  // lanes leave in LDS is for clear().
+  __device__ __forceinline__ void operator()(const char* src, uint32_t pitch, int n, char* tile) const {
+    const __amdgpu_buffer_rsrc_t buf = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(src), 0, int(uint32_t(n - 1) * pitch + ROW), 0x00027000);
 #pragma unroll
-  for (int i = 0; i < kPieces<T, D>; ++i) {
-    const int pc = i * 256 + threadIdx.x;
-    *reinterpret_cast<u32x4*>(tile + Lin<T>::template off<D>(pc / PR, (pc % PR) * (16 / int(sizeof(T))))) = r[i];
+    for (int a = 0; a < LPT; ++a)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_void_t*)((lds_char_t*)(tile + (a * NW + w) * 1024)), 16,
+                                               (a * NW * RPL + row) * pitch + 16 * piece, 0, 0, 0);
   }
-}
+  // zeros in a tile's rows from n on, when the block has come
+  static __device__ __forceinline__ void clear(char* tile, int n) {
+    for (int a = threadIdx.x; a < (Lin<T>::B - n) * PR; a += NW * 64) *reinterpret_cast<u32x4*>(tile + n * ROW + 16 * a) = u32x4{0, 0, 0, 0};
+  }
+};
 
 // ---------------------------------------------------------------------------
-// the state of a wave: columns [slab, slab + 16 VT) of S^T, all D rows
+// the state of a wave: columns [slab, slab + 16) of S^T, all D rows
 // ---------------------------------------------------------------------------
-template <typename T, int D, int VT>
+template <typename T, int D>
 struct State {
   static constexpr int KT = D / 16, JS = Lin<T>::B / Lin<T>::KS;
-  f32x4 s[KT][VT];
+  f32x4 s[KT];
 
   __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int t = 0; t < KT; ++t)
-#pragma unroll
-      for (int u = 0; u < VT; ++u) s[t][u] = zero4();
+    for (int t = 0; t < KT; ++t) s[t] = zero4();
   }
   // memory holds [z channel][y channel], or the transpose
   __device__ __forceinline__ void load(const float* m, bool transposed, int slab) {
-    const int l = lane_id(), q = l & 15, g = l >> 4;
+    const int l = lane_id(), g = l >> 4, v = slab + (l & 15);
 #pragma unroll
-    for (int t = 0; t < KT; ++t)
+    for (int t = 0; t < KT; ++t) {
+      const int k = Lin<T>::row(t, g);
+      if (!transposed) {
+        s[t] = *reinterpret_cast<const f32x4*>(m + v * D + k);
+      } else {
 #pragma unroll
-      for (int u = 0; u < VT; ++u) {
-        const int v = slab + Lin<T>::template col<VT>(u, q), k = Lin<T>::row(t, g);
-        if (!transposed) {
-          s[t][u] = *reinterpret_cast<const f32x4*>(m + v * D + k);
-        } else {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) s[t][u][r] = m[(k + r) * D + v];
-        }
+        for (int r = 0; r < 4; ++r) s[t][r] = m[(k + r) * D + v];
       }
+    }
   }
   __device__ __forceinline__ void store(float* m, int slab) const {
-    const int l = lane_id(), q = l & 15, g = l >> 4;
+    const int l = lane_id(), g = l >> 4, v = slab + (l & 15);
 #pragma unroll
-    for (int t = 0; t < KT; ++t)
-#pragma unroll
-      for (int u = 0; u < VT; ++u)
-        *reinterpret_cast<f32x4*>(m + (slab + Lin<T>::template col<VT>(u, q)) * D + Lin<T>::row(t, g)) = s[t][u];
+    for (int t = 0; t < KT; ++t) *reinterpret_cast<f32x4*>(m + v * D + Lin<T>::row(t, g)) = s[t];
   }
   __device__ __forceinline__ void decay(const Decay& d) {
 #pragma unroll
     for (int t = 0; t < KT; ++t)
 #pragma unroll
-      for (int u = 0; u < VT; ++u)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) s[t][u][r] = d(s[t][u][r]);
+      for (int r = 0; r < 4; ++r) s[t][r] = d(s[t][r]);
   }
   // S^T += y^T (w z).  The weighted z of bf16 tensors is a sum of bf16 parts: three (24 bits of
   // significand, as fp32) for states that are returned or that another segment starts from,
@@ -276,22 +275,18 @@ struct State {
   }
   // parts FROM .. TO - 1
   template <int FROM, int TO>
-  __device__ __forceinline__ void add(const char* y, const Frag (&z)[JS][VT], const float (&w)[JS][Lin<T>::E]) {
+  __device__ __forceinline__ void add(const char* y, const Frag (&z)[JS], const float (&w)[JS][Lin<T>::E]) {
     constexpr int N = sizeof(T) == 4 ? 1 : TO - FROM;
 #pragma unroll
     for (int js = 0; js < JS; ++js) {
-      Frag x[N][VT];
+      Frag x[N];
 #pragma unroll
-      for (int a = 0; a < N; ++a)
-#pragma unroll
-        for (int u = 0; u < VT; ++u) x[a][u] = weighted(z[js][u], w[js], FROM + a);
+      for (int a = 0; a < N; ++a) x[a] = weighted(z[js], w[js], FROM + a);
 #pragma unroll
       for (int t = 0; t < KT; ++t) {
         const Frag f = Lin<T>::template pair<D>(y, 32 * (t >> 1), t & 1, js * Lin<T>::KS);
 #pragma unroll
-        for (int a = 0; a < N; ++a)
-#pragma unroll
-          for (int u = 0; u < VT; ++u) Lin<T>::mul(f, x[a][u], s[t][u]);
+        for (int a = 0; a < N; ++a) Lin<T>::mul(f, x[a], s[t]);
       }
     }
   }
@@ -336,49 +331,57 @@ __global__ __launch_bounds__(256) void k_lin_table(const LinParams p, const LinB
 // a segment's own contribution to the state after it (before it, backwards)
 // ---------------------------------------------------------------------------
 template <typename T, int D, bool REV>
-__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_lin_local(const LinParams p) {
-  constexpr int kB = Lin<T>::B, TB = kB * D * int(sizeof(T)), VT = D / 64, JS = kB / Lin<T>::KS;
-  __shared__ __attribute__((aligned(1024))) char ys[TB], zs[TB];
+__global__ __launch_bounds__(D * 4, 2) void k_lin_local(const LinParams p) {
+  constexpr int kB = Lin<T>::B, JS = kB / Lin<T>::KS, TB = Mover<T, D>::TB, ROW = Mover<T, D>::ROW;
+  __shared__ __attribute__((aligned(1024))) char tiles0[2][TB], tiles1[2][TB];   // apart, as in k_lin_out
   int c, h;
   place_of(p, int(blockIdx.x), c, h);
   const LinSeg sg = seg_at(p, c);
   if (REV ? sg.idx == 0 : sg.idx == sg.nseg - 1) return;   // nothing starts from it
-  const int yH = p.Hk, yh = h / p.G;
-  const void *y = REV ? p.q : p.k, *z = REV ? p.dO : p.v;
-  const float l2 = decay2(p, h), wscale = REV ? p.scale : 1.f;
-  const int slab = wave_id() * 16 * VT, nb = (sg.len + kB - 1) / kB;
-  State<T, D, VT> S;
+  const float l2 = decay2(p, h);
+  const int w = __builtin_amdgcn_readfirstlane(wave_id()), slab = w * 16, nb = (sg.len + kB - 1) / kB;
+  const int n_last = sg.len - (nb - 1) * kB;
+  auto rows = [&](int i) { return i == (REV ? 0 : nb - 1) ? n_last : kB; };   // of the walk's i-th block
+  const Mover<T, D> mover(w);
+  const int64_t t0 = sg.t0 + (REV ? (nb - 1) * kB : 0), step = REV ? -kB : kB;
+  const uint32_t pitch[2] = {uint32_t(p.Hk) * ROW, uint32_t(p.H) * ROW};
+  const char* src[2] = {static_cast<const char*>(REV ? p.q : p.k) + (t0 * p.Hk + h / p.G) * ROW,
+                        static_cast<const char*>(REV ? p.dO : p.v) + (t0 * p.H + h) * ROW};
+  auto load = [&](int i, auto& tiles, int m) {
+    mover(src[m], pitch[m], rows(i), tiles[m]);
+    src[m] += step * pitch[m];
+  };
+  load(0, tiles0, 0);
+  load(0, tiles0, 1);
+  State<T, D> S;
   S.zero();
-  float w[JS][Lin<T>::E];
+  float wz[JS][Lin<T>::E];
   Decay over = {};   // a block
   int wn = -1;
-  u32x4 yr[kPieces<T, D>], zr[kPieces<T, D>];
-  auto load = [&](int i) {
-    const int b = REV ? nb - 1 - i : i, n = min(kB, sg.len - b * kB);
-    const int64_t t = sg.t0 + int64_t(b) * kB;
-    load_block<T, D>(y, (t * yH + yh) * D, int64_t(yH) * D, n, yr);
-    load_block<T, D>(z, (t * p.H + h) * D, int64_t(p.H) * D, n, zr);
-  };
-  load(0);
-  for (int i = 0; i < nb; ++i) {
-    const int b = REV ? nb - 1 - i : i, n = min(kB, sg.len - b * kB);
+  auto turn = [&](int i, auto& tiles, auto& next) {
+    wait_vm<0>();
+    chain_barrier();
+    const int n = rows(i);
     if (n != wn) {
-      state_weights<T, REV>(l2, n, wscale, w);
+      state_weights<T, REV>(l2, n, REV ? p.scale : 1.f, wz);
       over = decay_of(l2, n);
       wn = n;
     }
-    chain_barrier();
-    put_block<T, D>(ys, yr);
-    put_block<T, D>(zs, zr);
-    if (i + 1 < nb) load(i + 1);
-    chain_barrier();
-    typename Lin<T>::Frag zf[JS][VT];
+    if (n < kB) {
+      for (int m = 0; m < 2; ++m) mover.clear(tiles[m], n);
+      chain_barrier();
+    }
+    typename Lin<T>::Frag zf[JS];
 #pragma unroll
-    for (int js = 0; js < JS; ++js)
-#pragma unroll
-      for (int u = 0; u < VT; ++u) zf[js][u] = Lin<T>::template slab<D, VT>(zs, slab, u, js * Lin<T>::KS);
+    for (int js = 0; js < JS; ++js) zf[js] = Lin<T>::template kc<D>(tiles[1], slab, js * Lin<T>::KS);
+    if (i + 1 < nb) load(i + 1, next, 0);
     S.decay(over);
-    S.template add<0, 3>(ys, zf, w);
+    if (i + 1 < nb) load(i + 1, next, 1);
+    S.template add<0, 3>(tiles[0], zf, wz);
+  };
+  for (int i = 0; i < nb; i += 2) {
+    turn(i, tiles0, tiles1);
+    if (i + 1 < nb) turn(i + 1, tiles1, tiles0);
   }
   S.store((REV ? p.dst : p.st) + (int64_t(c) * p.H + h) * (D * D), slab);
 }
@@ -454,12 +457,9 @@ template <typename T, int D, bool REV>
 __global__ __launch_bounds__(D * 4, 2) void k_lin_out(const LinParams p, const LinRoles roles) {
   typedef typename Lin<T>::Frag Frag;
   constexpr int kB = Lin<T>::B, KS = Lin<T>::KS, JS = kB / KS, E = Lin<T>::E, TI = kB / 16;
-  constexpr int NW = D / 16;                                               // waves
-  constexpr int ROW = D * int(sizeof(T)), TB = kB * ROW, PR = ROW / 16;   // bytes of a row and a tile, pieces of a row
-  constexpr int LPT = TB / 1024 / NW, RPL = 1024 / ROW;                    // a wave's 1 KB loads of a tile, rows of a load
+  constexpr int NW = Mover<T, D>::NW, ROW = Mover<T, D>::ROW, TB = Mover<T, D>::TB;
   constexpr int NPAIR = TI * TI / NW > 0 ? TI * TI / NW : 1, JSTEP = NW / TI;   // a wave's tiles of pairs
   constexpr int PB = kB * kB * int(sizeof(T));
-  static_assert(LPT >= 1 && TB / 1024 % NW == 0 && (NW * RPL) % 16 == 0, "the rows of a wave's loads turn alike");
   // Arrays of their own, each named where it is used: of one array with two halves the
   // compiler takes it that a read may meet the loads on their way, and waits for them.
   __shared__ __attribute__((aligned(1024))) char tiles0[3][TB], tiles1[3][TB], pairs0[PB], pairs1[PB];
@@ -484,8 +484,7 @@ __global__ __launch_bounds__(D * 4, 2) void k_lin_out(const LinParams p, const L
   const int64_t sh = int64_t(sg.seq) * p.H + h;
   const int n_last = sg.len - (nb - 1) * kB;
   auto rows = [&](int i) { return i == (REV ? 0 : nb - 1) ? n_last : kB; };   // of the walk's i-th block
-  // A lane's row and place in a load, and the piece that belongs there
-  const int lrow = w * RPL + l / PR, piece = (Lin<T>::template off<D>(lrow & 15, 0) % ROW / 16) ^ (l % PR);
+  const Mover<T, D> mover(w);
   // Where the walk's next block begins, of x, y and z and of the output, and the bytes between rows
   const int64_t t0 = sg.t0 + (REV ? (nb - 1) * kB : 0);
   const int OB = o.wide ? 4 : int(sizeof(T));
@@ -501,20 +500,14 @@ __global__ __launch_bounds__(D * 4, 2) void k_lin_out(const LinParams p, const L
   const uint32_t out_pitch = uint32_t(p.H) * D * OB;
   char* out = static_cast<char*>(o.out) + (t0 * p.H + h) * (D * OB);
   auto load = [&](int i, auto& tiles, int m) {
-    // The buffer ends behind the block's last row: no lane reads past it.  What those lanes
-    // leave in LDS is cleared when the block has come.
-    const __amdgpu_buffer_rsrc_t buf = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(src[m]), 0, int(uint32_t(rows(i) - 1) * pitch[m] + ROW), 0x00027000);
-#pragma unroll
-    for (int a = 0; a < LPT; ++a)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_void_t*)((lds_char_t*)(tiles[m] + (a * NW + w) * 1024)), 16,
-                                               (a * NW * RPL + lrow) * pitch[m] + 16 * piece, 0, 0, 0);
+    mover(src[m], pitch[m], rows(i), tiles[m]);
     src[m] += (REV ? -int64_t(kB) : int64_t(kB)) * pitch[m];
   };
   if (nb) {
 #pragma unroll
     for (int m = 0; m < 3; ++m) load(0, tiles0, m);
   }
-  State<T, D, 1> S;
+  State<T, D> S;
   const bool start = REV ? sg.idx == sg.nseg - 1 : sg.idx == 0, end = REV ? sg.idx == 0 : sg.idx == sg.nseg - 1;
   const bool exact = end && o.last;
   if (!start) S.load(o.st + (int64_t(c) * p.H + h) * (D * D), o.transposed, slab);
@@ -632,8 +625,7 @@ __global__ __launch_bounds__(D * 4, 2) void k_lin_out(const LinParams p, const L
       wn = n;
     }
     if (n < kB) {
-      for (int m = 0; m < 3; ++m)
-        for (int a = threadIdx.x; a < (kB - n) * PR; a += NW * 64) *reinterpret_cast<u32x4*>(tiles[m] + n * ROW + 16 * a) = u32x4{0, 0, 0, 0};
+      for (int m = 0; m < 3; ++m) mover.clear(tiles[m], n);
       chain_barrier();
     }
     const char *const xs = tiles[0], *const ys = tiles[1], *const zs = tiles[2];
@@ -641,7 +633,7 @@ __global__ __launch_bounds__(D * 4, 2) void k_lin_out(const LinParams p, const L
     finish(i - 1, ps_before);
     if (i + 1 < nb) load(i + 1, next, 0);
 #pragma unroll
-    for (int js = 0; js < JS; ++js) zf[js] = Lin<T>::template slab<D, 1>(zs, slab, 0, js * KS);
+    for (int js = 0; js < JS; ++js) zf[js] = Lin<T>::template kc<D>(zs, slab, js * KS);
     // Infinities and NaN in z: a zero pair times one would reach tokens before it, so the
     // products take zeros in their place, and what comes from that token on is NaN: bad_from, in
     // the order of the walk, for the lane's column.
@@ -664,7 +656,7 @@ __global__ __launch_bounds__(D * 4, 2) void k_lin_out(const LinParams p, const L
     for (int it = 0; it < TI; ++it) acc[it] = zero4();
 #pragma unroll
     for (int ks = 0; ks < D / KS; ++ks) {
-      const Frag a = Lin<T>::state(S.s[ks * KS / 16][0], S.s[ks * KS / 16 + (KS == 32)][0]);
+      const Frag a = Lin<T>::state(S.s[ks * KS / 16], S.s[ks * KS / 16 + (KS == 32)]);
 #pragma unroll
       for (int it = 0; it < TI; ++it) Lin<T>::mul(a, Lin<T>::template rk<D>(xs, 16 * it, ks * KS), acc[it]);
     }
@@ -674,17 +666,14 @@ __global__ __launch_bounds__(D * 4, 2) void k_lin_out(const LinParams p, const L
       for (int r = 0; r < 4; ++r) acc[it][r] *= far[it];
     if (i + 1 < nb) load(i + 1, next, 1);
     S.decay(over);
-    Frag zv[JS][1];
-#pragma unroll
-    for (int js = 0; js < JS; ++js) zv[js][0] = zf[js];
-    S.template add<0, 2>(ys, zv, wz);
-    if (sizeof(T) == 2 && exact) S.template add<2, 3>(ys, zv, wz);
+    S.template add<0, 2>(ys, zf, wz);
+    if (sizeof(T) == 2 && exact) S.template add<2, 3>(ys, zf, wz);
     if (i + 1 < nb) load(i + 1, next, 2);
     if (odd && bad_from < kB) {
 #pragma unroll
       for (int t = 0; t < D / 16; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) S.s[t][0][r] = __builtin_nanf("");
+        for (int r = 0; r < 4; ++r) S.s[t][r] = __builtin_nanf("");
     }
     if (!early) pairs(tiles, ps);
   };
@@ -792,8 +781,8 @@ template <typename T, int D>
 int states(const LinParams& p, bool backward, hipStream_t s) {
   if (!p.split) return 0;
   const unsigned grid = unsigned(int64_t(p.NC) * p.H);
-  if (backward) k_lin_local<T, D, true><<<grid, 256, 0, s>>>(p);
-  else k_lin_local<T, D, false><<<grid, 256, 0, s>>>(p);
+  if (backward) k_lin_local<T, D, true><<<grid, D * 4, 0, s>>>(p);
+  else k_lin_local<T, D, false><<<grid, D * 4, 0, s>>>(p);
   if (const int e = last_error()) return e;
   const unsigned carry = unsigned(int64_t(p.N) * p.H * (D * D / 1024));
   if (backward) k_lin_carry<D, true><<<carry, 256, 0, s>>>(p);

@@ -5,7 +5,9 @@
 // 8 rg .. + 7 and columns 8 cg .. + 7), so that x is read once whatever direction the
 // scales run in: largest magnitudes of rows are reduced over 16 lanes, of columns over 4
 // lanes and 4 waves, of the block over both.  A transposed tile turns around in LDS as
-// bytes.  Streaming work, bound by HBM.
+// bytes.  Streaming work, bound by HBM: 4096 x 4096 bf16 to blocks, transposed, 11.2 us
+// (50 MB, 4.5 TB/s); 8192 x 4096, rows, 27.3 (the kernel; 101 MB, 3.7 TB/s) and transposed
+// 23.3 (4.4 TB/s).
 #include <hip/hip_runtime.h>
 
 #include "../gdr_device.h"
