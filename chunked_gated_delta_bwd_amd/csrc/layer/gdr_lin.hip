@@ -156,7 +156,9 @@ __device__ __forceinline__ LinSeg seg_at(const LinParams& p, int s) {
 }
 
 // Segment and head of a workgroup: the heads of a segment one after the other, since their
-// rows lie side by side.  Value heads that share q and k go to one XCD (see chunk_head_at).
+// rows lie side by side (T = 32768, 16 heads of 128, training: 718 us, and 733 with the
+// segments of a head one after the other).  Value heads that share q and k go to one XCD
+// (see chunk_head_at).
 __device__ __forceinline__ void place_of(const LinParams& p, int id, int& c, int& h) {
   if (p.G > 1) {
     chunk_head_at(p, id, c, h);
@@ -448,7 +450,6 @@ struct LinRole {
 struct LinRoles {
   LinRole r[2];
   int32_t n;
-  int32_t flip;           // last segment first: what the kernel before has read last is still near
 };
 
 // A wave holds 16 columns of S^T (channels of z) in registers.  The tiles of x, y and z are
@@ -476,7 +477,7 @@ __global__ __launch_bounds__(D * 4, 2) void k_lin_out(const LinParams p, const L
     }
   }
   const LinRole o = roles.r[role];
-  place_of(p, roles.flip ? places - 1 - id : id, c, h);
+  place_of(p, id, c, h);
   const LinSeg sg = seg_at(p, c);
   const int l = lane_id(), q = l & 15, g = l >> 4, w = __builtin_amdgcn_readfirstlane(wave_id());
   const int slab = w * 16, nb = (sg.len + kB - 1) / kB;
@@ -799,7 +800,7 @@ int out(const LinParams& p, const LinRoles& r, hipStream_t s) {
 template <typename T, int D>
 int fwd(const LinParams& p, hipStream_t s) {
   const LinRole o = {p.q, p.k, p.v, p.o, p.ht, p.h0, p.st, 1, 1, 0, 0, p.scale, p.scale, 1.f, 0};
-  return out<T, D, false>(p, {{o, o}, 1, 1}, s);
+  return out<T, D, false>(p, {{o, o}, 1}, s);
 }
 
 template <typename T, int D>
@@ -814,9 +815,9 @@ int bwd(const LinParams& p, hipStream_t s) {
   const LinRole q = {p.dO, p.v, p.k, grouped ? part : p.dq, nullptr, p.h0, p.st, 0, 0, 1, 1, p.scale, p.scale, 1.f, grouped};
   const LinRole k = {p.v, p.dO, p.q, grouped ? part : p.dk, nullptr, p.dht, p.dst, 0, 0, 1, 1, p.scale, 1.f, p.scale, grouped};
   const LinRole v = {p.k, p.q, p.dO, p.dv, p.dh0, p.dht, p.dst, 1, 1, 0, 0, p.scale, 1.f, p.scale, 0};
-  if (const int e = out<T, D, false>(p, {{q, q}, 1, 1}, s)) return e;
+  if (const int e = out<T, D, false>(p, {{q, q}, 1}, s)) return e;
   if (const int e = sum(p.dq)) return e;
-  if (const int e = out<T, D, true>(p, {{k, v}, 2, 0}, s)) return e;
+  if (const int e = out<T, D, true>(p, {{k, v}, 2}, s)) return e;
   return sum(p.dk);
 }
 
