@@ -22,7 +22,7 @@ BLOCK = 64
 def _factors(x, lam, nb):
     low = x.dtype is torch.bfloat16
     D = x.shape[-1]
-    fp32 = (2 * D + 3 * BLOCK + 8 * nb + 32 + 16 * BLOCK * min(float(-lam), 8.0)) * U
+    fp32 = (2 * D + 3 * BLOCK + 8 * nb + 32 + 16 * BLOCK * min(abs(float(lam)), 8.0)) * U
     return (2.0 ** -8 if low else 0.0), fp32
 
 

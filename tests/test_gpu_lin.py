@@ -93,9 +93,9 @@ def test_forward_and_backward(lengths, H, Hk, D, h0, dht, packed, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("lam", [0.0, -1e-6, -20.0, -1e4, float("-inf")])
+@pytest.mark.parametrize("lam", [0.0, -1e-6, -20.0, -1e4, float("-inf"), 0.02])
 def test_decays(lam, dtype):
-    """No decay, one that rounds away in a token, and ones that leave nothing of the state."""
+    """No decay, one that rounds away in a token, ones that leave nothing of the state, and growth."""
     lengths, H, D = [400, 70], 2, 64
     t, dO, dht = make(3, lengths, H, H, D, dtype, lam=[lam, -0.01])
     ref = L.lin(t["q"], t["k"], t["v"], t["log_decay"], t["h0"], lengths, 1.0, dO, dht)

@@ -272,6 +272,34 @@ def test_attention_beyond_32_bits():
         assert not x[:-tail].any() and not x[:, :-heads].any(), m
 
 
+@pytest.mark.parametrize("T,dtype,Hk", [(65, BF, 1 << 16), (65, BF, 1 << 15), (33, F32, 1 << 16)])
+def test_the_most_heads(T, dtype, Hk):
+    """2^16 heads: a block's rows reach 2^31 bytes from its first (dq and dk of grouped heads, and
+    fp32 tensors).  The last heads' tokens, zeros elsewhere."""
+    H, D, heads = 1 << 16, 128, 2
+    G, gen = H // Hk, torch.Generator().manual_seed(6)
+    hk = heads // G
+    small = {m: R.rand(gen, T, heads if m == "v" else hk, D, std=D ** -0.5).to(dtype) for m in "qkv"}
+    g, decay = R.rand(gen, T, heads, D).to(dtype), -torch.rand(H, generator=gen)
+    ref = L.lin(small["q"], small["k"], small["v"], decay[-heads:], None, [T], 1.0, g)
+
+    def big(x, n):
+        y = torch.zeros(T, n, D, dtype=dtype, device="cuda")
+        y[:, -x.shape[1]:] = x.cuda()
+        return y
+
+    t = {**{m: big(x, H if m == "v" else Hk) for m, x in small.items()}, "log_decay": decay.cuda()}
+    prob = B.LinProblem(1, T, H, D, 1, B.GDR_BF16 if dtype is BF else B.GDR_F32, 1.0, Hk=Hk)
+    ws, o, dO = B.alloc_lin_workspace(prob, backward=True), torch.full_like(t["v"], float("nan")), big(g, H)
+    B.gdr_lin_fwd(prob, t, ws, o)
+    out = {m: torch.full_like(t[m[1]], float("nan")) for m in ("dq", "dk", "dv")}
+    B.gdr_lin_bwd(prob, t, dO, None, ws, out)
+    for m, x in (("o", o), *out.items()):
+        n = heads if m in ("o", "dv") else hk
+        R.check(m, x[:, -n:], *ref[m])
+        assert not x[:, :-n].any(), m
+
+
 def test_pool_beyond_32_bits():
     N, H, D, P = 3, 16, 128, 16500
     gen = torch.Generator().manual_seed(2)
@@ -314,6 +342,31 @@ def test_product_beyond_32_bits(M, N, K, dtype):
     B.gdr_gemm(prob, a, sa, b.cuda(), sb.cuda(), c, B.alloc_gemm_workspace(prob))
     R.check("c", c[-last:], *L.product(a[-last:].cpu(), sa[-last:].cpu(), b, sb, 128, dtype))
     assert not c[:-last].any()
+
+
+@pytest.mark.parametrize("M,N,K", [(130, 20, 1 << 22), (130, 20, (1 << 22) + 4), (40, 300, 1 << 22), (5, 20, (1 << 24) + 1)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_long_contractions(M, N, K, dtype):
+    """The longest whose rows go to LDS directly, and longer ones: zeros but for the first and last
+    200 of the contraction."""
+    gen = torch.Generator().manual_seed(7)
+    G, at = -(-K // 128), K % 128 or 128                              # at: of the last group
+
+    def sparse(rows):
+        x = torch.zeros(rows, K, dtype=torch.uint8, device="cuda")
+        first, last = (R.rand(gen, rows, 200).to(F8) for _ in range(2))
+        x[:, :200], x[:, -200:] = first.view(torch.uint8).cuda(), last.view(torch.uint8).cuda()
+        s = torch.rand(rows if rows == M else -(-rows // 128), G, generator=gen)
+        # the same product over the groups at both ends alone
+        y = torch.cat([x[:, :256], x[:, K - at - 256:]], 1).cpu().view(F8)
+        return (x.view(F8), s.cuda()), (y, torch.cat([s[:, :2], s[:, -3:]], 1))
+
+    (a, sa), short_a = sparse(M)
+    (b, sb), short_b = sparse(N)
+    c = dev(M, N, dtype=dtype)
+    prob = B.GemmProblem(M, N, K, B.GDR_BF16 if dtype is BF else B.GDR_F32)
+    B.gdr_gemm(prob, a, sa, b, sb, c, B.alloc_gemm_workspace(prob))
+    R.check("c", c, *L.product(*short_a, *short_b, 128, dtype))
 
 
 @pytest.mark.parametrize("M,K", [(3, 4112), (32, 4111)])
