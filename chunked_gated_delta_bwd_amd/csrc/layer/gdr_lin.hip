@@ -13,7 +13,7 @@
 // Long sequences are cut into segments: k_lin_local forms what each adds to the state,
 // k_lin_carry runs the states through them, and k_lin_out walks every segment from its
 // state.  The state stays in registers, 16 columns of S^T a wave, so that a block's
-// products read LDS alone; a workgroup walks one head, since a block's work (64 tokens, 4
+// products read LDS alone; a workgroup walks one head, since a block's work (64 tokens, 6
 // MFLOP a head of 128) is a turn of a few microseconds and heads are many.
 //
 // T = 32768, 16 heads of 128, bf16 (a tensor is 134 MB): k_lin_local 70 to 85 us (two
@@ -446,7 +446,8 @@ struct LinRole {
   int32_t wide;           // out is fp32 (a value head's share of the gradient of a grouped q or k)
 };
 // One launch: n roles that walk the same way.  Two workgroups on one XCD, started together,
-// take the two roles of a segment and head: what both read comes from HBM once.
+// take the two roles of a segment and head, so that much of what both read comes from HBM
+// once (T = 32768, 16 heads of 128, dk and dv: 0.57 GB fetched of 0.81 GB read).
 struct LinRoles {
   LinRole r[2];
   int32_t n;
