@@ -43,13 +43,21 @@ gdr_status check_gemm_shape(const gdr_gemm_shape* s) {
 
 // The cut, by what was measured in us (M x N x K; bf16 results unless f32 is said):
 //                              64 x 128   128 x 128   256 x 256
-//   512 x 4096 x 4096             21.6        30.3         -
-//   2048 x 2048 x 2048            15.3        16.7        28.9
-//   2048 x 2048 x 2048, f32       27.2        32.0         -
+//   512 x 4096 x 4096             22.3        32.1         -
+//   1024 x 4096 x 4096            30.5        34.4         -
+//   2048 x 2048 x 2048            17.4        19.0        28.9
+//   2048 x 2048 x 2048, f32       25.9        31.6         -
+//   2304 x 2048 x 2048            26.3        21.8         -
+//   2560 x 2048 x 2048, f32       38.5        40.4         -
+//   3500 x 2048 x 2048, f32       45.5        42.6         -
+//   4096 x 2048 x 8192            98.5        72.5         -
 //   4096 x 2048 x 8192, rows     118          94.2       143
 //   4096 x 4096 x 4096            97.3        79.5        68.3
-//   8192 x 4096 x 256             33.8        27.3        31.9
+//   8192 x 4096 x 256             35.3        26.0        31.9
 //   32768 x 4096 x 4096          843         655         519
+// Two workgroups of 64 x 128 fit a compute unit: up to 512 they run together, and are the
+// shorter ones.  With fp32 results, where the instructions take twice as long, so they are a
+// little beyond.
 // A split contraction pays where few workgroups leave most compute units idle: 64 x 4096 x
 // 4096 with 32 workgroups 12.9 in 4 runs, 14.1 in 2, 16.2 as one for every 16 rows of b;
 // 256 x 4096 x 4096 with 128 workgroups 17.3 whole, 21.4 in 2 runs.  Rows that pass through
@@ -62,9 +70,9 @@ gdr::GemmPlan gemm_plan(const gdr_gemm_shape* s) {
   const int32_t copy = s->K % 4 == 0 && s->K <= (1 << 22);   // 256 rows within 32 bits
   if (copy && s->dtype == GDR_BF16 && groups >= 8 && ceil_div(s->M, 256) * ceil_div(s->N, 256) >= 256)
     return {gdr::kGemmLarge, 1, copy};
-  if (ceil_div(s->M, 128) * ceil_div(s->N, 128) >= 512) return {gdr::kGemmMedium, 1, copy};
   const int64_t tiles = ceil_div(s->M, 64) * ceil_div(s->N, 128);
-  const int64_t splits = std::min<int64_t>(tiles <= 64 ? 4 : !copy && tiles < 512 ? 2 : 1, groups / 8);
+  if (tiles > (s->dtype == GDR_BF16 ? 512 : 768)) return {gdr::kGemmMedium, 1, copy};
+  const int64_t splits = std::min<int64_t>(tiles <= 64 ? 4 : !copy && tiles <= 512 ? 2 : 1, groups / 8);
   if (splits < 2) return {gdr::kGemmSmall, 1, copy};
   // no run without a group: the last one may be shorter than the others
   return {gdr::kGemmSmall, int32_t(ceil_div(groups, ceil_div(groups, splits))), copy};
