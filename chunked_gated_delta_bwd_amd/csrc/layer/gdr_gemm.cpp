@@ -52,12 +52,20 @@ gdr_status check_gemm_shape(const gdr_gemm_shape* s) {
 //   3500 x 2048 x 2048, f32       45.5        42.6         -
 //   4096 x 2048 x 8192            98.5        72.5         -
 //   4096 x 2048 x 8192, rows     118          94.2       143
+//   2048 x 4096 x 4096            55.5        40.5        52.1
+//   2560 x 4096 x 4096             -          68.4        56.3
+//   3584 x 4096 x 4096             -          83.8        69.0
 //   4096 x 4096 x 4096            97.3        79.5        68.3
+//   4400 x 4096 x 4096             -         108.2       108.7
+//   10000 x 4096 x 4096            -         199         169
+//   4096 x 4096 x 512             24.1        19.0        18.1
 //   8192 x 4096 x 256             35.3        26.0        31.9
 //   32768 x 4096 x 4096          843         655         519
 // Two workgroups of 64 x 128 fit a compute unit: up to 512 they run together, and are the
 // shorter ones.  With fp32 results, where the instructions take twice as long, so they are a
 // little beyond.
+// One of 256 x 256 fills a compute unit as two of 128 x 128 do; a round of them takes about
+// 4 / 3 of the other's time.
 // A split contraction pays where few workgroups leave most compute units idle: 64 x 4096 x
 // 4096 with 32 workgroups 12.9 in 4 runs, 14.1 in 2, 16.2 as one for every 16 rows of b;
 // 256 x 4096 x 4096 with 128 workgroups 17.3 whole, 21.4 in 2 runs.  Rows that pass through
@@ -68,8 +76,9 @@ gdr::GemmPlan gemm_plan(const gdr_gemm_shape* s) {
   const int64_t groups = ceil_div(s->K, gdr::kGroup);
   if (s->M <= gdr::kFewRows) return {gdr::kGemmFew, 1, 0};
   const int32_t copy = s->K % 4 == 0 && s->K <= (1 << 22);   // 256 rows within 32 bits
-  if (copy && s->dtype == GDR_BF16 && groups >= 8 && ceil_div(s->M, 256) * ceil_div(s->N, 256) >= 256)
-    return {gdr::kGemmLarge, 1, copy};
+  const int64_t large = ceil_div(ceil_div(s->M, 256) * ceil_div(s->N, 256), 256);
+  const int64_t medium = ceil_div(ceil_div(s->M, 128) * ceil_div(s->N, 128), 512);
+  if (copy && s->dtype == GDR_BF16 && groups >= 4 && 4 * large < 3 * medium) return {gdr::kGemmLarge, 1, copy};
   const int64_t tiles = ceil_div(s->M, 64) * ceil_div(s->N, 128);
   if (tiles > (s->dtype == GDR_BF16 ? 512 : 768)) return {gdr::kGemmMedium, 1, copy};
   const int64_t splits = std::min<int64_t>(tiles <= 64 ? 4 : !copy && tiles <= 512 ? 2 : 1, groups / 8);

@@ -59,9 +59,10 @@ def test_product(M, N, K, block, dtype):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("block", [1, 128])
-@pytest.mark.parametrize("M,N,K", [(3584, 3600, 272), (4096, 3328, 256)])
+@pytest.mark.parametrize("M,N,K", [(3584, 3600, 272), (4096, 3328, 256), (2500, 3500, 652), (2560, 3340, 512), (2817, 2817, 1040)])
 def test_large_tiles(M, N, K, block, dtype):
-    """Enough rows and columns for the largest tiles, whole and cut; a last group of 16."""
+    """Enough rows and columns for the larger tiles and, from K = 512 on with a bf16 result, the largest,
+    whole and cut; last groups of 16 and of 12."""
     a, sa, b, sb = make(M, M, N, K, block)
     c = gemm(B.GemmProblem(M, N, K, CODE[dtype], block=block), a, sa, b, sb, dtype)
     want, err = L.product(a, sa, b, sb, block, DT[dtype])
@@ -80,7 +81,7 @@ def test_small_numbers_are_exact(M, N, K, block):
     assert torch.equal(c.cpu().double(), L.product(a.to(F8), sa, b.to(F8), sb, block)[0])
 
 
-@pytest.mark.parametrize("M,N,K", [(20, 50, 300), (200, 150, 300), (3584, 3584, 256)])
+@pytest.mark.parametrize("M,N,K", [(20, 50, 300), (200, 150, 300), (3584, 3584, 256), (2600, 3500, 650), (2600, 3500, 656)])
 def test_nan_stays_in_its_row_and_column(M, N, K):
     """A NaN byte or scale of a reaches its row of c, of b its column (a block's scale: its 128)."""
     a, sa, b, sb = make(2, M, N, K, 128)

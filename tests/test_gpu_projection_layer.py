@@ -329,6 +329,7 @@ def e4m3_rows(gen, rows, K, last):
     (1050000, 256, 4112, BF),      # rows of 16 bytes
     (1050000, 200, 4111, F32),     # rows through registers
     (4200000, 1040, 128, BF),      # c
+    (4200000, 1040, 516, BF),      # c, the largest tiles
     (4200000, 1030, 130, F32),
 ])
 def test_product_beyond_32_bits(M, N, K, dtype):
