@@ -368,7 +368,9 @@ gdr_status gdr_norm_bwd(const gdr_norm_shape* shape, const void* r, const float*
  * range for every n up to the longest sequence.
  * States, products and sums are fp32.  With bf16 tensors the products of pairs of
  * tokens and the states are rounded to bf16 once where they are multiplied with
- * bf16 tensors; the states themselves, returned or not, are not.  An infinity or NaN
+ * bf16 tensors; the states themselves are not: what a block adds to one keeps 16 bits
+ * of significand, or 24 where the state is returned or starts another run of tokens, so
+ * that asking for ht (dh0) may change the last bit of some o (dv).  An infinity or NaN
  * at a token reaches no token before it (after it, in the gradients of k and v) and no
  * other sequence; from there on, what the formulas make infinite or NaN is infinite or
  * NaN, not always the same of the two.  GDR_EUNSUPPORTED above 2^16 heads, and from

@@ -298,6 +298,30 @@ def test_streams_graphs_and_two_calls_at_once():
         assert same(ref, cap) and torch.equal(pool, want) and torch.equal(step_o, y)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_states_not_asked_for_and_a_second_backward(dtype):
+    """Without ht and dh0 everything is within the same bounds (fp32: the same bits); a second
+    backward on the same workspace gives the same bits."""
+    lengths, H, Hk, D = [700, 64, 3], 4, 2, 128
+    t, dO, dht = make(23, lengths, H, Hk, D, dtype)
+    ref = L.lin(t["q"], t["k"], t["v"], t["log_decay"], t["h0"], lengths, 1.0, dO, dht)
+    prob, d, dO, dht = problem(lengths, H, Hk, D, dtype, 1.0), cuda(t), dO.cuda(), dht.cuda()
+    full, bare, again = buffers(t), buffers(t), buffers(t)
+    full["ht"], full["dh0"] = nan_like(t["h0"]), nan_like(t["h0"])
+    ws = go(prob, d, dO, dht, full)
+    again["dh0"] = nan_like(t["h0"])
+    B.gdr_lin_bwd(prob, d, dO, dht, ws, again)
+    ws.fill_(255)
+    B.gdr_lin_fwd(prob, d, ws, bare["o"])
+    B.gdr_lin_bwd(prob, d, dO, dht, ws, bare)
+    torch.cuda.synchronize()
+    for m in ("dq", "dk", "dv", "dh0"):
+        assert torch.equal(full[m], again[m]), m
+    for m, x in bare.items():
+        R.check(m, x, *ref[m])
+        assert dtype == "bf16" or torch.equal(full[m], x), m
+
+
 def test_no_tokens():
     t, _, dht = make(1, [0, 0], 2, 2, 64, "f32")
     for packed in (True, False):
