@@ -516,7 +516,8 @@ __global__ __launch_bounds__(D * 4, 2) void k_lin_out(const LinParams p, const L
   else if (o.first) S.load(o.first + sh * (D * D), o.transposed, slab);
   else S.zero();
   // The wave's tiles of pairs: tokens i of tile w % TI, tokens j of w / TI and every JSTEP-th
-  // on, and the decay between them
+  // on, and the decay between them.  No two tokens are as far apart as the segment is long: a
+  // growth may leave fp32 there, and times the zeros behind a block's end would be a NaN.
   const int it0 = w % TI, jt0 = w / TI, gap0 = 16 * (it0 - jt0) + q - 4 * g;
   float near[NPAIR][4];
 #pragma unroll
@@ -524,7 +525,7 @@ __global__ __launch_bounds__(D * 4, 2) void k_lin_out(const LinParams p, const L
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int d = gap0 - (16 * a * JSTEP + r), n = REV ? -d : d;
-      near[a][r] = n >= 0 ? o.pair * fast_exp2(float(n) * l2) : 0.f;
+      near[a][r] = n >= 0 && n < sg.len ? o.pair * fast_exp2(float(n) * l2) : 0.f;
     }
   // the pairs of later tokens are never written again
   for (int i = threadIdx.x; i < PB / 16; i += NW * 64) {

@@ -364,8 +364,8 @@ gdr_status gdr_norm_bwd(const gdr_norm_shape* shape, const void* r, const float*
  * B, T, H, N, cu_seqlens_host, dtype, scale, Hk, the tensors' layouts and the
  * states [N,H,D,D] (row v, column k) as in gdr_shape; D is 64 or 128.  log_decay:
  * [H] fp32 on the device, meant to be <= 0; -inf keeps nothing of the state.  A
- * positive one is taken as it stands as long as e^(lambda n) stays in the fp32
- * range for every n up to the longest sequence.
+ * positive one is taken as it stands as long as e^(lambda n) and scale e^(lambda n)
+ * stay in the fp32 range for every n up to the longest sequence.
  * States, products and sums are fp32.  With bf16 tensors the products of pairs of
  * tokens and the states are rounded to bf16 once where they are multiplied with
  * bf16 tensors; the states themselves are not: what a block adds to one keeps 16 bits
