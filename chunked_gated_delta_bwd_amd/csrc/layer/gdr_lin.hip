@@ -186,6 +186,11 @@ __device__ __forceinline__ Decay decay_of(float l2, int n) {
   const bool slow = x > -1.f;
   return {slow ? expm1f(x * 0.6931471805599453f) : exp2f(x), slow ? ~0u : 0u};
 }
+// of one token; rounded to fp32, a decay of 1 - 1e-6 would be one of 1 - 1.013e-6
+__device__ __forceinline__ Decay decay_of(float lambda) {
+  const bool slow = lambda > -0.6931472f;
+  return {slow ? expm1f(lambda) : expf(lambda), slow ? ~0u : 0u};
+}
 
 // Copies blocks of a tensor to LDS, by the D / 16 waves of a workgroup.  A lane's row and place
 // in a load of 1 KB, and the piece that belongs there, are the same in each of its loads.
@@ -742,7 +747,7 @@ __global__ __launch_bounds__(256) void k_lin_step(const LinStepParams p) {
   load_row<T, D>(p.q, (int64_t(n) * p.Hk + h / p.G) * D, j, q);
   load_row<T, D>(p.k, (int64_t(n) * p.Hk + h / p.G) * D, j, k);
   float v = IO<T>::load1(p.v, (int64_t(n) * p.H + h) * D + row);
-  const float a = expf(p.log_decay[h]);
+  const Decay a = decay_of(p.log_decay[h]);
   // the slot is another row's if an earlier one names it, and takes the later ones that do along
   bool later = false;
   if (p.slots) {
@@ -759,7 +764,7 @@ __global__ __launch_bounds__(256) void k_lin_step(const LinStepParams p) {
     float o = 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      S[e] = fmaf(v, k[e], a * S[e]);
+      S[e] = fmaf(v, k[e], a(S[e]));
       o = fmaf(S[e], q[e], o);
     }
     o = group_sum_dpp<8>(o);
