@@ -3,8 +3,11 @@
 //   c[m][n] = sum_g sa[m][g] sb[n][g] sum_{k in g} a[m][k] b[n][k]
 // The inner sum over a group's 128 elements is matrix instructions alone (one 16x16x128 of
 // e4m3, or four 16x16x32 of bf16 where c is fp32), started from zero; what they leave is
-// scaled and added in fp32, so that the scales may be any numbers.  b's rows are the
-// instruction's rows and a's its columns: a lane then holds sums of one row of a, whose scale
+// scaled and added in fp32, so that the scales need not be powers of two.  One product,
+// sa sb, scales all 128 elements' sum: the two one after the other would double what the
+// VALU does beside the matrix instructions (41 % of the cycles of large products).  Both
+// scales may be as large or small as fp32 has them, as long as sa sb is a normal number.
+// b's rows are the instruction's rows and a's its columns: a lane then holds sums of one row of a, whose scale
 // is one register, and b's scale is the same for all of them where it belongs to a block of
 // 128 rows.
 //
