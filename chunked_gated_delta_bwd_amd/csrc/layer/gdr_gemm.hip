@@ -11,12 +11,14 @@
 // is one register, and b's scale is the same for all of them where it belongs to a block of
 // 128 rows.
 //
-// Large products are bound by the matrix instructions at the clock that the card's power
-// allows (32768 x 4096 x 4096: 514 to 550 us = 2,000 to 2,140 TFLOP/s; its instructions
-// alone, fed from registers, 365 to 380), ordinary ones by how far tiles fill 256 compute
+// Large products are bound by matrix instructions and scaling in turn: the first take 55 % of
+// the cycles and the VALU 41 %, hardly any of them together (32768 x 4096 x 4096: 485 to 550
+// us by card = 2,000 to 2,270 TFLOP/s; its instructions alone, fed from registers, 365 to
+// 380), ordinary ones by how far tiles fill 256 compute
 // units and LDS feeds them (1000 x 2050 x 4100, fp32: 44 us; 2048 cubed, bf16: 15.3), small
 // ones by latency (64 x 4096 x 4096: 12.8 us, of which the kernel 9.7; one row, 4096 x 2048:
-// 6.8, of which the kernel 3.8).
+// 6.8, of which the kernel 3.8).  One form spills, 6 registers: fp32 results, 128 x 128, block
+// 1, rows through registers.
 #include <hip/hip_runtime.h>
 
 #include "../gdr_device.h"

@@ -54,11 +54,12 @@ gdr_status check_lin_shape(const gdr_lin_shape* s) {
 }
 
 // Tokens per segment: whole blocks, as many as a model of the time finds best.  In units of a
-// block's turn in one of the four output kernels (2.7 us): segments run one to a compute unit,
-// split ones' own states cost a quarter more, and the states between them 3 and another 3 for
-// each 256.  Segments of one length take whole rounds of the compute units; of a pack's, which
-// are not, half a segment is lost at the end.  Measured, forward and backward together, heads
-// of 128, in us for segments of
+// block's turn in one of the four output kernels (4.2 to 4.8 us at T = 32768, 16 heads of 128,
+// bf16, with every compute unit at work): segments run one to a compute unit, split ones' own
+// states cost a quarter more, and the states between them 3 and another 3 for each 256.
+// Segments of one length take whole rounds of the compute units; of a pack's, which are not,
+// half a segment is lost at the end.  Measured, forward and backward together, heads of 128,
+// bf16, in us for segments of
 //                          1 block     2     4     8    16    32
 //   T = 512, 4 heads            51      61    87    90 (no split)
 //   T = 2048, 4 heads           64      69    93   145
@@ -69,6 +70,11 @@ gdr_status check_lin_shape(const gdr_lin_shape* s) {
 //   4 x 4095, 32 heads                                    675   667
 // and, heads of 64, T = 8192, 8 heads: 85 for 2, 74 for 4, 90 for 8; 12 uneven sequences, 32
 // heads: 1830 for 66, 1681 for 33, 1661 for 22.
+// Neither the type nor D is in the model.  fp32, heads of 128, us: T = 16384, 16 heads, 916 for
+// 16 (the model's), 966 for 8; T = 4096, 16 heads, 274 for 4 (the model's), 324 for 2; 4 x 4095,
+// 32 heads, 1758 for 32 (the model's), 1811 for 16.  Off the best: fp32, T = 2048, 4 heads, 123
+// for 2 (the model's), 92 for 1; 32 heads of 64, T = 16384, 348 for 32 (the model's), 324 for 16,
+// and fp32 680 and 601.
 int64_t segment_of(const gdr_lin_shape* s) {
   constexpr int64_t kUnits = 256;
   int64_t blocks = 0, longest = 0;

@@ -19,12 +19,17 @@
 // T = 32768, 16 heads of 128, bf16 (a tensor is 134 MB): k_lin_local 70 to 85 us (two
 // tensors: 55 at the rate of a large copy), k_lin_carry 8, k_lin_out 133 to 155 for one
 // output (four tensors: 110) and 253 to 305 for the gradients of k and v together (220, or
-// 165 with what both read counted once).  Neither HBM nor any unit is full: matrix cores
-// 24 %, VALU 33 %, LDS 29 % of the cycles; what a turn waits for is the chain from LDS
-// through the products to the next, with two waves a SIMD, which the state's registers and
-// the two blocks in LDS (114 KB) allow.  Measured slower: four waves of 32 columns, and two
-// workgroups of half the registers a compute unit.  k_lin_step: 250 rows, 32 heads of 128
-// (1.02 GB of states read and written): 189 us, 5.4 TB/s.
+// 165 with what both read counted once).  Forward and backward move 2.55 GB in 655 us, 3.9
+// TB/s or 80 % of a large copy's rate, where 1.48 GB would do with q, k and v read by both
+// calls: k_lin_local reads k and v, and q and dO, once more (0.5), and the launch of dq reads
+// v, k and dO apart from that of dk and dv (0.42).  That is the larger part of the distance to
+// the floor; the rest is the chain of a turn, from LDS through the products to the next, with
+// two waves a SIMD, which the state's registers and the two blocks in LDS (114 KB) allow
+// (matrix cores 24 %, VALU 33 %, LDS 29 % of the cycles).  k_lin_out<bf16, 128> uses all 256
+// vector registers; backwards it spills 8 of them and 25 scalar ones (into vector registers),
+// forwards 19 scalar ones, with heads of 64 31 and 27; fp32 spills none.  Measured slower: four
+// waves of 32 columns, and two workgroups of half the registers a compute unit.  k_lin_step:
+// 250 rows, 32 heads of 128 (1.02 GB of states read and written): 186 to 190 us, 5.4 TB/s.
 #include <hip/hip_runtime.h>
 
 #include "../gdr_device.h"
